@@ -2,7 +2,9 @@
 
 Argument marshalling only: every function forwards device pointers (taken
 from torch tensors with ``.data_ptr()``) and the current HIP stream to the C
-ABI declared in include/moe.h, and raises MoEError on a non-OK status.  All
+ABI declared in include/moe.h, and raises MoEError on a non-OK status.  The
+microscaled 4-bit and balance-loss calls check their tensors' types, sizes and
+device as well.  All
 computation happens in the library's HIP kernels; there is no fallback.
 """
 from __future__ import annotations
@@ -18,11 +20,18 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED_SH
 
 # Kernel ids of moe_profile_read.
 (K_LOGITS, K_TOPK, K_META, K_GATEUP_GEMM, K_DOWN_GEMM, K_GATEUP_GEMV, K_DOWN_GEMV, K_COMBINE, K_DEQUANT,
- K_PROBE_READ, K_PROBE_MFMA) = range(11)
+ K_PROBE_READ, K_PROBE_MFMA, K_MX4_QUANTIZE, K_MX4_DEQUANTIZE,
+ K_MX4_EXPERTS, K_BALANCE, K_BALANCE_GRAD) = range(16)
 KERNEL_NAMES = {K_LOGITS: "k_screen|k_logits_small", K_TOPK: "k_route_exact", K_META: "k_meta|k_topk_meta",
                 K_GATEUP_GEMM: "k_gateup_gemm", K_DOWN_GEMM: "k_down_gemm",
                 K_GATEUP_GEMV: "k_gemv_experts", K_DOWN_GEMV: "k_gemv_reduce", K_COMBINE: "k_combine",
-                K_DEQUANT: "k_dequant_active", K_PROBE_READ: "k_stream_read", K_PROBE_MFMA: "k_mfma_rate"}
+                K_DEQUANT: "k_dequant_active", K_PROBE_READ: "k_stream_read", K_PROBE_MFMA: "k_mfma_rate",
+                K_MX4_QUANTIZE: "k_mx4_quantize", K_MX4_DEQUANTIZE: "k_mx4_dequantize",
+                K_MX4_EXPERTS: "k_mx4_few",
+                K_BALANCE: "k_balance_rows|k_balance_sum", K_BALANCE_GRAD: "k_balance_grad"}
+
+# Element types of the microscaled 4-bit and balance-loss calls.
+MOE_F32, MOE_BF16, MOE_MX4 = range(3)
 
 
 class MoEError(RuntimeError):
@@ -35,6 +44,10 @@ class LayerDesc(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("hidden", "n_experts", "top_k", "inter", "shared_inter",
                                          "group_size", "gemv_max_rows", "max_chunk", "tile_rows",
                                          "host_sync_routing", "dequant_pass", "batch_invariant")]
+
+
+class Mx4Desc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_experts", "n", "k", "x_type", "y_type", "swiglu")]
 
 
 class QMatrix(C.Structure):
@@ -83,7 +96,16 @@ def lib():
         L.moe_profile_enable.argtypes = [i32]
         L.moe_profile_reset.argtypes = []
         L.moe_profile_read.argtypes = [i32, P(C.c_double), P(i32)]
-        for name in ("moe_packed_bytes", "moe_workspace_bytes", "moe_max_tiles", "moe_pack_weights",
+        i64 = C.c_int64
+        L.moe_mx4_quantize.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp]
+        L.moe_mx4_dequantize.argtypes = [vp, vp, i64, i64, vp, i32, i64, vp]
+        L.moe_mx4_experts.argtypes = [P(Mx4Desc), vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, i32, vp]
+        f32 = C.c_float
+        L.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, P(sz)]
+        L.moe_balance_loss_forward.argtypes = [vp, i32, i32, i32, vp, i32, vp, f32, f32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_loss_backward.argtypes = [vp, i32, i32, i32, i32, vp, f32, f32, vp, vp, vp, vp, vp]
+        for name in ("moe_balance_loss_workspace_bytes", "moe_balance_loss_forward", "moe_balance_loss_backward",
+                     "moe_mx4_experts", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_packed_bytes", "moe_workspace_bytes", "moe_max_tiles", "moe_pack_weights",
                      "moe_route", "moe_forward_prefill", "moe_forward_decode", "moe_forward_decode_static",
                      "moe_probe_stream_read", "moe_probe_mfma_rate", "moe_profile_enable",
                      "moe_profile_reset", "moe_profile_read"):
@@ -106,6 +128,164 @@ def _stream(stream):
         return stream
     import torch
     return torch.cuda.current_stream().cuda_stream
+
+
+# The calls from here to moe_profile_enable take torch tensors whose shapes and
+# types they check, so that a pointer never stands for less memory than the
+# kernel takes it for.  Their work goes to the tensors' device.
+
+def _bad(message, status=1):
+    raise MoEError(status, message)
+
+
+def _value_type(t, name):
+    import torch
+    if t.dtype is torch.bfloat16:
+        return MOE_BF16
+    return MOE_F32 if t.dtype is torch.float32 else _bad(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+
+
+def _arg(t, name, dtype, numel, device):
+    """A contiguous tensor of this type, size and device."""
+    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.device != device:
+        _bad(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device} "
+             f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device})")
+
+
+def _on_device(device, stream, call, *args):
+    """call(*args, stream) with the tensors' device current; stream None is that device's current one."""
+    import torch
+    if device.type != "cuda":
+        _bad(f"tensors must be on a GPU (got {device})")
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+        return
+    with torch.cuda.device(device):
+        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+
+
+def _mx4_rows(v, name, codes, scales):
+    import torch
+    if v.dim() != 2 or v.stride(1) != 1 and v.shape[1] > 1 or v.shape[0] > 1 and v.stride(0) < v.shape[1]:
+        _bad(f"{name} must be 2-D with rows of consecutive values (got {tuple(v.shape)}, strides {v.stride()})")
+    rows, cols = v.shape
+    if cols == 0 or cols % 32:
+        _bad(f"cols must be a positive multiple of 32 (got {cols})", 2)
+    _arg(codes, "codes", torch.uint8, rows * cols // 2, v.device)
+    _arg(scales, "scales", torch.uint8, rows * cols // 32, v.device)
+    return rows, cols, v.stride(0) if rows > 1 else cols
+
+
+def moe_mx4_quantize(x, codes, scales, stream=None):
+    """x [rows, cols] float32 or bfloat16 -> codes [rows, cols/2], scales [rows, cols/32] (uint8)."""
+    rows, cols, ld = _mx4_rows(x, "x", codes, scales)
+    _on_device(x.device, stream, lib().moe_mx4_quantize, x.data_ptr(), _value_type(x, "x"), rows, cols, ld,
+               codes.data_ptr(), scales.data_ptr())
+
+
+def moe_mx4_dequantize(codes, scales, y, stream=None):
+    """codes, scales as moe_mx4_quantize writes them -> y [rows, cols] float32 or bfloat16."""
+    rows, cols, ld = _mx4_rows(y, "y", codes, scales)
+    _on_device(y.device, stream, lib().moe_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, cols,
+               y.data_ptr(), _value_type(y, "y"), ld)
+
+
+def make_mx4_desc(n_experts, n, k, x_type, y_type, swiglu=0) -> Mx4Desc:
+    return Mx4Desc(n_experts, n, k, x_type, y_type, swiglu)
+
+
+def _row_count(t, name, kind, cols, scales, device):
+    """Rows of a 2-D operand of type `kind` with `cols` values a row, its tensors checked."""
+    import torch
+    dtype = (torch.float32, torch.bfloat16, torch.uint8)[kind]
+    width = cols // 2 if kind == MOE_MX4 else cols
+    if t.dim() != 2 or t.shape[1] != width:
+        _bad(f"{name} must be 2-D with {width} columns (got {tuple(t.shape)})")
+    rows = t.shape[0]
+    _arg(t, name, dtype, rows * width, device)
+    if kind == MOE_MX4:
+        if scales is None:
+            _bad(f"{name}_scales is missing")
+        _arg(scales, name + "_scales", torch.uint8, rows * (cols // 32), device)
+    elif scales is not None:
+        _bad(f"{name}_scales goes with a MOE_MX4 {name} only")
+    return rows
+
+
+def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, y, y_scales=None, src_rows=None,
+                    src_div=1, dst_rows=None, row_scale=None, stream=None):
+    """Position i of expert e's range gives y[dst_rows[i]] = row_scale * W_e x[src_rows[i] // src_div]."""
+    import torch
+    dev, E, n, k = x.device, desc.n_experts, desc.n, desc.k
+    if desc.x_type not in (MOE_BF16, MOE_MX4) or desc.y_type not in (MOE_F32, MOE_BF16, MOE_MX4):
+        _bad(f"x_type must be MOE_BF16 or MOE_MX4, y_type one of the three types (got {desc.x_type}, {desc.y_type})")
+    if k <= 0 or k % 32:
+        _bad(f"k must be a positive multiple of 32 (got {k})", 2)
+    _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev)
+    _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev)
+    _arg(expert_offsets, "expert_offsets", torch.int32, E + 1, dev)
+    x_rows = _row_count(x, "x", desc.x_type, k, x_scales, dev)
+    y_rows = _row_count(y, "y", desc.y_type, n // 2 if desc.swiglu else n, y_scales, dev)
+    for t, name in ((src_rows, "src_rows"), (dst_rows, "dst_rows")):
+        if t is not None:
+            _arg(t, name, torch.int32, rows, dev)
+    if row_scale is not None:
+        _arg(row_scale, "row_scale", torch.float32, y_rows, dev)
+    _on_device(dev, stream, lib().moe_mx4_experts, C.byref(desc), w_codes.data_ptr(), w_scales.data_ptr(),
+               x.data_ptr(), _ptr(x_scales), x_rows, expert_offsets.data_ptr(), rows, _ptr(src_rows), src_div,
+               _ptr(dst_rows), _ptr(row_scale), y.data_ptr(), _ptr(y_scales), y_rows)
+
+
+def moe_balance_loss_workspace_bytes(T: int, n_experts: int) -> int:
+    n = C.c_size_t()
+    _check(lib().moe_balance_loss_workspace_bytes(T, n_experts, C.byref(n)))
+    return n.value
+
+
+def _logits(logits, valid):
+    import torch
+    if logits.dim() != 2 or not logits.is_contiguous():
+        _bad(f"logits must be 2-D and contiguous (got {tuple(logits.shape)}, strides {logits.stride()})")
+    if valid is not None:
+        dtype = torch.bool if valid.dtype is torch.bool else torch.uint8
+        _arg(valid, "valid", dtype, logits.shape[0], logits.device)
+    return (*logits.shape, _value_type(logits, "logits"))
+
+
+def moe_balance_loss_forward(logits, topk_ids, valid, balance_coef, z_coef, losses, counts, mean_prob, n_valid, ws,
+                             stream=None):
+    """logits [T, E], topk_ids [T, k] int32, valid [T] uint8/bool or None -> losses [3] (loss, balance, z),
+    counts [E] int32, mean_prob [E], n_valid [1] int32."""
+    import torch
+    T, E, kind = _logits(logits, valid)
+    dev = logits.device
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        _bad(f"topk_ids must be [T, k] (got {tuple(topk_ids.shape)} for T = {T})")
+    k = topk_ids.shape[1]
+    _arg(topk_ids, "topk_ids", torch.int32, T * k, dev)
+    _arg(losses, "losses", torch.float32, 3, dev)
+    _arg(counts, "counts", torch.int32, E, dev)
+    _arg(mean_prob, "mean_prob", torch.float32, E, dev)
+    _arg(n_valid, "n_valid", torch.int32, 1, dev)
+    _arg(ws, "ws", torch.uint8, ws.numel(), dev)
+    _on_device(dev, stream, lib().moe_balance_loss_forward, logits.data_ptr(), kind, T, E, topk_ids.data_ptr(), k,
+               _ptr(valid), balance_coef, z_coef, losses.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(),
+               n_valid.data_ptr(), ws.data_ptr(), ws.numel())
+
+
+def moe_balance_loss_backward(logits, top_k, valid, balance_coef, z_coef, counts, n_valid, grad_loss, dlogits,
+                              stream=None):
+    """Gradient of moe_balance_loss_forward's loss; grad_loss [1] float32 or None (1)."""
+    import torch
+    T, E, kind = _logits(logits, valid)
+    dev = logits.device
+    _arg(counts, "counts", torch.int32, E, dev)
+    _arg(n_valid, "n_valid", torch.int32, 1, dev)
+    if grad_loss is not None:
+        _arg(grad_loss, "grad_loss", torch.float32, 1, dev)
+    _arg(dlogits, "dlogits", logits.dtype, T * E, dev)
+    _on_device(dev, stream, lib().moe_balance_loss_backward, logits.data_ptr(), kind, T, E, top_k, _ptr(valid),
+               balance_coef, z_coef, counts.data_ptr(), n_valid.data_ptr(), _ptr(grad_loss), dlogits.data_ptr())
 
 
 def make_desc(hidden, n_experts, top_k, inter, shared_inter, gemv_max_rows=-1, max_chunk=2048,

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = ["pack.hip", "route.hip", "gemm.hip", "gemv.hip", "probe.hip", "api.cpp"]
+SOURCES = ["pack.hip", "route.hip", "gemm.hip", "gemv.hip", "probe.hip", "mx4.hip", "mx4_experts.hip", "balance.hip",
+           "api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -194,7 +194,7 @@ int max_long_tiles(const moe_layer_desc* d) {
 }
 
 // ---- kernel timing (measurement mode) ----------------------------------------
-constexpr int kNumKernels = 11;
+constexpr int kNumKernels = 16;
 struct Pending {
   int kid;
   hipEvent_t a, b;
@@ -744,6 +744,196 @@ moe_status moe_forward_decode_static(const moe_layer_desc* desc, const void* pac
   TRY(static_scratch(&ws));
   TRY(forward_checks(desc, packed, router_w, x, T, y, ws, kStaticScratchBytes));
   return decode_impl(desc, packed, router_w, logit_bias, x, T, y, ws, kStaticScratchBytes, false, stream);
+}
+
+// The checks that both directions of the 4-bit storage share; `rows` = 0 needs no pointers.
+static moe_status mx4_row_args(const void* wide, int32_t type, int64_t rows, int64_t cols, int64_t ld,
+                               const uint8_t* codes, const uint8_t* scales, Mx4RowArgs* A) {
+  if (type != MOE_F32 && type != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the values must be MOE_F32 or MOE_BF16 (got type %d)", type);
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be >= 0 (got %lld)", (long long)rows);
+  if (cols <= 0 || cols % 32 || cols > (int64_t)1 << 24)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "cols must be a positive multiple of 32 <= 2^24 (got %lld)", (long long)cols);
+  if (rows > ((int64_t)1 << 46) / cols)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "%lld rows of %lld values are too many", (long long)rows, (long long)cols);
+  if (ld < cols || ld > (int64_t)1 << 40)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the row stride (%lld) is less than cols (%lld), or over 2^40", (long long)ld,
+                (long long)cols);
+  if (rows && (!wide || !codes || !scales)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (reinterpret_cast<uintptr_t>(codes) & 15)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(wide) & (type == MOE_F32 ? 3 : 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the values are not aligned to their type");
+  *A = Mx4RowArgs{const_cast<void*>(wide), const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales), rows, cols, ld,
+                  type == MOE_F32};
+  return MOE_OK;
+}
+
+moe_status moe_mx4_quantize(const void* x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx, uint8_t* codes,
+                            uint8_t* scales, void* stream) {
+  Mx4RowArgs A;
+  TRY(mx4_row_args(x, x_type, rows, cols, ldx, codes, scales, &A));
+  if (rows == 0) return MOE_OK;
+  TRY(check_device());
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(11, s, "4-bit quantisation", [&](const KTime& kt) { return launch_mx4_quantize(A, s, kt); });
+}
+
+moe_status moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols, void* y,
+                              int32_t y_type, int64_t ldy, void* stream) {
+  Mx4RowArgs A;
+  TRY(mx4_row_args(y, y_type, rows, cols, ldy, codes, scales, &A));
+  if (rows == 0) return MOE_OK;
+  TRY(check_device());
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(12, s, "4-bit read-back", [&](const KTime& kt) { return launch_mx4_dequantize(A, s, kt); });
+}
+
+moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const uint8_t* w_scales, const void* x,
+                           const uint8_t* x_scales, int32_t x_rows, const int32_t* expert_offsets, int32_t rows,
+                           const int32_t* src_rows, int32_t src_div, const int32_t* dst_rows, const float* row_scale,
+                           void* y, uint8_t* y_scales, int32_t y_rows, void* stream) {
+  if (!d) return fail(MOE_ERR_INVALID_ARGUMENT, "desc is null");
+  if (d->n_experts < 1 || d->n_experts > 512)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_experts must be in 1..512 (got %d)", d->n_experts);
+  if (d->k <= 0 || d->k % 32 || d->k > 65536)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "k must be a positive multiple of 32 <= 65536 (got %d)", d->k);
+  if (d->n <= 0 || d->n > 65536) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n must be in 1..65536 (got %d)", d->n);
+  if (d->x_type != MOE_BF16 && d->x_type != MOE_MX4)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "x_type must be MOE_BF16 or MOE_MX4 (got %d)", d->x_type);
+  if (d->y_type < MOE_F32 || d->y_type > MOE_MX4)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y_type must be MOE_F32, MOE_BF16 or MOE_MX4 (got %d)", d->y_type);
+  if (d->swiglu != 0 && d->swiglu != 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "swiglu must be 0 or 1 (got %d)", d->swiglu);
+  if (d->swiglu && d->n % 2) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n must be even with swiglu (got %d)", d->n);
+  const int n_out = d->swiglu ? d->n / 2 : d->n;
+  if (d->y_type == MOE_MX4 && n_out % 32)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "a MOE_MX4 y needs a multiple of 32 columns (got %d)", n_out);
+  if (rows < 0 || rows > 1 << 24) return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be in 0..2^24 (got %d)", rows);
+  if (rows == 0) return MOE_OK;
+  if (x_rows < 1 || y_rows < 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "x_rows and y_rows must be positive (got %d, %d)", x_rows, y_rows);
+  if (src_div < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "src_div must be positive (got %d)", src_div);
+  if (!w_codes || !w_scales || !x || !expert_offsets || !y || (d->x_type == MOE_MX4 && !x_scales) ||
+      (d->y_type == MOE_MX4 && !y_scales))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (!src_rows && rows > x_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "without src_rows x needs a row per position (%d < %d)", x_rows, rows);
+  if (!dst_rows && rows > y_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "without dst_rows y needs a row per position (%d < %d)", y_rows, rows);
+  if ((reinterpret_cast<uintptr_t>(w_codes) | reinterpret_cast<uintptr_t>(x)) & 15)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "w_codes and x must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(y) & (d->y_type == MOE_MX4 ? 15 : d->y_type == MOE_F32 ? 3 : 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y must be aligned to its type, codes to 16 bytes");
+  TRY(check_device());
+  Mx4ExpertArgs A{w_codes,   w_scales, x,        x_scales,  expert_offsets, src_rows, dst_rows,
+                  row_scale, y,        y_scales, d->n_experts, d->n,        d->k,     rows,
+                  x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, s, kt); });
+}
+
+static moe_status balance_shape(int32_t T, int32_t E, int32_t k) {
+  if (T < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %d)", T);
+  if (E < 1 || E > 512) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_experts must be in 1..512 (got %d)", E);
+  if (k < 1 || k > 16) return fail(MOE_ERR_INVALID_ARGUMENT, "top_k must be in 1..16 (got %d)", k);
+  if ((int64_t)T * k > 0x7FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T * top_k must be below 2^31 (got %d * %d)", T, k);
+  return MOE_OK;
+}
+
+static moe_status balance_logits(const void* logits, int32_t type) {
+  if (type != MOE_F32 && type != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the logits must be MOE_F32 or MOE_BF16 (got type %d)", type);
+  if (reinterpret_cast<uintptr_t>(logits) & (type == MOE_F32 ? 3 : 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "the logits are not aligned to their type");
+  return MOE_OK;
+}
+
+// Carves the forward pass's workspace (base may be null for its size alone).
+static size_t balance_ws(int32_t T, int32_t E, void* base, BalanceArgs* A) {
+  const int64_t parts = balance_parts(T, E);
+  size_t o = 0;
+  const size_t done = o; o += al(4);
+  const size_t dots = o; o += al((E + 15) / 16 * 8);
+  const size_t pz = o; o += al(parts * 8);
+  const size_t pn = o; o += al(parts * 4);
+  const size_t pc = o; o += al(parts * E * 4);
+  const size_t pp = o; o += al(parts * E * 4);
+  if (A) {
+    A->done = at<int32_t>(base, done);
+    A->dots = at<double>(base, dots);
+    A->part_z = at<double>(base, pz);
+    A->part_n = at<int32_t>(base, pn);
+    A->part_count = at<int32_t>(base, pc);
+    A->part_p = at<float>(base, pp);
+  }
+  return o;
+}
+
+moe_status moe_balance_loss_workspace_bytes(int32_t T, int32_t n_experts, size_t* bytes) {
+  TRY(balance_shape(T, n_experts, 1));
+  if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+  *bytes = balance_ws(T, n_experts, nullptr, nullptr);
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss_forward(const void* logits, int32_t logits_type, int32_t T, int32_t n_experts,
+                                    const int32_t* topk_ids, int32_t top_k, const uint8_t* valid, float balance_coef,
+                                    float z_coef, float* losses, int32_t* counts, float* mean_prob, int32_t* n_valid,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  TRY(balance_shape(T, n_experts, top_k));
+  TRY(balance_logits(logits, logits_type));
+  if (!losses || !counts || !mean_prob || !n_valid || !ws || (T > 0 && (!logits || !topk_ids)))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  BalanceArgs A{};
+  const size_t need = balance_ws(T, n_experts, ws, &A);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < required %zu", ws_bytes, need);
+  if (reinterpret_cast<uintptr_t>(ws) & 7) return fail(MOE_ERR_INVALID_ARGUMENT, "ws must be 8-byte aligned");
+  TRY(check_device());
+  A.logits = logits;
+  A.ids = topk_ids;
+  A.valid = valid;
+  A.T = T;
+  A.E = n_experts;
+  A.k = top_k;
+  A.balance_coef = balance_coef;
+  A.z_coef = z_coef;
+  A.f32 = logits_type == MOE_F32;
+  A.losses = losses;
+  A.counts = counts;
+  A.mean_prob = mean_prob;
+  A.n_valid = n_valid;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(14, s, "balance loss", [&](const KTime& kt) { return launch_balance_forward(A, s, kt); });
+}
+
+moe_status moe_balance_loss_backward(const void* logits, int32_t logits_type, int32_t T, int32_t n_experts,
+                                     int32_t top_k, const uint8_t* valid, float balance_coef, float z_coef,
+                                     const int32_t* counts, const int32_t* n_valid, const float* grad_loss,
+                                     void* dlogits, void* stream) {
+  TRY(balance_shape(T, n_experts, top_k));
+  TRY(balance_logits(logits, logits_type));
+  TRY(balance_logits(dlogits, logits_type));
+  if (T == 0) return MOE_OK;
+  if (!logits || !counts || !n_valid || !dlogits) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  TRY(check_device());
+  BalanceArgs A{};
+  A.logits = logits;
+  A.valid = valid;
+  A.T = T;
+  A.E = n_experts;
+  A.k = top_k;
+  A.balance_coef = balance_coef;
+  A.z_coef = z_coef;
+  A.f32 = logits_type == MOE_F32;
+  A.counts = const_cast<int32_t*>(counts);
+  A.n_valid = const_cast<int32_t*>(n_valid);
+  A.grad = grad_loss;
+  A.dlogits = dlogits;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(15, s, "balance loss gradient", [&](const KTime& kt) { return launch_balance_backward(A, s, kt); });
 }
 
 const char* moe_status_str(moe_status s) {

@@ -111,6 +111,64 @@ hipError_t launch_gemv_gateup_bi(const LayerArgs& L, const ChunkArgs& C, const f
 hipError_t launch_gemv_down_bi(const LayerArgs& L, const ChunkArgs& C, const uint16_t* h16, const int32_t* ids,
                                const float* tw, hipStream_t s, const KTime& kt = KTime{});
 
+// Rows of the microscaled 4-bit format (mx4.h) beside their values.
+struct Mx4RowArgs {
+  void* wide;       // [rows] of cols fp32 or bf16 values, ld apart (read by quantize, written by dequantize)
+  uint8_t* codes;   // [rows][cols / 2]
+  uint8_t* scales;  // [rows][cols / 32]
+  int64_t rows, cols, ld;
+  bool f32;
+};
+hipError_t launch_mx4_quantize(const Mx4RowArgs& A, hipStream_t s, const KTime& kt = KTime{});
+hipError_t launch_mx4_dequantize(const Mx4RowArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
+// Grouped product with microscaled 4-bit expert weights (mx4_experts.hip).
+constexpr int kMxTypeF32 = 0, kMxTypeBf16 = 1, kMxTypeMx4 = 2;
+struct Mx4ExpertArgs {
+  const uint8_t* w_codes;    // [E][n][k / 2]
+  const uint8_t* w_scales;   // [E][n][k / 32]
+  const void* x;             // [x_rows][k] bf16, or codes [x_rows][k / 2]
+  const uint8_t* x_scales;   // [x_rows][k / 32] with x_mx4
+  const int32_t* offsets;    // [E + 1]
+  const int32_t* src_rows;   // [P] or null
+  const int32_t* dst_rows;   // [P] or null
+  const float* row_scale;    // [y_rows] or null
+  void* y;                   // [y_rows][n_out] of y_type, n_out = swiglu ? n / 2 : n
+  uint8_t* y_scales;         // [y_rows][n_out / 32] with y_type = kMxTypeMx4
+  int E, n, k, P, x_rows, y_rows, src_div, y_type;
+  bool x_mx4, swiglu;
+};
+hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
+// The router's balance loss (balance.hip).
+constexpr int kBalMaxParts = 512;  // partial rows of the forward pass
+struct BalanceArgs {
+  const void* logits;    // [T][E] fp32 or bf16
+  const int32_t* ids;    // [T][k]
+  const uint8_t* valid;  // [T] or null
+  int T, E, k;
+  float balance_coef, z_coef;
+  bool f32;
+  float* losses;         // [3] loss, balance, z
+  int32_t* counts;       // [E]
+  float* mean_prob;      // [E]
+  int32_t* n_valid;      // [1]
+  // Workspace of the forward pass.
+  int32_t* done;         // [1]
+  double* dots;          // [E / 16, rounded up]
+  double* part_z;        // [kBalMaxParts]
+  int32_t* part_n;       // [kBalMaxParts]
+  int32_t* part_count;   // [kBalMaxParts][E]
+  float* part_p;         // [kBalMaxParts][E]
+  // Backward pass.
+  const float* grad;     // [1] or null
+  void* dlogits;         // [T][E] of the logits' type
+};
+// Partial rows of the forward pass over T tokens (1: no second launch).
+int balance_parts(int T, int E);
+hipError_t launch_balance_forward(const BalanceArgs& A, hipStream_t s, const KTime& kt = KTime{});
+hipError_t launch_balance_backward(const BalanceArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
 // Measurement probes (csrc/probe.hip): a 16-byte-per-lane streaming read of
 // `bytes` with at most max_wgs workgroups (sink: max_wgs words), and the
 // MFMA-only rate kernel over `wgs` workgroups (clocks: 2 * wgs words or null;

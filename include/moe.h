@@ -290,6 +290,142 @@ moe_status moe_forward_decode_static(const moe_layer_desc *desc, const void *pac
                                      const float *router_w, const float *logit_bias,
                                      const uint16_t *x, int32_t T, float *y, void *stream);
 
+/*
+ * Element types of the calls below.  MOE_F32 and MOE_BF16 are plain values;
+ * MOE_MX4 is the microscaled 4-bit format (MXFP4), held in two arrays:
+ *   codes  [rows][cols/2]  uint8, two e2m1 codes per byte, the even column in
+ *                          the low nibble; a code is a sign bit and one of the
+ *                          magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   scales [rows][cols/32] uint8, one per 32 consecutive values of a row: s
+ *                          stands for 2^(s - 127), and 255 for NaN
+ * A value is code * 2^(s - 127); 0.53125 bytes per value.  It is the 4-bit
+ * floating format beside the integer one of moe_pack_weights, and the one that
+ * the matrix units multiply without rebuilding it.
+ */
+enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MX4 = 2 };
+
+/*
+ * Quantise rows to MOE_MX4.  For each block of 32 values with the largest
+ * magnitude amax, the scale is 2^(floor(log2 amax) - 2), not below 2^-127, and
+ * a code is the e2m1 value nearest to x / scale, ties to the one with an even
+ * mantissa bit; magnitudes above 6 scales are held at 6 (amax / scale is below 8).
+ * Exact in every other respect, subnormal inputs included; -0 keeps its sign.
+ * A block of zeros has the scale byte 0.  A block that holds a NaN or an
+ * infinity gets the scale byte 255 and zero codes: it reads back as NaN.
+ *   x      [rows] of cols values of x_type (MOE_F32 or MOE_BF16), the rows
+ *          ldx values apart (ldx >= cols); any alignment of its type, 16-byte
+ *          aligned rows are faster
+ *   cols   a positive multiple of 32, at most 2^24; rows = 0 is a no-op
+ *   codes, scales  as above, contiguous; codes 16-byte aligned
+ */
+moe_status moe_mx4_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
+                            uint8_t *codes, uint8_t *scales, void *stream);
+
+/*
+ * Read MOE_MX4 rows back as values of y_type (MOE_F32 or MOE_BF16), exactly,
+ * but for magnitudes of 2^128 and more (scale bytes 253 and 254 with the large
+ * codes, which moe_mx4_quantize never writes): those become infinity.  y as x
+ * above; the values between cols and ldy stay as they were.
+ */
+moe_status moe_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols,
+                              void *y, int32_t y_type, int64_t ldy, void *stream);
+
+/*
+ * A stack of expert matrices W_e [n][k] in MOE_MX4 and how they are applied.
+ */
+typedef struct {
+    int32_t n_experts; /* E: 1..512; 1 for one dense matrix */
+    int32_t n;         /* rows of a matrix, 1..65536; with swiglu even: the gate rows, then the up rows */
+    int32_t k;         /* columns: a multiple of 32, at most 65536 */
+    int32_t x_type;    /* MOE_BF16 or MOE_MX4 */
+    int32_t y_type;    /* MOE_F32, MOE_BF16, or MOE_MX4 (its columns then a multiple of 32) */
+    int32_t swiglu;    /* 1: y = silu(z[:n/2]) * z[n/2:], n/2 columns; 0: y = z, n columns */
+} moe_mx4_desc;
+
+/*
+ * Grouped product of routed rows with their experts' matrices, the form that
+ * moe_forward_* have inside for the integer format: position i in
+ * [expert_offsets[e], expert_offsets[e+1]) has z = W_e x[src(i)], and
+ * y[dst(i)] = row_scale[dst(i)] * (z, or its SwiGLU).  For any number of rows:
+ * a single token's positions are products with a vector.
+ *   w_codes, w_scales  [E][n][k/2] and [E][n][k/32]: moe_mx4_quantize of E * n
+ *                      rows of k values
+ *   x, x_scales        [x_rows] rows of k values of x_type (x_scales NULL for
+ *                      MOE_BF16)
+ *   expert_offsets     [E+1] int32, increasing from 0 to the number of
+ *                      positions, as moe_route writes them
+ *   rows               the positions' upper bound on the host: expert_offsets[E]
+ *                      is at most rows (offsets are held inside [0, rows])
+ *   src_rows, src_div  src(i) = src_rows[i] / src_div, or i where src_rows is
+ *                      NULL; moe_route's sorted_assign with src_div = k gives
+ *                      each assignment its token's row
+ *   dst_rows           dst(i) = dst_rows[i], or i where NULL; each row at most
+ *                      once; sorted_assign gives each assignment its own row
+ *   row_scale          [y_rows] float or NULL: a factor for each row of y
+ *                      (moe_route's topk_weights beside dst_rows = sorted_assign)
+ *   y, y_scales        [y_rows] rows of n (with swiglu n/2) values of y_type
+ *                      (y_scales NULL but for MOE_MX4)
+ * w_codes, x and a MOE_MX4 y are 16-byte aligned, another y to its type.  A src(i) outside x reads as a row of
+ * zeros and a dst(i) outside y is not written.  Rows of y that no position
+ * maps to, those of positions behind expert_offsets[E] among them, stay as
+ * they were.  y must not overlap an input.
+ * Products are summed in fp32 (bf16 x with the weights' exact bf16 values;
+ * MOE_MX4 x in the scaled matrix instructions), SwiGLU and row_scale are
+ * applied in fp32, and the result is rounded once to y_type, for MOE_MX4 as
+ * moe_mx4_quantize does.  Repeated calls give identical bits.  No workspace.
+ * rows = 0 is a no-op.
+ */
+moe_status moe_mx4_experts(const moe_mx4_desc *desc, const uint8_t *w_codes, const uint8_t *w_scales,
+                           const void *x, const uint8_t *x_scales, int32_t x_rows,
+                           const int32_t *expert_offsets, int32_t rows, const int32_t *src_rows,
+                           int32_t src_div, const int32_t *dst_rows, const float *row_scale, void *y,
+                           uint8_t *y_scales, int32_t y_rows, void *stream);
+
+/*
+ * The router's balance loss for training, with the per-expert counts.  With
+ * p_t the softmax of token t's logits over the E = n_experts experts, lse_t
+ * its log-sum-exp, n the valid tokens, counts_e the assignments of valid
+ * tokens to expert e, f_e = counts_e / (n k) and P_e = sum_t p_te / n (sums
+ * over valid tokens):
+ *   balance = E sum_e f_e P_e          (1 where all experts are used alike)
+ *   z       = sum_t lse_t^2 / n
+ *   loss    = balance_coef * balance + z_coef * z
+ *   logits    [T][E] of logits_type (MOE_F32 or MOE_BF16), any alignment of it
+ *   topk_ids  [T][k] int32, moe_route's; an id outside 0..E-1 is counted
+ *             nowhere, one that stands twice in a row counts twice
+ *   valid     [T] uint8, 0 for a padding token, or NULL: all are valid
+ *   losses    [3] float: loss, balance, z
+ *   counts    [E] int32
+ *   mean_prob [E] float: P_e
+ *   n_valid   [1] int32: n
+ *   ws        moe_balance_loss_workspace_bytes(T, E) bytes, 8-byte aligned
+ * Logits are finite or -inf; a row of -inf alone adds nothing to the sums and
+ * has a zero gradient, but counts as a token.  A NaN or +inf in a valid row
+ * makes the loss and that row's gradient NaN.  With no valid token, T = 0
+ * included, the losses, P and counts are 0.  T * top_k < 2^31.
+ * Probabilities are fp32, the sums over tokens fp32 within a workgroup's rows
+ * and float64 beyond; repeated calls give identical bits.  Two calls that
+ * overlap in time need two workspaces, also when replayed from graphs.
+ */
+moe_status moe_balance_loss_workspace_bytes(int32_t T, int32_t n_experts, size_t *bytes);
+moe_status moe_balance_loss_forward(const void *logits, int32_t logits_type, int32_t T, int32_t n_experts,
+                                    const int32_t *topk_ids, int32_t top_k, const uint8_t *valid,
+                                    float balance_coef, float z_coef, float *losses, int32_t *counts,
+                                    float *mean_prob, int32_t *n_valid, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+/*
+ * Gradient of the loss with respect to the logits, times the float at
+ * grad_loss (device; NULL = 1), from what the forward call read and wrote:
+ *   dlogits_te = grad p_te (balance_coef E / n (f_e - sum_j f_j p_tj) + 2 z_coef lse_t / n)
+ * with zeros for padding tokens.  f, made of counts, has no gradient.
+ *   dlogits  [T][E] of logits_type; may be logits itself
+ */
+moe_status moe_balance_loss_backward(const void *logits, int32_t logits_type, int32_t T, int32_t n_experts,
+                                     int32_t top_k, const uint8_t *valid, float balance_coef,
+                                     float z_coef, const int32_t *counts, const int32_t *n_valid,
+                                     const float *grad_loss, void *dlogits, void *stream);
+
 /* Default R* of the library with batch_invariant = 0 (host output); with
  * batch_invariant = 1 the default is 4. */
 int32_t moe_default_gemv_max_rows(void);
@@ -312,7 +448,10 @@ const char *moe_last_error(void);
  *   the decode GEMV path), 3 = gate/up grouped GEMM, 4 = down grouped GEMM,
  *   5 = top-k + gate/up GEMV + split down GEMV (decode GEMV path), 6 = sum of
  *   the decode path's partial outputs, 7 = per-token combine of the
- *   grouped-GEMM path, 8 = separate dequant pass (dequant_pass = 1)
+ *   grouped-GEMM path, 8 = separate dequant pass (dequant_pass = 1), 9 and
+ *   10 = the measurement probes, 11 = moe_mx4_quantize, 12 = moe_mx4_dequantize,
+ *   13 = moe_mx4_experts, 14 = moe_balance_loss_forward,
+ *   15 = moe_balance_loss_backward
  */
 moe_status moe_profile_enable(int32_t mask);
 moe_status moe_profile_reset(void);
