@@ -6,6 +6,8 @@
 //
 // The weights are the matrix instructions' first operand, so that a lane of
 // the result holds one row of x and four consecutive columns of y.
+#include <type_traits>
+
 #include "launch.h"
 #include "mx4.h"
 
@@ -218,11 +220,307 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows an expert, 4-bit x: a workgroup of WN x WT waves takes BN weight
+// rows x BT positions; a wave takes FN x FT blocks of 32 x 32 with the
+// 32x32x64 scaled instruction.  K goes by in tiles of 256 columns (8 blocks,
+// 128 bytes a row) through S stages in LDS, filled by direct loads that stay
+// in flight across the barriers.
+//
+// LDS.  A row's 8 blocks of 16 bytes are stored at slot (block ^ row % 8), so
+// that the 16-byte reads of 8 consecutive rows touch all banks; the direct
+// loads write consecutive lanes to consecutive addresses, so the exchange is
+// made on the memory side, inside the row's 128 bytes.  In step s of a tile a
+// lane of half h multiplies block 4 h + s: its four scale bytes of the tile are
+// then one dword, of which the instruction picks byte s.
+//
+// Ragged: k is no multiple of 256, or the scale arrays are not dword aligned.
+// The scales are then staged a byte a lane, each in a dword of its own, and
+// blocks past the row's end, for which the loads bring the last block again,
+// are multiplied as zeros.
+// ---------------------------------------------------------------------------
+constexpr int kKtBlocks = 8;  // blocks of a K tile
+
+// 16, 4 or 1 bytes a lane from memory to lds + lane * max(size, 4), not waited
+// for: the compiler's own form of this load makes it wait for every load in
+// flight before the next read of LDS.  m0 holds the LDS address; nothing else
+// in these kernels uses it.
+template <int Size>
+__device__ __forceinline__ void load_to_lds(const void* p, uint32_t lds) {
+  static_assert(Size == 16 || Size == 4 || Size == 1, "a direct load's size");
+  if constexpr (Size == 16)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "s"(lds) : "memory");
+  else if constexpr (Size == 4)
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(p), "s"(lds) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_ubyte %0, off" ::"v"(p), "s"(lds) : "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "vmcnt");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+template <int BN, int BT, int WN, int WT, int S, bool Ragged>
+struct MxTileShape {
+  static constexpr int kWaves = WN * WT;
+  static constexpr int kCodeLoads = (BN + BT) / 8 / kWaves;  // of 8 rows each, a wave
+  static constexpr int kScaleRows = Ragged ? 8 : 32;         // rows of a scale load
+  static constexpr int kScaleLoads = ((BN + BT) / kScaleRows + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kCodeLoads + kScaleLoads;
+  static constexpr int kScaleRow = Ragged ? 32 : 8;          // LDS bytes of a row's scales
+  static constexpr int kStage = (BN + BT) * (128 + kScaleRow);
+  static constexpr int kLds = S * kStage + BT * 12;          // and each position's src, dst, factor
+  static_assert((BN + BT) / 8 % kWaves == 0, "code loads divide among the waves");
+  static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
+  static_assert(kLoads * (S - 2) < 64, "vmcnt");
+};
+
+// Values of one 32-column block for the lane's position, in the instruction's
+// result order: element 4 i + j is column 8 i + 4 h + j.
+__device__ __forceinline__ void mx4_store_block(const Mx4ExpertArgs& A, int n_out, int dst, int c0, int h, float v[16]) {
+  if (A.y_type == kMxTypeMx4) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; i++) m = max(m, f32_abs_bits(v[i]));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+    const int s = mx4_scale_byte(m);
+    const float inv = mx4_inv_scale(s);
+    const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
+    if (dst < 0 || c0 >= n_out) return;
+    const int64_t block = (int64_t)dst * (n_out >> 5) + (c0 >> 5);
+    uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes);
+    out[h] = (uint16_t)d0;
+    out[2 + h] = (uint16_t)(d0 >> 16);
+    out[4 + h] = (uint16_t)d1;
+    out[6 + h] = (uint16_t)(d1 >> 16);
+    if (h == 0) A.y_scales[block] = (uint8_t)s;
+    return;
+  }
+  if (dst < 0) return;
+#pragma unroll
+  for (int i = 0; i < 16; i++) {
+    const int c = c0 + 8 * (i >> 2) + 4 * h + (i & 3);
+    if (c >= n_out) continue;
+    const int64_t at = (int64_t)dst * n_out + c;
+    if (A.y_type == kMxTypeF32)
+      static_cast<float*>(A.y)[at] = v[i];
+    else
+      static_cast<uint16_t*>(A.y)[at] = (uint16_t)f32_to_bf16_bits(v[i]);
+  }
+}
+
+template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
+__global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A) {
+  using Sh = MxTileShape<BN, BT, WN, WT, S, Ragged>;
+  constexpr int FN = BN / 32 / WN, FT = BT / 32 / WT, NW = WN * WT;
+  constexpr int kCols = Swiglu ? BN / 2 : BN;  // columns of y
+  static_assert(!Swiglu || FN % 2 == 0, "gate and up blocks go in pairs");
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+  int* s_src = reinterpret_cast<int*>(sm + S * Sh::kStage);
+  int* s_dst = s_src + BT;
+  float* s_fac = reinterpret_cast<float*>(s_dst + BT);
+  const int n_out = Swiglu ? A.n >> 1 : A.n;
+  const int cols = (n_out + kCols - 1) / kCols;
+  const int tile = blockIdx.x / cols, c0 = (blockIdx.x - tile * cols) * kCols;
+  MxTile t;
+  if (!mx4_find_tile<BT>(A.offsets, A.E, A.P, tile, &t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wn = wave % WN, wt = wave / WN;
+  const int r = lane & 31, h = lane >> 5;
+  const int nb = A.k >> 5, nkt = (nb + kKtBlocks - 1) / kKtBlocks;
+
+  for (int q = threadIdx.x; q < BT; q += 64 * NW) {
+    const bool on = q < t.rows;
+    const int dst = on ? mx4_dst(A, t.row + q) : -1;
+    s_src[q] = on ? mx4_src(A, t.row + q) : -1;
+    s_dst[q] = dst;
+    s_fac[q] = A.row_scale && dst >= 0 ? A.row_scale[dst] : 1.f;
+  }
+  __syncthreads();
+
+  // Memory row of tile row q.  With SwiGLU blocks of 32 gate rows and of the
+  // same 32 up rows take turns.  Rows past the last one read the last one, and
+  // positions past the tile, or with no row of x, row 0 (their results are
+  // dropped, or zeroed).
+  auto w_row = [&](int q) -> int64_t {
+    const int c = Swiglu ? c0 + (q >> 6) * 32 + (q & 31) : c0 + q;
+    return (int64_t)t.e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
+  };
+  const uint8_t* code_p[Sh::kCodeLoads];
+  const uint8_t* scale_p[Sh::kScaleLoads];
+#pragma unroll
+  for (int j = 0; j < Sh::kCodeLoads; j++) {
+    const int q = (wave + NW * j) * 8 + (lane >> 3);
+    code_p[j] = (q < BN ? A.w_codes + w_row(q) * nb * kMxBlockBytes
+                        : static_cast<const uint8_t*>(A.x) + (int64_t)max(s_src[q - BN], 0) * nb * kMxBlockBytes);
+  }
+  // Where the scale loads do not divide among the waves, the last ones are made twice.
+  auto scale_load = [&](int j) { return min(wave + NW * j, (BN + BT) / Sh::kScaleRows - 1); };
+#pragma unroll
+  for (int j = 0; j < Sh::kScaleLoads; j++) {
+    const int q = scale_load(j) * Sh::kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
+    scale_p[j] = q < BN ? A.w_scales + w_row(q) * nb : A.x_scales + (int64_t)max(s_src[q - BN], 0) * nb;
+  }
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
+  auto issue = [&](int kt, int stage) {
+    const uint32_t base = lds0 + stage * Sh::kStage;
+    int cb = kt * kKtBlocks + ((lane & 7) ^ (lane >> 3));
+    int so = kt * kKtBlocks + (Ragged ? lane & 7 : (lane & 1) * 4);
+    if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
+#pragma unroll
+    for (int j = 0; j < Sh::kCodeLoads; j++)
+      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+#pragma unroll
+    for (int j = 0; j < Sh::kScaleLoads; j++)
+      load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + (BN + BT) * 128 + scale_load(j) * 256);
+  };
+
+  f32x16_t acc[FN][FT] = {};
+  struct Frags {
+    uint4 w[FN], x[FT];
+    uint32_t ws[FN], xs[FT];
+  };
+  auto compute = [&](int kt, int stage) {
+    const uint8_t* wl = sm + stage * Sh::kStage + (wn * FN * 32 + r) * 128;
+    const uint8_t* xl = sm + stage * Sh::kStage + (BN + wt * FT * 32 + r) * 128;
+    const uint8_t* ss = sm + stage * Sh::kStage + (BN + BT) * 128;
+    const uint8_t* sw = ss + (wn * FN * 32 + r) * Sh::kScaleRow + h * (Sh::kScaleRow / 2);
+    const uint8_t* sx = ss + (BN + wt * FT * 32 + r) * Sh::kScaleRow + h * (Sh::kScaleRow / 2);
+    Frags a, b;
+    auto load = [&](auto sc, Frags& d) {
+      constexpr int s = sc.value;
+      const int slot = ((4 * h + s) ^ (r & 7)) * 16;
+#pragma unroll
+      for (int f = 0; f < FN; f++) d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 128 + slot);
+#pragma unroll
+      for (int f = 0; f < FT; f++) d.x[f] = *reinterpret_cast<const uint4*>(xl + f * 32 * 128 + slot);
+      // The tile's dword of scales is read in step 0; a ragged one's each step.
+      if (Ragged || s == 0) {
+#pragma unroll
+        for (int f = 0; f < FN; f++)
+          d.ws[f] = *reinterpret_cast<const uint32_t*>(sw + f * 32 * Sh::kScaleRow + (Ragged ? s * 4 : 0));
+#pragma unroll
+        for (int f = 0; f < FT; f++)
+          d.xs[f] = *reinterpret_cast<const uint32_t*>(sx + f * 32 * Sh::kScaleRow + (Ragged ? s * 4 : 0));
+      }
+    };
+    auto mul = [&](auto sc, Frags& d, const Frags& sd) {
+      constexpr int s = sc.value;
+      uint32_t ws[FN], xs[FT];
+      const bool in = !Ragged || kt * kKtBlocks + 4 * h + s < nb;
+#pragma unroll
+      for (int f = 0; f < FN; f++) ws[f] = in ? sd.ws[f] : 0x7Fu;
+#pragma unroll
+      for (int f = 0; f < FT; f++) {
+        xs[f] = in ? sd.xs[f] : 0x7Fu;
+        if (!in) d.x[f] = make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < FN; i++)
+#pragma unroll
+        for (int j = 0; j < FT; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(d.w[i]), mx4_operand(d.x[j]), acc[i][j],
+                                                                      kE2m1, kE2m1, Ragged ? 0 : s, ws[i], Ragged ? 0 : s,
+                                                                      xs[j]);
+    };
+    // The next step's operands are read while the present one's are multiplied.
+    const auto s0 = std::integral_constant<int, 0>{};
+    const auto s1 = std::integral_constant<int, 1>{};
+    const auto s2 = std::integral_constant<int, 2>{};
+    const auto s3 = std::integral_constant<int, 3>{};
+    load(s0, a);
+    load(s1, b);
+    mul(s0, a, a);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (Ragged) {
+      load(s2, a);
+      mul(s1, b, b);
+      __builtin_amdgcn_sched_barrier(0);
+      load(s3, b);
+      mul(s2, a, a);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(s3, b, b);
+    } else {
+      load(s2, a);  // leaves the scales
+      mul(s1, b, a);
+      __builtin_amdgcn_sched_barrier(0);
+      load(s3, b);
+      mul(s2, a, a);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(s3, b, a);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < S - 1; i++)
+    if (i < nkt) issue(i, i);
+  int stage = 0;
+  for (int kt = 0; kt < nkt; kt++) {
+    // Stage kt's loads have landed when at most those of the later stages in flight are left.
+    const int later = min(S - 2, nkt - 1 - kt);
+    if (S >= 4 && later >= 2) wait_loads<Sh::kLoads * (S >= 4 ? 2 : 0)>();
+    else if (S >= 3 && later == 1) wait_loads<Sh::kLoads * (S >= 3 ? 1 : 0)>();
+    else wait_loads<0>();
+    // Every wave's loads have landed, and every wave is done reading the stage that is filled next.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + S - 1 < nkt) issue(kt + S - 1, stage == 0 ? S - 1 : stage - 1);
+    compute(kt, stage);
+    stage = stage == S - 1 ? 0 : stage + 1;
+  }
+
+#pragma unroll
+  for (int j = 0; j < FT; j++) {
+    const int q = (wt * FT + j) * 32 + r;
+    const bool zero = s_src[q] < 0;
+    const int dst = s_dst[q];
+    const float w = s_fac[q];
+#pragma unroll
+    for (int i = 0; i < FN; i += Swiglu ? 2 : 1) {
+      float v[16];
+#pragma unroll
+      for (int l = 0; l < 16; l++) {
+        const float z = acc[i][j][l];
+        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[i + (Swiglu ? 1 : 0)][j][l]) : z) * w;
+      }
+      mx4_store_block(A, n_out, dst, c0 + (wn * FN + i) * (Swiglu ? 16 : 32), h, v);
+    }
+  }
+}
+
 // Tiles of BT positions that E experts with P positions in all can have.
 static int64_t max_tiles(int64_t P, int64_t E, int64_t bt) { return P / bt + (E < P ? E : P); }
 
+template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
+static hipError_t launch_tile_as(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+  using Sh = MxTileShape<BN, BT, WN, WT, S, Ragged>;
+  auto* f = k_mx4_tile<BN, BT, WN, WT, S, Occ, Swiglu, Ragged>;
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), Sh::kLds, done);
+  if (e != hipSuccess) return e;
+  const int64_t n_out = Swiglu ? A.n / 2 : A.n, kc = Swiglu ? BN / 2 : BN;
+  const int64_t grid = max_tiles(A.P, A.E, BT) * ((n_out + kc - 1) / kc);
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
+  MOE_LAUNCH(f, dim3((unsigned)grid), dim3(64 * WN * WT), Sh::kLds, s, kt.start, kt.stop, A);
+  return hipGetLastError();
+}
+
+template <int BN, int BT, int WN, int WT, int S, int Occ, bool Ragged>
+static hipError_t launch_tile(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+  return A.swiglu ? launch_tile_as<BN, BT, WN, WT, S, Occ, true, Ragged>(A, s, kt)
+                  : launch_tile_as<BN, BT, WN, WT, S, Occ, false, Ragged>(A, s, kt);
+}
+
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
   const int64_t n_out = A.swiglu ? A.n / 2 : A.n;
+  const bool ragged = A.k % 256 != 0 ||
+                      ((reinterpret_cast<uintptr_t>(A.w_scales) | reinterpret_cast<uintptr_t>(A.x_scales)) & 3) != 0;
+  if (A.x_mx4 && A.P > 64 * (int64_t)A.E) {
+    if (ragged) return launch_tile<256, 128, 2, 2, 2, 1, true>(A, s, kt);
+    if (A.P >= 1024 && A.E == 1) return launch_tile<256, 256, 2, 4, 2, 2, false>(A, s, kt);
+    return launch_tile<256, 128, 2, 2, 3, 1, false>(A, s, kt);
+  }
   const int64_t grid = max_tiles(A.P, A.E, 16) * ((n_out + kFewCols - 1) / kFewCols);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
   auto* f = A.x_mx4 ? (A.swiglu ? k_mx4_few<true, true> : k_mx4_few<true, false>)
