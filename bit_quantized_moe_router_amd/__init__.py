@@ -119,6 +119,17 @@ def _check(status: int):
         raise MoEError(status, lib().moe_last_error().decode())
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -130,110 +141,118 @@ def _stream(stream):
     return torch.cuda.current_stream().cuda_stream
 
 
-# The calls from here to moe_profile_enable take torch tensors whose shapes and
-# types they check, so that a pointer never stands for less memory than the
-# kernel takes it for.  Their work goes to the tensors' device.
+# The calls from here to make_desc check their tensors' types, sizes and device,
+# so that a pointer never stands for less memory than the kernel takes it for,
+# and put their work on the tensors' device.  A decode step's call is bound by
+# this code, so the checks look at little and make no objects.
 
 def _bad(message, status=1):
     raise MoEError(status, message)
 
 
 def _value_type(t, name):
-    import torch
+    torch = _torch()
     if t.dtype is torch.bfloat16:
         return MOE_BF16
     return MOE_F32 if t.dtype is torch.float32 else _bad(f"{name} must be bfloat16 or float32 (got {t.dtype})")
 
 
-def _arg(t, name, dtype, numel, device):
-    """A contiguous tensor of this type, size and device."""
-    if t.dtype is not dtype or t.numel() != numel or not t.is_contiguous() or t.device != device:
-        _bad(f"{name} must be a contiguous {dtype} tensor of {numel} elements on {device} "
+def _arg(t, name, dtype, numel, dev):
+    """The address of a contiguous tensor of this type, size and device index."""
+    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
+        _bad(f"{name} must be a contiguous {dtype} tensor of {numel} elements on the call's device "
              f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device})")
+    return t.data_ptr()
 
 
-def _on_device(device, stream, call, *args):
-    """call(*args, stream) with the tensors' device current; stream None is that device's current one."""
-    import torch
-    if device.type != "cuda":
-        _bad(f"tensors must be on a GPU (got {device})")
-    if device.index == torch.cuda.current_device():
-        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
-        return
-    with torch.cuda.device(device):
-        _check(call(*args, torch.cuda.current_stream().cuda_stream if stream is None else stream))
+def _on_device(dev, stream, call, *args):
+    """call(*args, stream) with device `dev` current; stream None is that device's current one."""
+    torch = _torch()
+    if dev < 0:
+        _bad("the tensors must be on a GPU")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    if dev == torch._C._cuda_getDevice():
+        status = call(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = call(*args, stream)
+    if status != 0:
+        _check(status)
 
 
 def _mx4_rows(v, name, codes, scales):
-    import torch
-    if v.dim() != 2 or v.stride(1) != 1 and v.shape[1] > 1 or v.shape[0] > 1 and v.stride(0) < v.shape[1]:
-        _bad(f"{name} must be 2-D with rows of consecutive values (got {tuple(v.shape)}, strides {v.stride()})")
+    torch = _torch()
+    if v.dim() != 2:
+        _bad(f"{name} must be 2-D (got {tuple(v.shape)})")
     rows, cols = v.shape
+    ld, one = v.stride()
+    if one != 1 and cols > 1 or ld < cols and rows > 1:
+        _bad(f"{name} must have rows of consecutive values (got {tuple(v.shape)}, strides {v.stride()})")
     if cols == 0 or cols % 32:
         _bad(f"cols must be a positive multiple of 32 (got {cols})", 2)
-    _arg(codes, "codes", torch.uint8, rows * cols // 2, v.device)
-    _arg(scales, "scales", torch.uint8, rows * cols // 32, v.device)
-    return rows, cols, v.stride(0) if rows > 1 else cols
+    dev = v.get_device()
+    return (_value_type(v, name), rows, cols, ld if rows > 1 else cols, dev,
+            _arg(codes, "codes", torch.uint8, rows * cols // 2, dev),
+            _arg(scales, "scales", torch.uint8, rows * cols // 32, dev))
 
 
 def moe_mx4_quantize(x, codes, scales, stream=None):
     """x [rows, cols] float32 or bfloat16 -> codes [rows, cols/2], scales [rows, cols/32] (uint8)."""
-    rows, cols, ld = _mx4_rows(x, "x", codes, scales)
-    _on_device(x.device, stream, lib().moe_mx4_quantize, x.data_ptr(), _value_type(x, "x"), rows, cols, ld,
-               codes.data_ptr(), scales.data_ptr())
+    kind, rows, cols, ld, dev, c, s = _mx4_rows(x, "x", codes, scales)
+    _on_device(dev, stream, lib().moe_mx4_quantize, x.data_ptr(), kind, rows, cols, ld, c, s)
 
 
 def moe_mx4_dequantize(codes, scales, y, stream=None):
     """codes, scales as moe_mx4_quantize writes them -> y [rows, cols] float32 or bfloat16."""
-    rows, cols, ld = _mx4_rows(y, "y", codes, scales)
-    _on_device(y.device, stream, lib().moe_mx4_dequantize, codes.data_ptr(), scales.data_ptr(), rows, cols,
-               y.data_ptr(), _value_type(y, "y"), ld)
+    kind, rows, cols, ld, dev, c, s = _mx4_rows(y, "y", codes, scales)
+    _on_device(dev, stream, lib().moe_mx4_dequantize, c, s, rows, cols, y.data_ptr(), kind, ld)
 
 
 def make_mx4_desc(n_experts, n, k, x_type, y_type, swiglu=0) -> Mx4Desc:
     return Mx4Desc(n_experts, n, k, x_type, y_type, swiglu)
 
 
-def _row_count(t, name, kind, cols, scales, device):
-    """Rows of a 2-D operand of type `kind` with `cols` values a row, its tensors checked."""
-    import torch
-    dtype = (torch.float32, torch.bfloat16, torch.uint8)[kind]
-    width = cols // 2 if kind == MOE_MX4 else cols
+def _rows(t, name, kind, cols, scales, dev):
+    """(rows, address, scales' address) of a 2-D operand of type `kind` with `cols` values a row."""
+    torch = _torch()
+    if kind == MOE_MX4:
+        dtype, width = torch.uint8, cols // 2
+    else:
+        dtype, width = torch.float32 if kind == MOE_F32 else torch.bfloat16, cols
     if t.dim() != 2 or t.shape[1] != width:
         _bad(f"{name} must be 2-D with {width} columns (got {tuple(t.shape)})")
     rows = t.shape[0]
-    _arg(t, name, dtype, rows * width, device)
+    p = _arg(t, name, dtype, rows * width, dev)
     if kind == MOE_MX4:
         if scales is None:
             _bad(f"{name}_scales is missing")
-        _arg(scales, name + "_scales", torch.uint8, rows * (cols // 32), device)
-    elif scales is not None:
+        return rows, p, _arg(scales, name + "_scales", torch.uint8, rows * (cols // 32), dev)
+    if scales is not None:
         _bad(f"{name}_scales goes with a MOE_MX4 {name} only")
-    return rows
+    return rows, p, None
 
 
 def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, y, y_scales=None, src_rows=None,
                     src_div=1, dst_rows=None, row_scale=None, stream=None):
     """Position i of expert e's range gives y[dst_rows[i]] = row_scale * W_e x[src_rows[i] // src_div]."""
-    import torch
-    dev, E, n, k = x.device, desc.n_experts, desc.n, desc.k
-    if desc.x_type not in (MOE_BF16, MOE_MX4) or desc.y_type not in (MOE_F32, MOE_BF16, MOE_MX4):
-        _bad(f"x_type must be MOE_BF16 or MOE_MX4, y_type one of the three types (got {desc.x_type}, {desc.y_type})")
+    torch = _torch()
+    E, n, k, x_type, y_type = desc.n_experts, desc.n, desc.k, desc.x_type, desc.y_type
+    if x_type not in (MOE_BF16, MOE_MX4) or y_type not in (MOE_F32, MOE_BF16, MOE_MX4):
+        _bad(f"x_type must be MOE_BF16 or MOE_MX4, y_type one of the three types (got {x_type}, {y_type})")
     if k <= 0 or k % 32:
         _bad(f"k must be a positive multiple of 32 (got {k})", 2)
-    _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev)
-    _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev)
-    _arg(expert_offsets, "expert_offsets", torch.int32, E + 1, dev)
-    x_rows = _row_count(x, "x", desc.x_type, k, x_scales, dev)
-    y_rows = _row_count(y, "y", desc.y_type, n // 2 if desc.swiglu else n, y_scales, dev)
-    for t, name in ((src_rows, "src_rows"), (dst_rows, "dst_rows")):
-        if t is not None:
-            _arg(t, name, torch.int32, rows, dev)
-    if row_scale is not None:
-        _arg(row_scale, "row_scale", torch.float32, y_rows, dev)
-    _on_device(dev, stream, lib().moe_mx4_experts, C.byref(desc), w_codes.data_ptr(), w_scales.data_ptr(),
-               x.data_ptr(), _ptr(x_scales), x_rows, expert_offsets.data_ptr(), rows, _ptr(src_rows), src_div,
-               _ptr(dst_rows), _ptr(row_scale), y.data_ptr(), _ptr(y_scales), y_rows)
+    dev, i32 = x.get_device(), torch.int32
+    wc = _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev)
+    ws = _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev)
+    off = _arg(expert_offsets, "expert_offsets", i32, E + 1, dev)
+    x_rows, xp, xs = _rows(x, "x", x_type, k, x_scales, dev)
+    y_rows, yp, ys = _rows(y, "y", y_type, n // 2 if desc.swiglu else n, y_scales, dev)
+    src = None if src_rows is None else _arg(src_rows, "src_rows", i32, rows, dev)
+    dst = None if dst_rows is None else _arg(dst_rows, "dst_rows", i32, rows, dev)
+    fac = None if row_scale is None else _arg(row_scale, "row_scale", torch.float32, y_rows, dev)
+    _on_device(dev, stream, lib().moe_mx4_experts, C.byref(desc), wc, ws, xp, xs, x_rows, off, rows, src, src_div, dst,
+               fac, yp, ys, y_rows)
 
 
 def moe_balance_loss_workspace_bytes(T: int, n_experts: int) -> int:
@@ -243,49 +262,42 @@ def moe_balance_loss_workspace_bytes(T: int, n_experts: int) -> int:
 
 
 def _logits(logits, valid):
-    import torch
+    """(T, E, type, device index, address, valid's address)."""
+    torch = _torch()
     if logits.dim() != 2 or not logits.is_contiguous():
         _bad(f"logits must be 2-D and contiguous (got {tuple(logits.shape)}, strides {logits.stride()})")
+    T, E = logits.shape
+    dev = logits.get_device()
+    v = None
     if valid is not None:
-        dtype = torch.bool if valid.dtype is torch.bool else torch.uint8
-        _arg(valid, "valid", dtype, logits.shape[0], logits.device)
-    return (*logits.shape, _value_type(logits, "logits"))
+        v = _arg(valid, "valid", torch.bool if valid.dtype is torch.bool else torch.uint8, T, dev)
+    return T, E, _value_type(logits, "logits"), dev, logits.data_ptr(), v
 
 
 def moe_balance_loss_forward(logits, topk_ids, valid, balance_coef, z_coef, losses, counts, mean_prob, n_valid, ws,
                              stream=None):
     """logits [T, E], topk_ids [T, k] int32, valid [T] uint8/bool or None -> losses [3] (loss, balance, z),
     counts [E] int32, mean_prob [E], n_valid [1] int32."""
-    import torch
-    T, E, kind = _logits(logits, valid)
-    dev = logits.device
+    torch = _torch()
+    T, E, kind, dev, p, v = _logits(logits, valid)
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         _bad(f"topk_ids must be [T, k] (got {tuple(topk_ids.shape)} for T = {T})")
-    k = topk_ids.shape[1]
-    _arg(topk_ids, "topk_ids", torch.int32, T * k, dev)
-    _arg(losses, "losses", torch.float32, 3, dev)
-    _arg(counts, "counts", torch.int32, E, dev)
-    _arg(mean_prob, "mean_prob", torch.float32, E, dev)
-    _arg(n_valid, "n_valid", torch.int32, 1, dev)
-    _arg(ws, "ws", torch.uint8, ws.numel(), dev)
-    _on_device(dev, stream, lib().moe_balance_loss_forward, logits.data_ptr(), kind, T, E, topk_ids.data_ptr(), k,
-               _ptr(valid), balance_coef, z_coef, losses.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(),
-               n_valid.data_ptr(), ws.data_ptr(), ws.numel())
+    k, i32, f32 = topk_ids.shape[1], torch.int32, torch.float32
+    _on_device(dev, stream, lib().moe_balance_loss_forward, p, kind, T, E, _arg(topk_ids, "topk_ids", i32, T * k, dev),
+               k, v, balance_coef, z_coef, _arg(losses, "losses", f32, 3, dev), _arg(counts, "counts", i32, E, dev),
+               _arg(mean_prob, "mean_prob", f32, E, dev), _arg(n_valid, "n_valid", i32, 1, dev),
+               _arg(ws, "ws", torch.uint8, ws.numel(), dev), ws.numel())
 
 
 def moe_balance_loss_backward(logits, top_k, valid, balance_coef, z_coef, counts, n_valid, grad_loss, dlogits,
                               stream=None):
     """Gradient of moe_balance_loss_forward's loss; grad_loss [1] float32 or None (1)."""
-    import torch
-    T, E, kind = _logits(logits, valid)
-    dev = logits.device
-    _arg(counts, "counts", torch.int32, E, dev)
-    _arg(n_valid, "n_valid", torch.int32, 1, dev)
-    if grad_loss is not None:
-        _arg(grad_loss, "grad_loss", torch.float32, 1, dev)
-    _arg(dlogits, "dlogits", logits.dtype, T * E, dev)
-    _on_device(dev, stream, lib().moe_balance_loss_backward, logits.data_ptr(), kind, T, E, top_k, _ptr(valid),
-               balance_coef, z_coef, counts.data_ptr(), n_valid.data_ptr(), _ptr(grad_loss), dlogits.data_ptr())
+    torch = _torch()
+    T, E, kind, dev, p, v = _logits(logits, valid)
+    _on_device(dev, stream, lib().moe_balance_loss_backward, p, kind, T, E, top_k, v, balance_coef, z_coef,
+               _arg(counts, "counts", torch.int32, E, dev), _arg(n_valid, "n_valid", torch.int32, 1, dev),
+               None if grad_loss is None else _arg(grad_loss, "grad_loss", torch.float32, 1, dev),
+               _arg(dlogits, "dlogits", logits.dtype, T * E, dev))
 
 
 def make_desc(hidden, n_experts, top_k, inter, shared_inter, gemv_max_rows=-1, max_chunk=2048,
