@@ -141,7 +141,7 @@ struct Mx4ExpertArgs {
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt = KTime{});
 
 // The router's balance loss (balance.hip).
-constexpr int kBalMaxParts = 512;  // partial rows of the forward pass
+constexpr int kBalMaxParts = 256;  // partial rows of the forward pass
 struct BalanceArgs {
   const void* logits;    // [T][E] fp32 or bf16
   const int32_t* ids;    // [T][k]
