@@ -262,6 +262,52 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
+// Source row, target row and factor of a tile's positions, by all threads of NW waves.
+template <int BT, int NW>
+__device__ __forceinline__ void mx4_tile_rows(const Mx4ExpertArgs& A, const MxTile& t, int* s_src, int* s_dst, float* s_fac) {
+  for (int q = threadIdx.x; q < BT; q += 64 * NW) {
+    const bool on = q < t.rows;
+    const int dst = on ? mx4_dst(A, t.row + q) : -1;
+    s_src[q] = on ? mx4_src(A, t.row + q) : -1;
+    s_dst[q] = dst;
+    s_fac[q] = A.row_scale && dst >= 0 ? A.row_scale[dst] : 1.f;
+  }
+  __syncthreads();
+}
+
+// Weight row of tile row q from column c0 of y on.  With SwiGLU blocks of 32
+// gate rows and of the same 32 up rows take turns.  Rows past the last one read
+// the last one, and (in the kernels) positions past the tile, or with no row of
+// x, row 0: their results are dropped, or zeroed.
+template <bool Swiglu>
+__device__ __forceinline__ int64_t mx4_w_row(const Mx4ExpertArgs& A, int e, int n_out, int c0, int q) {
+  const int c = Swiglu ? c0 + (q >> 6) * 32 + (q & 31) : c0 + q;
+  return (int64_t)e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
+}
+
+// The K loop over S stages: issue(kt, stage) starts a tile's loads (Loads
+// instructions a wave), compute(kt, stage) multiplies it.
+template <int S, int Loads, class Issue, class Compute>
+__device__ __forceinline__ void mx4_k_loop(int nkt, Issue issue, Compute compute) {
+#pragma unroll
+  for (int i = 0; i < S - 1; i++)
+    if (i < nkt) issue(i, i);
+  int stage = 0;
+  for (int kt = 0; kt < nkt; kt++) {
+    // Stage kt's loads have landed when at most those of the later stages in flight are left.
+    const int later = min(S - 2, nkt - 1 - kt);
+    if (S >= 5 && later >= 3) wait_loads<Loads * (S >= 5 ? 3 : 0)>();
+    else if (S >= 4 && later == 2) wait_loads<Loads * (S >= 4 ? 2 : 0)>();
+    else if (S >= 3 && later == 1) wait_loads<Loads * (S >= 3 ? 1 : 0)>();
+    else wait_loads<0>();
+    // Every wave's loads have landed, and every wave is done reading the stage that is filled next.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kt + S - 1 < nkt) issue(kt + S - 1, stage == 0 ? S - 1 : stage - 1);
+    compute(kt, stage);
+    stage = stage == S - 1 ? 0 : stage + 1;
+  }
+}
+
 template <int BN, int BT, int WN, int WT, int S, bool Ragged>
 struct MxTileShape {
   static constexpr int kWaves = WN * WT;
@@ -311,6 +357,31 @@ __device__ __forceinline__ void mx4_store_block(const Mx4ExpertArgs& A, int n_ou
   }
 }
 
+// A wave's FN x FT results to y: columns from c0 on (with SwiGLU gate and up
+// blocks take turns), tile positions from q0 on.
+template <int FN, int FT, bool Swiglu>
+__device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, const f32x16_t (&acc)[FN][FT], int n_out, int c0,
+                                               const int* s_src, const int* s_dst, const float* s_fac, int q0) {
+  const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+#pragma unroll
+  for (int j = 0; j < FT; j++) {
+    const int q = q0 + j * 32 + r;
+    const bool zero = s_src[q] < 0;
+    const int dst = s_dst[q];
+    const float w = s_fac[q];
+#pragma unroll
+    for (int i = 0; i < FN; i += Swiglu ? 2 : 1) {
+      float v[16];
+#pragma unroll
+      for (int l = 0; l < 16; l++) {
+        const float z = acc[i][j][l];
+        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[i + (Swiglu ? 1 : 0)][j][l]) : z) * w;
+      }
+      mx4_store_block(A, n_out, dst, c0 + i * (Swiglu ? 16 : 32), h, v);
+    }
+  }
+}
+
 template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
 __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A) {
   using Sh = MxTileShape<BN, BT, WN, WT, S, Ragged>;
@@ -331,23 +402,9 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A)
   const int r = lane & 31, h = lane >> 5;
   const int nb = A.k >> 5, nkt = (nb + kKtBlocks - 1) / kKtBlocks;
 
-  for (int q = threadIdx.x; q < BT; q += 64 * NW) {
-    const bool on = q < t.rows;
-    const int dst = on ? mx4_dst(A, t.row + q) : -1;
-    s_src[q] = on ? mx4_src(A, t.row + q) : -1;
-    s_dst[q] = dst;
-    s_fac[q] = A.row_scale && dst >= 0 ? A.row_scale[dst] : 1.f;
-  }
-  __syncthreads();
+  mx4_tile_rows<BT, NW>(A, t, s_src, s_dst, s_fac);
 
-  // Memory row of tile row q.  With SwiGLU blocks of 32 gate rows and of the
-  // same 32 up rows take turns.  Rows past the last one read the last one, and
-  // positions past the tile, or with no row of x, row 0 (their results are
-  // dropped, or zeroed).
-  auto w_row = [&](int q) -> int64_t {
-    const int c = Swiglu ? c0 + (q >> 6) * 32 + (q & 31) : c0 + q;
-    return (int64_t)t.e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
-  };
+  auto w_row = [&](int q) -> int64_t { return mx4_w_row<Swiglu>(A, t.e, n_out, c0, q); };
   const uint8_t* code_p[Sh::kCodeLoads];
   const uint8_t* scale_p[Sh::kScaleLoads];
 #pragma unroll
@@ -453,73 +510,193 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A)
     }
   };
 
-#pragma unroll
-  for (int i = 0; i < S - 1; i++)
-    if (i < nkt) issue(i, i);
-  int stage = 0;
-  for (int kt = 0; kt < nkt; kt++) {
-    // Stage kt's loads have landed when at most those of the later stages in flight are left.
-    const int later = min(S - 2, nkt - 1 - kt);
-    if (S >= 4 && later >= 2) wait_loads<Sh::kLoads * (S >= 4 ? 2 : 0)>();
-    else if (S >= 3 && later == 1) wait_loads<Sh::kLoads * (S >= 3 ? 1 : 0)>();
-    else wait_loads<0>();
-    // Every wave's loads have landed, and every wave is done reading the stage that is filled next.
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + S - 1 < nkt) issue(kt + S - 1, stage == 0 ? S - 1 : stage - 1);
-    compute(kt, stage);
-    stage = stage == S - 1 ? 0 : stage + 1;
-  }
+  mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
+  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32);
+}
 
+// ---------------------------------------------------------------------------
+// Many rows an expert, bf16 x: the same tiles with K tiles of 128 columns (64
+// bytes of codes and 256 bytes of x a row).  A wave reads its weight codes from
+// LDS, converts them to bf16 (exactly, two a conversion) and multiplies with
+// the 32x32x16 instruction; each conversion serves FT instructions.
+//
+// LDS.  x: 16-byte piece c of a row at slot (c ^ row % 8).  Codes: block b at
+// slot (b ^ (row / 4) % 4), 4 blocks a row.  In turn p of a tile a lane of half
+// h multiplies block 2 p + h, 8 columns at a time.  Ragged (k no multiple of
+// 128, or the scales not dword aligned): as above.
+// ---------------------------------------------------------------------------
+constexpr int kBtBlocks = 4;  // blocks of a K tile
+
+template <int BN, int BT, int WN, int WT, int S, bool Ragged>
+struct MxBfShape {
+  static constexpr int kWaves = WN * WT;
+  static constexpr int kCodeLoads = BN / 16 / kWaves;  // of 16 rows each, a wave
+  static constexpr int kXLoads = BT / 4 / kWaves;      // of 4 rows each
+  static constexpr int kScaleRows = Ragged ? 16 : 64;  // rows of a scale load
+  static constexpr int kScaleLoads = (BN / kScaleRows + kWaves - 1) / kWaves;
+  static constexpr int kLoads = kCodeLoads + kXLoads + kScaleLoads;
+  static constexpr int kScaleRow = Ragged ? 16 : 4;
+  static constexpr int kStage = BN * (64 + kScaleRow) + BT * 256;
+  static constexpr int kLds = S * kStage + BT * 12;
+  static_assert(BN / 16 % kWaves == 0 && BT / 4 % kWaves == 0, "loads divide among the waves");
+  static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
+  static_assert(kLoads * (S - 2) < 64, "vmcnt");
+};
+
+template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
+__global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile_bf16(Mx4ExpertArgs A) {
+  using Sh = MxBfShape<BN, BT, WN, WT, S, Ragged>;
+  constexpr int FN = BN / 32 / WN, FT = BT / 32 / WT, NW = WN * WT;
+  constexpr int kCols = Swiglu ? BN / 2 : BN;  // columns of y
+  static_assert(!Swiglu || FN % 2 == 0, "gate and up blocks go in pairs");
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+  int* s_src = reinterpret_cast<int*>(sm + S * Sh::kStage);
+  int* s_dst = s_src + BT;
+  float* s_fac = reinterpret_cast<float*>(s_dst + BT);
+  const int n_out = Swiglu ? A.n >> 1 : A.n;
+  const int cols = (n_out + kCols - 1) / kCols;
+  const int tile = blockIdx.x / cols, c0 = (blockIdx.x - tile * cols) * kCols;
+  MxTile t;
+  if (!mx4_find_tile<BT>(A.offsets, A.E, A.P, tile, &t)) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wn = wave % WN, wt = wave / WN;
+  const int r = lane & 31, h = lane >> 5;
+  const int nb = A.k >> 5, nkt = (nb + kBtBlocks - 1) / kBtBlocks;
+
+  mx4_tile_rows<BT, NW>(A, t, s_src, s_dst, s_fac);
+
+  auto w_row = [&](int q) -> int64_t { return mx4_w_row<Swiglu>(A, t.e, n_out, c0, q); };
+  const uint8_t *code_p[Sh::kCodeLoads], *x_p[Sh::kXLoads], *scale_p[Sh::kScaleLoads];
 #pragma unroll
-  for (int j = 0; j < FT; j++) {
-    const int q = (wt * FT + j) * 32 + r;
-    const bool zero = s_src[q] < 0;
-    const int dst = s_dst[q];
-    const float w = s_fac[q];
+  for (int j = 0; j < Sh::kCodeLoads; j++)
+    code_p[j] = A.w_codes + w_row((wave + NW * j) * 16 + (lane >> 2)) * nb * kMxBlockBytes;
 #pragma unroll
-    for (int i = 0; i < FN; i += Swiglu ? 2 : 1) {
-      float v[16];
+  for (int j = 0; j < Sh::kXLoads; j++)
+    x_p[j] = static_cast<const uint8_t*>(A.x) + (int64_t)max(s_src[(wave + NW * j) * 4 + (lane >> 4)], 0) * A.k * 2;
+  // Where the scale loads do not divide among the waves, the last ones are made twice.
+  auto scale_load = [&](int j) { return min(wave + NW * j, BN / Sh::kScaleRows - 1); };
 #pragma unroll
-      for (int l = 0; l < 16; l++) {
-        const float z = acc[i][j][l];
-        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[i + (Swiglu ? 1 : 0)][j][l]) : z) * w;
-      }
-      mx4_store_block(A, n_out, dst, c0 + (wn * FN + i) * (Swiglu ? 16 : 32), h, v);
+  for (int j = 0; j < Sh::kScaleLoads; j++)
+    scale_p[j] = A.w_scales + w_row(scale_load(j) * Sh::kScaleRows + (Ragged ? lane >> 2 : lane)) * nb;
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
+  auto issue = [&](int kt, int stage) {
+    const uint32_t base = lds0 + stage * Sh::kStage;
+    int cb = kt * kBtBlocks + ((lane & 3) ^ ((lane >> 4) & 3));
+    // A row of x is row j of 4 in its load, and row (4 (wave + NW j) + lane / 16) % 8 of the swizzle.
+    int so = kt * kBtBlocks + (Ragged ? lane & 3 : 0);
+    if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
+#pragma unroll
+    for (int j = 0; j < Sh::kCodeLoads; j++)
+      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+#pragma unroll
+    for (int j = 0; j < Sh::kXLoads; j++) {
+      int c = (lane & 15) ^ ((4 * (wave + NW * j) + (lane >> 4)) & 7);
+      int xb = kt * kBtBlocks * 4 + c;
+      if (Ragged) xb = min(xb, nb * 4 - 1);
+      load_to_lds<16>(x_p[j] + xb * 16, base + BN * 64 + (wave + NW * j) * 1024);
     }
-  }
+#pragma unroll
+    for (int j = 0; j < Sh::kScaleLoads; j++)
+      load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + BN * 64 + BT * 256 + scale_load(j) * 256);
+  };
+
+  f32x16_t acc[FN][FT] = {};
+  auto compute = [&](int kt, int stage) {
+    const uint8_t* wl = sm + stage * Sh::kStage + (wn * FN * 32 + r) * 64;
+    const uint8_t* xl = sm + stage * Sh::kStage + BN * 64 + (wt * FT * 32 + r) * 256;
+    const uint8_t* sl = sm + stage * Sh::kStage + BN * 64 + BT * 256 + (wn * FN * 32 + r) * Sh::kScaleRow;
+    struct Frags {
+      uint4 w[FN], x[FT][4];
+      float s[FN];
+    } a, b;
+    auto load = [&](int p, Frags& d) {
+      const int blk = 2 * p + h;
+      const bool in = !Ragged || kt * kBtBlocks + blk < nb;
+#pragma unroll
+      for (int f = 0; f < FN; f++) {
+        d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 64 + ((blk ^ ((r >> 2) & 3)) * 16));
+        uint32_t sc = *reinterpret_cast<const uint32_t*>(sl + f * 32 * Sh::kScaleRow + (Ragged ? blk * 4 : 0));
+        if (!Ragged) sc >>= 8 * blk;
+        d.s[f] = mx4_scale_f32(in ? sc & 0xFFu : 127u);
+      }
+#pragma unroll
+      for (int f = 0; f < FT; f++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+          d.x[f][j] = *reinterpret_cast<const uint4*>(xl + f * 32 * 256 + (((4 * blk + j) ^ (r & 7)) * 16));
+          if (!in) d.x[f][j] = make_uint4(0, 0, 0, 0);
+        }
+    };
+    auto mul = [&](const Frags& d) {
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        bf16x8_t w[FN];
+#pragma unroll
+        for (int i = 0; i < FN; i++) {
+          const uint32_t c = j == 0 ? d.w[i].x : j == 1 ? d.w[i].y : j == 2 ? d.w[i].z : d.w[i].w;
+          w[i] = __builtin_bit_cast(bf16x8_t, mx4_unpack8_bf16(c, d.s[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < FN; i++)
+#pragma unroll
+          for (int f = 0; f < FT; f++)
+            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], __builtin_bit_cast(bf16x8_t, d.x[f][j]), acc[i][f], 0, 0, 0);
+      }
+    };
+    load(0, a);
+    load(1, b);
+    mul(a);
+    mul(b);
+  };
+  mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
+  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32);
 }
 
 // Tiles of BT positions that E experts with P positions in all can have.
 static int64_t max_tiles(int64_t P, int64_t E, int64_t bt) { return P / bt + (E < P ? E : P); }
 
-template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
-static hipError_t launch_tile_as(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
-  using Sh = MxTileShape<BN, BT, WN, WT, S, Ragged>;
-  auto* f = k_mx4_tile<BN, BT, WN, WT, S, Occ, Swiglu, Ragged>;
-  static std::atomic<uint64_t> done{0};
-  hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), Sh::kLds, done);
+template <int BN, int BT, int NW, bool Swiglu>
+static hipError_t launch_tile(void (*f)(Mx4ExpertArgs), int lds, std::atomic<uint64_t>& done, const Mx4ExpertArgs& A,
+                              hipStream_t s, const KTime& kt) {
+  hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), lds, done);
   if (e != hipSuccess) return e;
   const int64_t n_out = Swiglu ? A.n / 2 : A.n, kc = Swiglu ? BN / 2 : BN;
   const int64_t grid = max_tiles(A.P, A.E, BT) * ((n_out + kc - 1) / kc);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  MOE_LAUNCH(f, dim3((unsigned)grid), dim3(64 * WN * WT), Sh::kLds, s, kt.start, kt.stop, A);
+  MOE_LAUNCH(f, dim3((unsigned)grid), dim3(64 * NW), lds, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
 
+// 4-bit x.
 template <int BN, int BT, int WN, int WT, int S, int Occ, bool Ragged>
-static hipError_t launch_tile(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
-  return A.swiglu ? launch_tile_as<BN, BT, WN, WT, S, Occ, true, Ragged>(A, s, kt)
-                  : launch_tile_as<BN, BT, WN, WT, S, Occ, false, Ragged>(A, s, kt);
+static hipError_t tile_mx4(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+  static std::atomic<uint64_t> done[2];
+  constexpr int lds = MxTileShape<BN, BT, WN, WT, S, Ragged>::kLds;
+  return A.swiglu ? launch_tile<BN, BT, WN * WT, true>(k_mx4_tile<BN, BT, WN, WT, S, Occ, true, Ragged>, lds, done[1], A, s, kt)
+                  : launch_tile<BN, BT, WN * WT, false>(k_mx4_tile<BN, BT, WN, WT, S, Occ, false, Ragged>, lds, done[0], A, s, kt);
+}
+
+// bf16 x.
+template <int BN, int BT, int WN, int WT, int S, int Occ, bool Ragged>
+static hipError_t tile_bf16(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+  static std::atomic<uint64_t> done[2];
+  constexpr int lds = MxBfShape<BN, BT, WN, WT, S, Ragged>::kLds;
+  return A.swiglu ? launch_tile<BN, BT, WN * WT, true>(k_mx4_tile_bf16<BN, BT, WN, WT, S, Occ, true, Ragged>, lds, done[1], A, s, kt)
+                  : launch_tile<BN, BT, WN * WT, false>(k_mx4_tile_bf16<BN, BT, WN, WT, S, Occ, false, Ragged>, lds, done[0], A, s, kt);
 }
 
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
-  const int64_t n_out = A.swiglu ? A.n / 2 : A.n;
-  const bool ragged = A.k % 256 != 0 ||
-                      ((reinterpret_cast<uintptr_t>(A.w_scales) | reinterpret_cast<uintptr_t>(A.x_scales)) & 3) != 0;
-  if (A.x_mx4 && A.P > 64 * (int64_t)A.E) {
-    if (ragged) return launch_tile<256, 128, 2, 2, 2, 1, true>(A, s, kt);
-    if (A.P >= 1024 && A.E == 1) return launch_tile<256, 256, 2, 4, 2, 2, false>(A, s, kt);
-    return launch_tile<256, 128, 2, 2, 3, 1, false>(A, s, kt);
+  const int64_t n_out = A.swiglu ? A.n / 2 : A.n, avg = A.P / A.E;
+  const bool dwords = ((reinterpret_cast<uintptr_t>(A.w_scales) | reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 3) == 0;
+  if (A.x_mx4 && avg >= 64) {
+    if (!dwords || A.k % 256) return tile_mx4<256, 128, 2, 2, 2, 1, true>(A, s, kt);
+    if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 2, false>(A, s, kt);
+    return tile_mx4<256, 128, 2, 2, 3, 1, false>(A, s, kt);
+  }
+  if (!A.x_mx4 && avg >= 12) {
+    const bool ragged = !dwords || A.k % 128;
+    if (avg >= 64) return ragged ? tile_bf16<256, 128, 4, 2, 2, 2, true>(A, s, kt) : tile_bf16<256, 128, 4, 2, 3, 2, false>(A, s, kt);
+    return ragged ? tile_bf16<256, 32, 4, 1, 3, 2, true>(A, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, s, kt);
   }
   const int64_t grid = max_tiles(A.P, A.E, 16) * ((n_out + kFewCols - 1) / kFewCols);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
