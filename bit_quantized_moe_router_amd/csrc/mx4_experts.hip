@@ -308,6 +308,9 @@ __device__ __forceinline__ void mx4_k_loop(int nkt, Issue issue, Compute compute
   }
 }
 
+// LDS bytes that a wave of mx4_store_tile needs for C columns.
+constexpr int mx4_store_bytes(int C) { return 32 * (C * 4 + 16); }
+
 template <int BN, int BT, int WN, int WT, int S, bool Ragged>
 struct MxTileShape {
   static constexpr int kWaves = WN * WT;
@@ -321,48 +324,24 @@ struct MxTileShape {
   static_assert((BN + BT) / 8 % kWaves == 0, "code loads divide among the waves");
   static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
   static_assert(kLoads * (S - 2) < 64, "vmcnt");
+  static_assert(mx4_store_bytes(BN / WN) * kWaves <= S * kStage, "the results pass through the stages' LDS");
 };
 
-// Values of one 32-column block for the lane's position, in the instruction's
-// result order: element 4 i + j is column 8 i + 4 h + j.
-__device__ __forceinline__ void mx4_store_block(const Mx4ExpertArgs& A, int n_out, int dst, int c0, int h, float v[16]) {
-  if (A.y_type == kMxTypeMx4) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 16; i++) m = max(m, f32_abs_bits(v[i]));
-    m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-    const int s = mx4_scale_byte(m);
-    const float inv = mx4_inv_scale(s);
-    const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
-    if (dst < 0 || c0 >= n_out) return;
-    const int64_t block = (int64_t)dst * (n_out >> 5) + (c0 >> 5);
-    uint16_t* out = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes);
-    out[h] = (uint16_t)d0;
-    out[2 + h] = (uint16_t)(d0 >> 16);
-    out[4 + h] = (uint16_t)d1;
-    out[6 + h] = (uint16_t)(d1 >> 16);
-    if (h == 0) A.y_scales[block] = (uint8_t)s;
-    return;
-  }
-  if (dst < 0) return;
-#pragma unroll
-  for (int i = 0; i < 16; i++) {
-    const int c = c0 + 8 * (i >> 2) + 4 * h + (i & 3);
-    if (c >= n_out) continue;
-    const int64_t at = (int64_t)dst * n_out + c;
-    if (A.y_type == kMxTypeF32)
-      static_cast<float*>(A.y)[at] = v[i];
-    else
-      static_cast<uint16_t*>(A.y)[at] = (uint16_t)f32_to_bf16_bits(v[i]);
-  }
-}
-
-// A wave's FN x FT results to y: columns from c0 on (with SwiGLU gate and up
-// blocks take turns), tile positions from q0 on.
+// A wave's FN x FT results to y: C columns from c0 on (with SwiGLU gate and up
+// blocks take turns), tile positions from q0 on.  A lane holds one position and
+// 4 consecutive columns at a time, so its own stores would be 8 or 16 bytes a
+// row; 32 positions at a time go through `buf`, LDS of the wave's own, and out
+// as whole rows of C columns.  (Element by element from the registers, the
+// stores took 210 of 355 us at 4096 x 8192 x 8192 with bf16 results.)
 template <int FN, int FT, bool Swiglu>
 __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, const f32x16_t (&acc)[FN][FT], int n_out, int c0,
-                                               const int* s_src, const int* s_dst, const float* s_fac, int q0) {
-  const int r = threadIdx.x & 31, h = (threadIdx.x >> 5) & 1;
+                                               const int* s_src, const int* s_dst, const float* s_fac, int q0,
+                                               uint8_t* buf) {
+  constexpr int FO = Swiglu ? FN / 2 : FN, C = FO * 32;
+  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  // 16-byte stores where every row of y starts at a multiple of 16 bytes.
+  const bool f32 = A.y_type == kMxTypeF32;
+  const bool wide = n_out % (f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 15) == 0;
 #pragma unroll
   for (int j = 0; j < FT; j++) {
     const int q = q0 + j * 32 + r;
@@ -370,15 +349,75 @@ __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, const f32
     const int dst = s_dst[q];
     const float w = s_fac[q];
 #pragma unroll
-    for (int i = 0; i < FN; i += Swiglu ? 2 : 1) {
-      float v[16];
+    for (int i = 0; i < FO; i++) {
+      float v[16];  // element 4 g + l is column 8 g + 4 h + l of the block
 #pragma unroll
       for (int l = 0; l < 16; l++) {
-        const float z = acc[i][j][l];
-        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[i + (Swiglu ? 1 : 0)][j][l]) : z) * w;
+        const float z = acc[Swiglu ? 2 * i : i][j][l];
+        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[Swiglu ? 2 * i + 1 : i][j][l]) : z) * w;
       }
-      mx4_store_block(A, n_out, dst, c0 + i * (Swiglu ? 16 : 32), h, v);
+      if (A.y_type == kMxTypeMx4) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int l = 0; l < 16; l++) m = max(m, f32_abs_bits(v[l]));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        const int s = mx4_scale_byte(m);
+        const float inv = mx4_inv_scale(s);
+        // Half h has the 16-bit pieces h, 2 + h, 4 + h, 6 + h of the block's 8; it keeps those of its
+        // own 8 bytes and gets the others from the other half.
+        const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
+        const uint32_t own = h ? d1 : d0, got = (uint32_t)__shfl_xor((int)(h ? d0 : d1), 32);
+        const uint32_t lo = h ? got : own, hi = h ? own : got;
+        if (dst >= 0 && c0 + i * 32 < n_out) {
+          const int64_t block = (int64_t)dst * (n_out >> 5) + ((c0 + i * 32) >> 5);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes + 8 * h) =
+              make_uint2((lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u));
+          if (h == 0) A.y_scales[block] = (uint8_t)s;
+        }
+      } else if (f32) {
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+          *reinterpret_cast<float4*>(buf + r * (C * 4 + 16) + (i * 32 + 8 * g + 4 * h) * 4) =
+              make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+          *reinterpret_cast<uint2*>(buf + r * (C * 2 + 16) + (i * 32 + 8 * g + 4 * h) * 2) =
+              make_uint2(f32_to_bf16_bits(v[4 * g]) | f32_to_bf16_bits(v[4 * g + 1]) << 16,
+                         f32_to_bf16_bits(v[4 * g + 2]) | f32_to_bf16_bits(v[4 * g + 3]) << 16);
+      }
     }
+    if (A.y_type == kMxTypeMx4) continue;
+    // The wave's lanes exchange through LDS: writes before reads, and reads before the next round's writes.
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    auto rows = [&](auto size_c) {
+      constexpr int size = size_c.value, stride = C * size + 16, per = C * size / 16;  // lanes a row
+      if (wide) {
+#pragma unroll
+        for (int p = 0; p < 32 * per / 64; p++) {
+          const int row = p * (64 / per) + lane / per, piece = lane % per, c = c0 + piece * (16 / size);
+          const uint4 d = *reinterpret_cast<const uint4*>(buf + row * stride + piece * 16);
+          const int to = s_dst[q0 + j * 32 + row];
+          if (to >= 0 && c < n_out)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + ((int64_t)to * n_out + c) * size) = d;
+        }
+      } else {
+        for (int e = lane; e < 32 * C; e += 64) {
+          const int row = e / C, col = e % C, c = c0 + col, to = s_dst[q0 + j * 32 + row];
+          if (to < 0 || c >= n_out) continue;
+          const int64_t at = (int64_t)to * n_out + c;
+          if constexpr (size == 4)
+            static_cast<float*>(A.y)[at] = *reinterpret_cast<const float*>(buf + row * stride + col * 4);
+          else
+            static_cast<uint16_t*>(A.y)[at] = *reinterpret_cast<const uint16_t*>(buf + row * stride + col * 2);
+        }
+      }
+    };
+    if (f32) rows(std::integral_constant<int, 4>{});
+    else rows(std::integral_constant<int, 2>{});
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -511,7 +550,9 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A)
   };
 
   mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
-  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32);
+  __syncthreads();  // the stages are free
+  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32,
+                                 sm + wave * mx4_store_bytes(kCols / WN));
 }
 
 // ---------------------------------------------------------------------------
@@ -541,6 +582,7 @@ struct MxBfShape {
   static_assert(BN / 16 % kWaves == 0 && BT / 4 % kWaves == 0, "loads divide among the waves");
   static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
   static_assert(kLoads * (S - 2) < 64, "vmcnt");
+  static_assert(mx4_store_bytes(BN / WN) * kWaves <= S * kStage, "the results pass through the stages' LDS");
 };
 
 template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
@@ -649,7 +691,9 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile_bf16(Mx4ExpertAr
     mul(b);
   };
   mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
-  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32);
+  __syncthreads();  // the stages are free
+  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32,
+                                 sm + wave * mx4_store_bytes(kCols / WN));
 }
 
 // Tiles of BT positions that E experts with P positions in all can have.
