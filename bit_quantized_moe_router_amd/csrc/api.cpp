@@ -184,6 +184,14 @@ moe_status check_device() {
   return MOE_OK;
 }
 
+// Compute units of the current device (after check_device on it).
+int device_cus() {
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 1;
+  std::lock_guard<std::mutex> lk(g_dev_mu);
+  return g_dev_cus[dev];
+}
+
 // Long tiles the schedule keeps whole: one round of gate/up workgroups over
 // the device (after check_device on the current device).
 int max_long_tiles(const moe_layer_desc* d) {
@@ -830,7 +838,8 @@ moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const 
                   row_scale, y,        y_scales, d->n_experts, d->n,        d->k,     rows,
                   x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, s, kt); });
+  const int cus = device_cus();
+  return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, cus, s, kt); });
 }
 
 static moe_status balance_shape(int32_t T, int32_t E, int32_t k) {

@@ -138,7 +138,8 @@ struct Mx4ExpertArgs {
   int E, n, k, P, x_rows, y_rows, src_div, y_type;
   bool x_mx4, swiglu;
 };
-hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt = KTime{});
+// cus: the device's compute units.
+hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt = KTime{});
 
 // The router's balance loss (balance.hip).
 constexpr int kBalMaxParts = 256;  // partial rows of the forward pass

@@ -68,14 +68,13 @@ __device__ __forceinline__ bool mx4_find_tile(const int32_t* __restrict__ offset
   return true;
 }
 
-// Row of x that position i reads, or -1 for none.
-__device__ __forceinline__ int mx4_src(const Mx4ExpertArgs& A, int i) {
-  int r = i;
-  if (A.src_rows) {
-    r = A.src_rows[i];
-    if (r >= 0 && A.src_div > 1) r /= A.src_div;
-  }
+// Row of x for what src_rows says (or the position, where there is none), or -1 for none.
+__device__ __forceinline__ int mx4_src_of(const Mx4ExpertArgs& A, int r) {
+  if (A.src_rows && r >= 0 && A.src_div > 1) r /= A.src_div;
   return (unsigned)r < (unsigned)A.x_rows ? r : -1;
+}
+__device__ __forceinline__ int mx4_src(const Mx4ExpertArgs& A, int i) {
+  return mx4_src_of(A, A.src_rows ? A.src_rows[i] : i);
 }
 
 // Row of y that position i writes, or -1 for none.
@@ -239,8 +238,6 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // blocks past the row's end, for which the loads bring the last block again,
 // are multiplied as zeros.
 // ---------------------------------------------------------------------------
-constexpr int kKtBlocks = 8;  // blocks of a K tile
-
 // 16, 4 or 1 bytes a lane from memory to lds + lane * max(size, 4), not waited
 // for: the compiler's own form of this load makes it wait for every load in
 // flight before the next read of LDS.  m0 holds the LDS address; nothing else
@@ -262,19 +259,6 @@ __device__ __forceinline__ void wait_loads() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-// Source row, target row and factor of a tile's positions, by all threads of NW waves.
-template <int BT, int NW>
-__device__ __forceinline__ void mx4_tile_rows(const Mx4ExpertArgs& A, const MxTile& t, int* s_src, int* s_dst, float* s_fac) {
-  for (int q = threadIdx.x; q < BT; q += 64 * NW) {
-    const bool on = q < t.rows;
-    const int dst = on ? mx4_dst(A, t.row + q) : -1;
-    s_src[q] = on ? mx4_src(A, t.row + q) : -1;
-    s_dst[q] = dst;
-    s_fac[q] = A.row_scale && dst >= 0 ? A.row_scale[dst] : 1.f;
-  }
-  __syncthreads();
-}
-
 // Weight row of tile row q from column c0 of y on.  With SwiGLU blocks of 32
 // gate rows and of the same 32 up rows take turns.  Rows past the last one read
 // the last one, and (in the kernels) positions past the tile, or with no row of
@@ -285,206 +269,196 @@ __device__ __forceinline__ int64_t mx4_w_row(const Mx4ExpertArgs& A, int e, int 
   return (int64_t)e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
 }
 
-// The K loop over S stages: issue(kt, stage) starts a tile's loads (Loads
-// instructions a wave), compute(kt, stage) multiplies it.
-template <int S, int Loads, class Issue, class Compute>
-__device__ __forceinline__ void mx4_k_loop(int nkt, Issue issue, Compute compute) {
-#pragma unroll
-  for (int i = 0; i < S - 1; i++)
-    if (i < nkt) issue(i, i);
-  int stage = 0;
-  for (int kt = 0; kt < nkt; kt++) {
-    // Stage kt's loads have landed when at most those of the later stages in flight are left.
-    const int later = min(S - 2, nkt - 1 - kt);
-    if (S >= 5 && later >= 3) wait_loads<Loads * (S >= 5 ? 3 : 0)>();
-    else if (S >= 4 && later == 2) wait_loads<Loads * (S >= 4 ? 2 : 0)>();
-    else if (S >= 3 && later == 1) wait_loads<Loads * (S >= 3 ? 1 : 0)>();
-    else wait_loads<0>();
-    // Every wave's loads have landed, and every wave is done reading the stage that is filled next.
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (kt + S - 1 < nkt) issue(kt + S - 1, stage == 0 ? S - 1 : stage - 1);
-    compute(kt, stage);
-    stage = stage == S - 1 ? 0 : stage + 1;
-  }
-}
+// LDS bytes that a wave of mx4_store_tile needs for C columns, RT positions at a time.
+constexpr int mx4_store_bytes(int RT, int C) { return RT * (C * 4 + 16); }
 
-// LDS bytes that a wave of mx4_store_tile needs for C columns.
-constexpr int mx4_store_bytes(int C) { return 32 * (C * 4 + 16); }
-
-template <int BN, int BT, int WN, int WT, int S, bool Ragged>
-struct MxTileShape {
-  static constexpr int kWaves = WN * WT;
-  static constexpr int kCodeLoads = (BN + BT) / 8 / kWaves;  // of 8 rows each, a wave
-  static constexpr int kScaleRows = Ragged ? 8 : 32;         // rows of a scale load
-  static constexpr int kScaleLoads = ((BN + BT) / kScaleRows + kWaves - 1) / kWaves;
-  static constexpr int kLoads = kCodeLoads + kScaleLoads;
-  static constexpr int kScaleRow = Ragged ? 32 : 8;          // LDS bytes of a row's scales
-  static constexpr int kStage = (BN + BT) * (128 + kScaleRow);
-  static constexpr int kLds = S * kStage + BT * 12;          // and each position's src, dst, factor
-  static_assert((BN + BT) / 8 % kWaves == 0, "code loads divide among the waves");
-  static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
-  static_assert(kLoads * (S - 2) < 64, "vmcnt");
-  static_assert(mx4_store_bytes(BN / WN) * kWaves <= S * kStage, "the results pass through the stages' LDS");
+// A tile's positions in LDS.  src and dst hold what src_rows and dst_rows say
+// (or nothing, where the position itself is meant), fac row_scale's value.
+template <int BT>
+struct MxRows {
+  int src[BT], dst[BT];
+  float fac[BT];
 };
 
 // A wave's FN x FT results to y: C columns from c0 on (with SwiGLU gate and up
-// blocks take turns), tile positions from q0 on.  A lane holds one position and
-// 4 consecutive columns at a time, so its own stores would be 8 or 16 bytes a
-// row; 32 positions at a time go through `buf`, LDS of the wave's own, and out
-// as whole rows of C columns.  (Element by element from the registers, the
-// stores took 210 of 355 us at 4096 x 8192 x 8192 with bf16 results.)
-template <int FN, int FT, bool Swiglu>
-__device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, const f32x16_t (&acc)[FN][FT], int n_out, int c0,
-                                               const int* s_src, const int* s_dst, const float* s_fac, int q0,
-                                               uint8_t* buf) {
+// blocks take turns), tile positions from q0 on of the `rows` from `row` on.  A
+// lane holds one position and 4 consecutive columns at a time, so its own
+// stores would be 8 or 16 bytes a row; RT positions at a time go through `buf`,
+// LDS of the wave's own, and out as whole rows of C columns.  (Element by
+// element from the registers, the stores took 210 of 355 us at
+// 4096 x 8192 x 8192 with bf16 results.)
+template <int FN, int FT, int RT, int BT, bool Swiglu>
+__device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t (&acc)[FN][FT], int n_out, int c0,
+                                               const MxRows<BT>& R, int row, int rows, int q0, uint8_t* buf) {
   constexpr int FO = Swiglu ? FN / 2 : FN, C = FO * 32;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
   // 16-byte stores where every row of y starts at a multiple of 16 bytes.
   const bool f32 = A.y_type == kMxTypeF32;
   const bool wide = n_out % (f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 15) == 0;
+  auto target = [&](int q) {
+    const int d = A.dst_rows ? R.dst[q] : row + q;
+    return q < rows && (unsigned)d < (unsigned)A.y_rows ? d : -1;
+  };
 #pragma unroll
   for (int j = 0; j < FT; j++) {
     const int q = q0 + j * 32 + r;
-    const bool zero = s_src[q] < 0;
-    const int dst = s_dst[q];
-    const float w = s_fac[q];
+    const bool zero = mx4_src_of(A, A.src_rows ? R.src[q] : row + q) < 0;
+    const int dst = target(q);
+    const float w = A.row_scale ? R.fac[q] : 1.f;
 #pragma unroll
-    for (int i = 0; i < FO; i++) {
-      float v[16];  // element 4 g + l is column 8 g + 4 h + l of the block
+    for (int i = 0; i < FO; i++)
 #pragma unroll
       for (int l = 0; l < 16; l++) {
         const float z = acc[Swiglu ? 2 * i : i][j][l];
-        v[l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[Swiglu ? 2 * i + 1 : i][j][l]) : z) * w;
+        acc[i][j][l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[Swiglu ? 2 * i + 1 : i][j][l]) : z) * w;
       }
-      if (A.y_type == kMxTypeMx4) {
-        uint32_t m = 0;
 #pragma unroll
-        for (int l = 0; l < 16; l++) m = max(m, f32_abs_bits(v[l]));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-        const int s = mx4_scale_byte(m);
-        const float inv = mx4_inv_scale(s);
-        // Half h has the 16-bit pieces h, 2 + h, 4 + h, 6 + h of the block's 8; it keeps those of its
-        // own 8 bytes and gets the others from the other half.
-        const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
-        const uint32_t own = h ? d1 : d0, got = (uint32_t)__shfl_xor((int)(h ? d0 : d1), 32);
-        const uint32_t lo = h ? got : own, hi = h ? own : got;
-        if (dst >= 0 && c0 + i * 32 < n_out) {
-          const int64_t block = (int64_t)dst * (n_out >> 5) + ((c0 + i * 32) >> 5);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes + 8 * h) =
-              make_uint2((lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u));
-          if (h == 0) A.y_scales[block] = (uint8_t)s;
+    for (int half = 0; half < 32 / RT; half++) {
+      const bool turn = RT == 32 || r / RT == half;  // the lanes whose position passes through buf
+#pragma unroll
+      for (int i = 0; i < FO; i++) {
+        const f32x16_t& f = acc[i][j];  // element 4 g + l is column 8 g + 4 h + l of the block
+        if (A.y_type == kMxTypeMx4) {
+          if (half > 0) continue;
+          float v[16];
+#pragma unroll
+          for (int l = 0; l < 16; l++) v[l] = f[l];
+          uint32_t m = 0;
+#pragma unroll
+          for (int l = 0; l < 16; l++) m = max(m, f32_abs_bits(v[l]));
+          m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+          const int s = mx4_scale_byte(m);
+          const float inv = mx4_inv_scale(s);
+          // Half h has the 16-bit pieces h, 2 + h, 4 + h, 6 + h of the block's 8; it keeps those of its
+          // own 8 bytes and gets the others from the other half.
+          const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
+          const uint32_t own = h ? d1 : d0, got = (uint32_t)__shfl_xor((int)(h ? d0 : d1), 32);
+          const uint32_t lo = h ? got : own, hi = h ? own : got;
+          if (dst >= 0 && c0 + i * 32 < n_out) {
+            const int64_t block = (int64_t)dst * (n_out >> 5) + ((c0 + i * 32) >> 5);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes + 8 * h) =
+                make_uint2((lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u));
+            if (h == 0) A.y_scales[block] = (uint8_t)s;
+          }
+        } else if (!turn) {
+        } else if (f32) {
+#pragma unroll
+          for (int g = 0; g < 4; g++)
+            *reinterpret_cast<float4*>(buf + r % RT * (C * 4 + 16) + (i * 32 + 8 * g + 4 * h) * 4) =
+                make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
+        } else {
+#pragma unroll
+          for (int g = 0; g < 4; g++)
+            *reinterpret_cast<uint2*>(buf + r % RT * (C * 2 + 16) + (i * 32 + 8 * g + 4 * h) * 2) =
+                make_uint2(f32_to_bf16_bits(f[4 * g]) | f32_to_bf16_bits(f[4 * g + 1]) << 16,
+                           f32_to_bf16_bits(f[4 * g + 2]) | f32_to_bf16_bits(f[4 * g + 3]) << 16);
         }
-      } else if (f32) {
-#pragma unroll
-        for (int g = 0; g < 4; g++)
-          *reinterpret_cast<float4*>(buf + r * (C * 4 + 16) + (i * 32 + 8 * g + 4 * h) * 4) =
-              make_float4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
-      } else {
-#pragma unroll
-        for (int g = 0; g < 4; g++)
-          *reinterpret_cast<uint2*>(buf + r * (C * 2 + 16) + (i * 32 + 8 * g + 4 * h) * 2) =
-              make_uint2(f32_to_bf16_bits(v[4 * g]) | f32_to_bf16_bits(v[4 * g + 1]) << 16,
-                         f32_to_bf16_bits(v[4 * g + 2]) | f32_to_bf16_bits(v[4 * g + 3]) << 16);
       }
+      if (A.y_type == kMxTypeMx4) continue;
+      // The wave's lanes exchange through LDS: writes before reads, and reads before the next round's writes.
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int qr = q0 + j * 32 + half * RT;
+      auto out = [&](auto size_c) {
+        constexpr int size = size_c.value, stride = C * size + 16, per = C * size / 16;  // lanes a row
+        if (wide) {
+#pragma unroll
+          for (int p = 0; p < (RT * per + 63) / 64; p++) {
+            const int rr = p * (64 / per) + lane / per, piece = lane % per, c = c0 + piece * (16 / size);
+            if (rr >= RT) continue;
+            const uint4 d = *reinterpret_cast<const uint4*>(buf + rr * stride + piece * 16);
+            const int to = target(qr + rr);
+            if (to >= 0 && c < n_out)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + ((int64_t)to * n_out + c) * size) = d;
+          }
+        } else {
+          for (int e = lane; e < RT * C; e += 64) {
+            const int rr = e / C, col = e % C, c = c0 + col, to = target(qr + rr);
+            if (to < 0 || c >= n_out) continue;
+            const int64_t at = (int64_t)to * n_out + c;
+            if constexpr (size == 4)
+              static_cast<float*>(A.y)[at] = *reinterpret_cast<const float*>(buf + rr * stride + col * 4);
+            else
+              static_cast<uint16_t*>(A.y)[at] = *reinterpret_cast<const uint16_t*>(buf + rr * stride + col * 2);
+          }
+        }
+      };
+      if (f32) out(std::integral_constant<int, 4>{});
+      else out(std::integral_constant<int, 2>{});
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
-    if (A.y_type == kMxTypeMx4) continue;
-    // The wave's lanes exchange through LDS: writes before reads, and reads before the next round's writes.
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    auto rows = [&](auto size_c) {
-      constexpr int size = size_c.value, stride = C * size + 16, per = C * size / 16;  // lanes a row
-      if (wide) {
-#pragma unroll
-        for (int p = 0; p < 32 * per / 64; p++) {
-          const int row = p * (64 / per) + lane / per, piece = lane % per, c = c0 + piece * (16 / size);
-          const uint4 d = *reinterpret_cast<const uint4*>(buf + row * stride + piece * 16);
-          const int to = s_dst[q0 + j * 32 + row];
-          if (to >= 0 && c < n_out)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + ((int64_t)to * n_out + c) * size) = d;
-        }
-      } else {
-        for (int e = lane; e < 32 * C; e += 64) {
-          const int row = e / C, col = e % C, c = c0 + col, to = s_dst[q0 + j * 32 + row];
-          if (to < 0 || c >= n_out) continue;
-          const int64_t at = (int64_t)to * n_out + c;
-          if constexpr (size == 4)
-            static_cast<float*>(A.y)[at] = *reinterpret_cast<const float*>(buf + row * stride + col * 4);
-          else
-            static_cast<uint16_t*>(A.y)[at] = *reinterpret_cast<const uint16_t*>(buf + row * stride + col * 2);
-        }
-      }
-    };
-    if (f32) rows(std::integral_constant<int, 4>{});
-    else rows(std::integral_constant<int, 2>{});
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
-__global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A) {
-  using Sh = MxTileShape<BN, BT, WN, WT, S, Ragged>;
-  constexpr int FN = BN / 32 / WN, FT = BT / 32 / WT, NW = WN * WT;
-  constexpr int kCols = Swiglu ? BN / 2 : BN;  // columns of y
-  static_assert(!Swiglu || FN % 2 == 0, "gate and up blocks go in pairs");
-  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
-  int* s_src = reinterpret_cast<int*>(sm + S * Sh::kStage);
-  int* s_dst = s_src + BT;
-  float* s_fac = reinterpret_cast<float*>(s_dst + BT);
-  const int n_out = Swiglu ? A.n >> 1 : A.n;
-  const int cols = (n_out + kCols - 1) / kCols;
-  const int tile = blockIdx.x / cols, c0 = (blockIdx.x - tile * cols) * kCols;
-  MxTile t;
-  if (!mx4_find_tile<BT>(A.offsets, A.E, A.P, tile, &t)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wn = wave % WN, wt = wave / WN;
-  const int r = lane & 31, h = lane >> 5;
-  const int nb = A.k >> 5, nkt = (nb + kKtBlocks - 1) / kKtBlocks;
+// ---- the operands of a tile, 4-bit x -------------------------------------------
+template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged>
+struct MxOp4 {
+  static constexpr int BN = BN_, BT = BT_, WN = WN_, WT = WT_;
+  static constexpr bool Swiglu = Swiglu_;
+  static constexpr int NW = WN * WT, FN = BN / 32 / WN, FT = BT / 32 / WT;
+  static constexpr int kBlocks = 8;                          // of a K tile
+  static constexpr int kCodeLoads = (BN + BT) / 8 / NW;      // of 8 rows each, a wave
+  static constexpr int kScaleRows = Ragged ? 8 : 32;         // rows of a scale load
+  static constexpr int kScaleLoads = ((BN + BT) / kScaleRows + NW - 1) / NW;
+  static constexpr int kLoads = kCodeLoads + kScaleLoads;
+  static constexpr int kScaleRow = Ragged ? 32 : 8;          // LDS bytes of a row's scales
+  static constexpr int kStage = (BN + BT) * (128 + kScaleRow);
+  static_assert((BN + BT) / 8 % NW == 0, "code loads divide among the waves");
 
-  mx4_tile_rows<BT, NW>(A, t, s_src, s_dst, s_fac);
+  const uint8_t* code_p[kCodeLoads];
+  const uint8_t* scale_p[kScaleLoads];
+  int wave, lane, nb;
 
-  auto w_row = [&](int q) -> int64_t { return mx4_w_row<Swiglu>(A, t.e, n_out, c0, q); };
-  const uint8_t* code_p[Sh::kCodeLoads];
-  const uint8_t* scale_p[Sh::kScaleLoads];
-#pragma unroll
-  for (int j = 0; j < Sh::kCodeLoads; j++) {
-    const int q = (wave + NW * j) * 8 + (lane >> 3);
-    code_p[j] = (q < BN ? A.w_codes + w_row(q) * nb * kMxBlockBytes
-                        : static_cast<const uint8_t*>(A.x) + (int64_t)max(s_src[q - BN], 0) * nb * kMxBlockBytes);
-  }
   // Where the scale loads do not divide among the waves, the last ones are made twice.
-  auto scale_load = [&](int j) { return min(wave + NW * j, (BN + BT) / Sh::kScaleRows - 1); };
+  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, (BN + BT) / kScaleRows - 1); }
+
+  __device__ __forceinline__ void set_w(const Mx4ExpertArgs& A, int e, int n_out, int c0) {
 #pragma unroll
-  for (int j = 0; j < Sh::kScaleLoads; j++) {
-    const int q = scale_load(j) * Sh::kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
-    scale_p[j] = q < BN ? A.w_scales + w_row(q) * nb : A.x_scales + (int64_t)max(s_src[q - BN], 0) * nb;
+    for (int j = 0; j < kCodeLoads; j++) {
+      const int q = (wave + NW * j) * 8 + (lane >> 3);
+      if ((wave + NW * j) * 8 < BN) code_p[j] = A.w_codes + mx4_w_row<Swiglu>(A, e, n_out, c0, q) * nb * kMxBlockBytes;
+    }
+#pragma unroll
+    for (int j = 0; j < kScaleLoads; j++) {
+      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
+      if (scale_load(j) * kScaleRows < BN) scale_p[j] = A.w_scales + mx4_w_row<Swiglu>(A, e, n_out, c0, q) * nb;
+    }
   }
-  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
-  auto issue = [&](int kt, int stage) {
-    const uint32_t base = lds0 + stage * Sh::kStage;
-    int cb = kt * kKtBlocks + ((lane & 7) ^ (lane >> 3));
-    int so = kt * kKtBlocks + (Ragged ? lane & 7 : (lane & 1) * 4);
+  template <class Src>
+  __device__ __forceinline__ void set_x(const Mx4ExpertArgs& A, Src src) {
+#pragma unroll
+    for (int j = 0; j < kCodeLoads; j++) {
+      const int q = (wave + NW * j) * 8 + (lane >> 3);
+      if ((wave + NW * j) * 8 >= BN)
+        code_p[j] = static_cast<const uint8_t*>(A.x) + (int64_t)max(src(q - BN), 0) * nb * kMxBlockBytes;
+    }
+#pragma unroll
+    for (int j = 0; j < kScaleLoads; j++) {
+      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
+      if (scale_load(j) * kScaleRows >= BN) scale_p[j] = A.x_scales + (int64_t)max(src(q - BN), 0) * nb;
+    }
+  }
+  __device__ __forceinline__ void issue(int kt, uint32_t base) const {
+    int cb = kt * kBlocks + ((lane & 7) ^ (lane >> 3));
+    int so = kt * kBlocks + (Ragged ? lane & 7 : (lane & 1) * 4);
     if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
 #pragma unroll
-    for (int j = 0; j < Sh::kCodeLoads; j++)
-      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+    for (int j = 0; j < kCodeLoads; j++) load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
 #pragma unroll
-    for (int j = 0; j < Sh::kScaleLoads; j++)
+    for (int j = 0; j < kScaleLoads; j++)
       load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + (BN + BT) * 128 + scale_load(j) * 256);
-  };
-
-  f32x16_t acc[FN][FT] = {};
-  struct Frags {
-    uint4 w[FN], x[FT];
-    uint32_t ws[FN], xs[FT];
-  };
-  auto compute = [&](int kt, int stage) {
-    const uint8_t* wl = sm + stage * Sh::kStage + (wn * FN * 32 + r) * 128;
-    const uint8_t* xl = sm + stage * Sh::kStage + (BN + wt * FT * 32 + r) * 128;
-    const uint8_t* ss = sm + stage * Sh::kStage + (BN + BT) * 128;
-    const uint8_t* sw = ss + (wn * FN * 32 + r) * Sh::kScaleRow + h * (Sh::kScaleRow / 2);
-    const uint8_t* sx = ss + (BN + wt * FT * 32 + r) * Sh::kScaleRow + h * (Sh::kScaleRow / 2);
-    Frags a, b;
+  }
+  __device__ __forceinline__ void compute(int kt, const uint8_t* st, int wn, int wt, f32x16_t (&acc)[FN][FT]) const {
+    const int r = lane & 31, h = lane >> 5;
+    const uint8_t* wl = st + (wn * FN * 32 + r) * 128;
+    const uint8_t* xl = st + (BN + wt * FT * 32 + r) * 128;
+    const uint8_t* sw = st + (BN + BT) * 128 + (wn * FN * 32 + r) * kScaleRow + h * (kScaleRow / 2);
+    const uint8_t* sx = st + (BN + BT) * 128 + (BN + wt * FT * 32 + r) * kScaleRow + h * (kScaleRow / 2);
+    struct Frags {
+      uint4 w[FN], x[FT];
+      uint32_t ws[FN], xs[FT];
+    } a, b;
     auto load = [&](auto sc, Frags& d) {
       constexpr int s = sc.value;
       const int slot = ((4 * h + s) ^ (r & 7)) * 16;
@@ -496,16 +470,16 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A)
       if (Ragged || s == 0) {
 #pragma unroll
         for (int f = 0; f < FN; f++)
-          d.ws[f] = *reinterpret_cast<const uint32_t*>(sw + f * 32 * Sh::kScaleRow + (Ragged ? s * 4 : 0));
+          d.ws[f] = *reinterpret_cast<const uint32_t*>(sw + f * 32 * kScaleRow + (Ragged ? s * 4 : 0));
 #pragma unroll
         for (int f = 0; f < FT; f++)
-          d.xs[f] = *reinterpret_cast<const uint32_t*>(sx + f * 32 * Sh::kScaleRow + (Ragged ? s * 4 : 0));
+          d.xs[f] = *reinterpret_cast<const uint32_t*>(sx + f * 32 * kScaleRow + (Ragged ? s * 4 : 0));
       }
     };
     auto mul = [&](auto sc, Frags& d, const Frags& sd) {
       constexpr int s = sc.value;
       uint32_t ws[FN], xs[FT];
-      const bool in = !Ragged || kt * kKtBlocks + 4 * h + s < nb;
+      const bool in = !Ragged || kt * kBlocks + 4 * h + s < nb;
 #pragma unroll
       for (int f = 0; f < FN; f++) ws[f] = in ? sd.ws[f] : 0x7Fu;
 #pragma unroll
@@ -530,134 +504,83 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile(Mx4ExpertArgs A)
     load(s1, b);
     mul(s0, a, a);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (Ragged) {
-      load(s2, a);
-      mul(s1, b, b);
-      __builtin_amdgcn_sched_barrier(0);
-      load(s3, b);
-      mul(s2, a, a);
-      __builtin_amdgcn_sched_barrier(0);
-      mul(s3, b, b);
-    } else {
-      load(s2, a);  // leaves the scales
-      mul(s1, b, a);
-      __builtin_amdgcn_sched_barrier(0);
-      load(s3, b);
-      mul(s2, a, a);
-      __builtin_amdgcn_sched_barrier(0);
-      mul(s3, b, a);
-    }
-  };
+    load(s2, a);  // leaves the scales of step 0, but for a ragged tile
+    mul(s1, b, Ragged ? b : a);
+    __builtin_amdgcn_sched_barrier(0);
+    load(s3, b);
+    mul(s2, a, a);
+    __builtin_amdgcn_sched_barrier(0);
+    mul(s3, b, Ragged ? b : a);
+  }
+};
 
-  mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
-  __syncthreads();  // the stages are free
-  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32,
-                                 sm + wave * mx4_store_bytes(kCols / WN));
-}
-
-// ---------------------------------------------------------------------------
-// Many rows an expert, bf16 x: the same tiles with K tiles of 128 columns (64
-// bytes of codes and 256 bytes of x a row).  A wave reads its weight codes from
-// LDS, converts them to bf16 (exactly, two a conversion) and multiplies with
-// the 32x32x16 instruction; each conversion serves FT instructions.
-//
-// LDS.  x: 16-byte piece c of a row at slot (c ^ row % 8).  Codes: block b at
-// slot (b ^ (row / 4) % 4), 4 blocks a row.  In turn p of a tile a lane of half
-// h multiplies block 2 p + h, 8 columns at a time.  Ragged (k no multiple of
-// 128, or the scales not dword aligned): as above.
-// ---------------------------------------------------------------------------
-constexpr int kBtBlocks = 4;  // blocks of a K tile
-
-template <int BN, int BT, int WN, int WT, int S, bool Ragged>
-struct MxBfShape {
-  static constexpr int kWaves = WN * WT;
-  static constexpr int kCodeLoads = BN / 16 / kWaves;  // of 16 rows each, a wave
-  static constexpr int kXLoads = BT / 4 / kWaves;      // of 4 rows each
-  static constexpr int kScaleRows = Ragged ? 16 : 64;  // rows of a scale load
-  static constexpr int kScaleLoads = (BN / kScaleRows + kWaves - 1) / kWaves;
+// ---- the operands of a tile, bf16 x ----------------------------------------------
+template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged>
+struct MxOp16 {
+  static constexpr int BN = BN_, BT = BT_, WN = WN_, WT = WT_;
+  static constexpr bool Swiglu = Swiglu_;
+  static constexpr int NW = WN * WT, FN = BN / 32 / WN, FT = BT / 32 / WT;
+  static constexpr int kBlocks = 4;                   // of a K tile
+  static constexpr int kCodeLoads = BN / 16 / NW;     // of 16 rows each, a wave
+  static constexpr int kXLoads = BT / 4 / NW;         // of 4 rows each
+  static constexpr int kScaleRows = Ragged ? 16 : 64; // rows of a scale load
+  static constexpr int kScaleLoads = (BN / kScaleRows + NW - 1) / NW;
   static constexpr int kLoads = kCodeLoads + kXLoads + kScaleLoads;
   static constexpr int kScaleRow = Ragged ? 16 : 4;
   static constexpr int kStage = BN * (64 + kScaleRow) + BT * 256;
-  static constexpr int kLds = S * kStage + BT * 12;
-  static_assert(BN / 16 % kWaves == 0 && BT / 4 % kWaves == 0, "loads divide among the waves");
-  static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
-  static_assert(kLoads * (S - 2) < 64, "vmcnt");
-  static_assert(mx4_store_bytes(BN / WN) * kWaves <= S * kStage, "the results pass through the stages' LDS");
-};
+  static_assert(BN / 16 % NW == 0 && BT / 4 % NW == 0, "loads divide among the waves");
 
-template <int BN, int BT, int WN, int WT, int S, int Occ, bool Swiglu, bool Ragged>
-__global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile_bf16(Mx4ExpertArgs A) {
-  using Sh = MxBfShape<BN, BT, WN, WT, S, Ragged>;
-  constexpr int FN = BN / 32 / WN, FT = BT / 32 / WT, NW = WN * WT;
-  constexpr int kCols = Swiglu ? BN / 2 : BN;  // columns of y
-  static_assert(!Swiglu || FN % 2 == 0, "gate and up blocks go in pairs");
-  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
-  int* s_src = reinterpret_cast<int*>(sm + S * Sh::kStage);
-  int* s_dst = s_src + BT;
-  float* s_fac = reinterpret_cast<float*>(s_dst + BT);
-  const int n_out = Swiglu ? A.n >> 1 : A.n;
-  const int cols = (n_out + kCols - 1) / kCols;
-  const int tile = blockIdx.x / cols, c0 = (blockIdx.x - tile * cols) * kCols;
-  MxTile t;
-  if (!mx4_find_tile<BT>(A.offsets, A.E, A.P, tile, &t)) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wn = wave % WN, wt = wave / WN;
-  const int r = lane & 31, h = lane >> 5;
-  const int nb = A.k >> 5, nkt = (nb + kBtBlocks - 1) / kBtBlocks;
+  const uint8_t *code_p[kCodeLoads], *x_p[kXLoads], *scale_p[kScaleLoads];
+  int wave, lane, nb;
 
-  mx4_tile_rows<BT, NW>(A, t, s_src, s_dst, s_fac);
+  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, BN / kScaleRows - 1); }
 
-  auto w_row = [&](int q) -> int64_t { return mx4_w_row<Swiglu>(A, t.e, n_out, c0, q); };
-  const uint8_t *code_p[Sh::kCodeLoads], *x_p[Sh::kXLoads], *scale_p[Sh::kScaleLoads];
+  __device__ __forceinline__ void set_w(const Mx4ExpertArgs& A, int e, int n_out, int c0) {
 #pragma unroll
-  for (int j = 0; j < Sh::kCodeLoads; j++)
-    code_p[j] = A.w_codes + w_row((wave + NW * j) * 16 + (lane >> 2)) * nb * kMxBlockBytes;
+    for (int j = 0; j < kCodeLoads; j++)
+      code_p[j] = A.w_codes + mx4_w_row<Swiglu>(A, e, n_out, c0, (wave + NW * j) * 16 + (lane >> 2)) * nb * kMxBlockBytes;
 #pragma unroll
-  for (int j = 0; j < Sh::kXLoads; j++)
-    x_p[j] = static_cast<const uint8_t*>(A.x) + (int64_t)max(s_src[(wave + NW * j) * 4 + (lane >> 4)], 0) * A.k * 2;
-  // Where the scale loads do not divide among the waves, the last ones are made twice.
-  auto scale_load = [&](int j) { return min(wave + NW * j, BN / Sh::kScaleRows - 1); };
+    for (int j = 0; j < kScaleLoads; j++)
+      scale_p[j] = A.w_scales + mx4_w_row<Swiglu>(A, e, n_out, c0, scale_load(j) * kScaleRows + (Ragged ? lane >> 2 : lane)) * nb;
+  }
+  template <class Src>
+  __device__ __forceinline__ void set_x(const Mx4ExpertArgs& A, Src src) {
 #pragma unroll
-  for (int j = 0; j < Sh::kScaleLoads; j++)
-    scale_p[j] = A.w_scales + w_row(scale_load(j) * Sh::kScaleRows + (Ragged ? lane >> 2 : lane)) * nb;
-  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
-  auto issue = [&](int kt, int stage) {
-    const uint32_t base = lds0 + stage * Sh::kStage;
-    int cb = kt * kBtBlocks + ((lane & 3) ^ ((lane >> 4) & 3));
-    // A row of x is row j of 4 in its load, and row (4 (wave + NW j) + lane / 16) % 8 of the swizzle.
-    int so = kt * kBtBlocks + (Ragged ? lane & 3 : 0);
+    for (int j = 0; j < kXLoads; j++)
+      x_p[j] = static_cast<const uint8_t*>(A.x) + (int64_t)max(src((wave + NW * j) * 4 + (lane >> 4)), 0) * A.k * 2;
+  }
+  __device__ __forceinline__ void issue(int kt, uint32_t base) const {
+    int cb = kt * kBlocks + ((lane & 3) ^ ((lane >> 4) & 3));
+    int so = kt * kBlocks + (Ragged ? lane & 3 : 0);
     if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
 #pragma unroll
-    for (int j = 0; j < Sh::kCodeLoads; j++)
-      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+    for (int j = 0; j < kCodeLoads; j++) load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
 #pragma unroll
-    for (int j = 0; j < Sh::kXLoads; j++) {
-      int c = (lane & 15) ^ ((4 * (wave + NW * j) + (lane >> 4)) & 7);
-      int xb = kt * kBtBlocks * 4 + c;
+    for (int j = 0; j < kXLoads; j++) {
+      int xb = kt * kBlocks * 4 + ((lane & 15) ^ ((4 * (wave + NW * j) + (lane >> 4)) & 7));
       if (Ragged) xb = min(xb, nb * 4 - 1);
       load_to_lds<16>(x_p[j] + xb * 16, base + BN * 64 + (wave + NW * j) * 1024);
     }
 #pragma unroll
-    for (int j = 0; j < Sh::kScaleLoads; j++)
+    for (int j = 0; j < kScaleLoads; j++)
       load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + BN * 64 + BT * 256 + scale_load(j) * 256);
-  };
-
-  f32x16_t acc[FN][FT] = {};
-  auto compute = [&](int kt, int stage) {
-    const uint8_t* wl = sm + stage * Sh::kStage + (wn * FN * 32 + r) * 64;
-    const uint8_t* xl = sm + stage * Sh::kStage + BN * 64 + (wt * FT * 32 + r) * 256;
-    const uint8_t* sl = sm + stage * Sh::kStage + BN * 64 + BT * 256 + (wn * FN * 32 + r) * Sh::kScaleRow;
+  }
+  __device__ __forceinline__ void compute(int kt, const uint8_t* st, int wn, int wt, f32x16_t (&acc)[FN][FT]) const {
+    const int r = lane & 31, h = lane >> 5;
+    const uint8_t* wl = st + (wn * FN * 32 + r) * 64;
+    const uint8_t* xl = st + BN * 64 + (wt * FT * 32 + r) * 256;
+    const uint8_t* sl = st + BN * 64 + BT * 256 + (wn * FN * 32 + r) * kScaleRow;
     struct Frags {
       uint4 w[FN], x[FT][4];
       float s[FN];
     } a, b;
     auto load = [&](int p, Frags& d) {
       const int blk = 2 * p + h;
-      const bool in = !Ragged || kt * kBtBlocks + blk < nb;
+      const bool in = !Ragged || kt * kBlocks + blk < nb;
 #pragma unroll
       for (int f = 0; f < FN; f++) {
         d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 64 + ((blk ^ ((r >> 2) & 3)) * 16));
-        uint32_t sc = *reinterpret_cast<const uint32_t*>(sl + f * 32 * Sh::kScaleRow + (Ragged ? blk * 4 : 0));
+        uint32_t sc = *reinterpret_cast<const uint32_t*>(sl + f * 32 * kScaleRow + (Ragged ? blk * 4 : 0));
         if (!Ragged) sc >>= 8 * blk;
         d.s[f] = mx4_scale_f32(in ? sc & 0xFFu : 127u);
       }
@@ -689,58 +612,248 @@ __global__ __launch_bounds__(64 * WN * WT, Occ) void k_mx4_tile_bf16(Mx4ExpertAr
     load(1, b);
     mul(a);
     mul(b);
+  }
+};
+
+// ---- the kernel ----------------------------------------------------------------------
+// Units are (tile of BT positions, BN weight rows), columns fastest.  A
+// workgroup takes a contiguous range of them, and its loads run through it
+// without a pause: while a unit's results are stored, the next unit's first K
+// tiles are on their way, and a tile's src, dst and factors are brought by the
+// same direct loads while the tile before it is worked on.  (With a workgroup a
+// unit, the chain offsets -> src -> x cost about 8 us each time: 116 and 121 us
+// for the products below where this takes ...)  Consecutive ranges share an
+// XCD, whose L2 then keeps an expert's weights for its tiles.
+template <class Op, int S>
+struct MxGrid {
+  static constexpr int kFrame = S * Op::kStage;
+  static constexpr int kRows = 3 * (int)sizeof(MxRows<Op::BT>);
+  static constexpr int kLds = kFrame + kRows + 513 * 4;
+  static constexpr int kCols = Op::Swiglu ? Op::BN / 2 : Op::BN;
+  static constexpr int kStore = Op::kStage / Op::NW;  // a wave's share of a stage
+  static constexpr int RT = mx4_store_bytes(32, kCols / Op::WN) <= kStore ? 32 : 16;
+  static_assert(mx4_store_bytes(RT, kCols / Op::WN) <= kStore, "the results pass through a stage");
+  static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
+  static_assert(Op::kLoads * (S - 2) < 64, "vmcnt");
+  static_assert(!Op::Swiglu || Op::FN % 2 == 0, "gate and up blocks go in pairs");
+};
+
+template <class Op, int S, int Occ>
+__global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) {
+  using G = MxGrid<Op, S>;
+  constexpr int BT = Op::BT, NW = Op::NW, kCols = G::kCols;
+  extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
+  auto* rows3 = reinterpret_cast<MxRows<BT>*>(sm + G::kFrame);
+  int* s_off = reinterpret_cast<int*>(sm + G::kFrame + G::kRows);
+  const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int n_out = Op::Swiglu ? A.n >> 1 : A.n, E = A.E;
+  const int cols = (n_out + kCols - 1) / kCols;
+
+  for (int i = threadIdx.x; i <= E; i += 64 * NW) s_off[i] = min(max(A.offsets[i], 0), A.P);
+  __syncthreads();
+  // Tiles: those of E / 64 consecutive experts a lane, summed over the lanes.
+  const int per = (E + 63) >> 6, e0 = lane * per;
+  auto tiles_of = [&](int e) { return (max(s_off[e + 1] - s_off[e], 0) + BT - 1) / BT; };
+  int mine = 0;
+  for (int j = 0; j < per; j++)
+    if (e0 + j < E) mine += tiles_of(e0 + j);
+  int end = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(end, d);
+    if (lane >= d) end += v;
+  }
+  const int tiles = __builtin_amdgcn_readlane(end, 63);
+  const int64_t units = (int64_t)tiles * cols;
+  // Workgroup b runs on XCD b % 8: each XCD gets consecutive ranges.
+  const int n_wg = gridDim.x, wg = (blockIdx.x & 7) * (n_wg >> 3) + (blockIdx.x >> 3);  // n_wg is a multiple of 8
+  const int64_t u0 = units * wg / n_wg, u1 = units * (wg + 1) / n_wg;
+  if (u0 >= u1) return;
+
+  // Position of a walk over the units.
+  struct Walk {
+    int e, row, hi, col, slot;  // expert, first position, its end, column tile, rows' slot
+    int tile;
   };
-  mx4_k_loop<S, Sh::kLoads>(nkt, issue, compute);
-  __syncthreads();  // the stages are free
-  mx4_store_tile<FN, FT, Swiglu>(A, acc, n_out, c0 + wn * FN * (Swiglu ? 16 : 32), s_src, s_dst, s_fac, wt * FT * 32,
-                                 sm + wave * mx4_store_bytes(kCols / WN));
+  auto next_tile = [&](Walk& w) {
+    w.tile++;
+    w.slot = w.slot == 2 ? 0 : w.slot + 1;
+    w.row += BT;
+    if (w.row < w.hi) return;
+    do w.e++;
+    while (w.e < E - 1 && s_off[w.e + 1] <= s_off[w.e]);
+    w.row = __builtin_amdgcn_readfirstlane(s_off[w.e]);
+    w.hi = __builtin_amdgcn_readfirstlane(s_off[w.e + 1]);
+  };
+  Walk in;  // the loads' walk
+  {
+    const int t0 = (int)(u0 / cols);
+    in.tile = t0;
+    in.col = (int)(u0 - (int64_t)t0 * cols);
+    in.slot = 0;
+    int first = end - mine, e = 0;
+    const int owner = __builtin_ctzll(__ballot(t0 >= first && t0 < end));
+    if (lane == owner)
+      for (e = e0; t0 >= first + tiles_of(e); e++) first += tiles_of(e);
+    in.e = __builtin_amdgcn_readlane(e, owner);
+    first = __builtin_amdgcn_readlane(first, owner);
+    in.row = __builtin_amdgcn_readfirstlane(s_off[in.e]) + (t0 - first) * BT;
+    in.hi = __builtin_amdgcn_readfirstlane(s_off[in.e + 1]);
+  }
+  const int last_tile = (int)((u1 - 1) / cols);
+
+  // Direct loads of what src_rows and dst_rows say about a tile, 64 positions a wave.
+  const uint32_t rows_lds = lds0 + G::kFrame;
+  auto load_rows = [&](const Walk& w) {
+    for (int q = wave * 64; q < BT; q += NW * 64) {
+      const int64_t at = min(w.row + q + lane, A.P - 1);
+      const uint32_t to = rows_lds + w.slot * (int)sizeof(MxRows<BT>) + q * 4;
+      if (BT % 64 == 0 || q + lane < BT) {
+        if (A.src_rows) load_to_lds<4>(A.src_rows + at, to);
+        if (A.dst_rows) load_to_lds<4>(A.dst_rows + at, to + BT * 4);
+      }
+    }
+  };
+  // The same for the factors, once the tile's dst are in LDS.
+  auto load_factors = [&](const Walk& w) {
+    if (!A.row_scale) return;
+    for (int q = wave * 64; q < BT; q += NW * 64) {
+      if (BT % 64 != 0 && q + lane >= BT) continue;
+      const int d = A.dst_rows ? rows3[w.slot].dst[q + lane] : w.row + q + lane;
+      load_to_lds<4>(A.row_scale + ((unsigned)d < (unsigned)A.y_rows ? d : 0),
+                     rows_lds + w.slot * (int)sizeof(MxRows<BT>) + (2 * BT + q) * 4);
+    }
+  };
+
+  Op op;
+  op.wave = wave;
+  op.lane = lane;
+  op.nb = A.k >> 5;
+  const int nkt = (op.nb + Op::kBlocks - 1) / Op::kBlocks;
+  const int n_it = (int)((u1 - u0) * nkt);  // nkt is at least S - 1 (launch_mx4_experts)
+  load_rows(in);
+  wait_loads<0>();
+  __syncthreads();
+  Walk out = in;  // the products' walk
+
+  int in_kt = 0, in_stage = 0;
+  bool in_new = true;
+  auto issue_next = [&] {
+    if (in_kt == 0) {
+      if (in_new) {
+        in_new = false;
+        const MxRows<BT>& R = rows3[in.slot];
+        op.set_x(A, [&](int q) { return mx4_src_of(A, A.src_rows ? R.src[q] : min(in.row + q, A.P - 1)); });
+        load_factors(in);
+        if (in.tile < last_tile) {
+          Walk w = in;
+          next_tile(w);
+          load_rows(w);
+        }
+      }
+      op.set_w(A, in.e, n_out, in.col * kCols);
+    }
+    op.issue(in_kt, lds0 + in_stage * Op::kStage);
+    in_stage = in_stage == S - 1 ? 0 : in_stage + 1;
+    if (++in_kt == nkt) {
+      in_kt = 0;
+      if (++in.col == cols) {
+        in.col = 0;
+        in_new = true;
+        if (in.tile < last_tile) next_tile(in);
+      }
+    }
+  };
+
+  const int wn = wave % Op::WN, wt = wave / Op::WN;
+  f32x16_t acc[Op::FN][Op::FT] = {};
+#pragma unroll
+  for (int i = 0; i < S - 1; i++)
+    if (i < n_it) issue_next();
+  int stage = 0, kt = 0;
+  for (int it = 0; it < n_it; it++) {
+    // The stage's loads have landed when at most those of the later stages are in flight.
+    const int later = min(S - 2, n_it - 1 - it);
+    if (S >= 4 && later >= 2) wait_loads<Op::kLoads * (S >= 4 ? 2 : 0)>();
+    else if (S >= 3 && later == 1) wait_loads<Op::kLoads * (S >= 3 ? 1 : 0)>();
+    else wait_loads<0>();
+    // Every wave's loads have landed, and every wave is done with the stage that is filled next.
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (it + S - 1 < n_it) issue_next();
+    uint8_t* st = sm + stage * Op::kStage;
+    op.compute(kt, st, wn, wt, acc);
+    if (++kt == nkt) {
+      kt = 0;
+      // Every wave is done reading this stage; the results pass through it.
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      mx4_store_tile<Op::FN, Op::FT, G::RT, BT, Op::Swiglu>(
+          A, acc, n_out, out.col * kCols + wn * (kCols / Op::WN), rows3[out.slot], out.row, min(out.hi - out.row, BT),
+          wt * Op::FT * 32, st + wave * G::kStore);
+#pragma unroll
+      for (int i = 0; i < Op::FN; i++)
+#pragma unroll
+        for (int j = 0; j < Op::FT; j++) acc[i][j] = f32x16_t{};
+      if (++out.col == cols) {
+        out.col = 0;
+        if (out.tile < last_tile) next_tile(out);
+      }
+    }
+    stage = stage == S - 1 ? 0 : stage + 1;
+  }
 }
 
 // Tiles of BT positions that E experts with P positions in all can have.
 static int64_t max_tiles(int64_t P, int64_t E, int64_t bt) { return P / bt + (E < P ? E : P); }
 
-template <int BN, int BT, int NW, bool Swiglu>
-static hipError_t launch_tile(void (*f)(Mx4ExpertArgs), int lds, std::atomic<uint64_t>& done, const Mx4ExpertArgs& A,
-                              hipStream_t s, const KTime& kt) {
-  hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), lds, done);
+// PerCu workgroups a compute unit, or as many as there may be units.
+template <class Op, int S, int PerCu>
+static hipError_t launch_grid(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+  using G = MxGrid<Op, S>;
+  auto* f = k_mx4_grid<Op, S, Op::NW * PerCu / 4>;
+  static_assert(G::kLds * PerCu <= 160 * 1024, "LDS");
+  static std::atomic<uint64_t> done{0};
+  hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), G::kLds, done);
   if (e != hipSuccess) return e;
-  const int64_t n_out = Swiglu ? A.n / 2 : A.n, kc = Swiglu ? BN / 2 : BN;
-  const int64_t grid = max_tiles(A.P, A.E, BT) * ((n_out + kc - 1) / kc);
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  MOE_LAUNCH(f, dim3((unsigned)grid), dim3(64 * NW), lds, s, kt.start, kt.stop, A);
+  const int64_t n_out = Op::Swiglu ? A.n / 2 : A.n;
+  const int64_t units = max_tiles(A.P, A.E, Op::BT) * ((n_out + G::kCols - 1) / G::kCols);
+  const int64_t most = ((int64_t)cus * PerCu + 7) / 8 * 8, want = (units + 7) / 8 * 8;
+  MOE_LAUNCH(f, dim3((unsigned)(want < most ? want : most)), dim3(64 * Op::NW), G::kLds, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
 
-// 4-bit x.
-template <int BN, int BT, int WN, int WT, int S, int Occ, bool Ragged>
-static hipError_t tile_mx4(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
-  static std::atomic<uint64_t> done[2];
-  constexpr int lds = MxTileShape<BN, BT, WN, WT, S, Ragged>::kLds;
-  return A.swiglu ? launch_tile<BN, BT, WN * WT, true>(k_mx4_tile<BN, BT, WN, WT, S, Occ, true, Ragged>, lds, done[1], A, s, kt)
-                  : launch_tile<BN, BT, WN * WT, false>(k_mx4_tile<BN, BT, WN, WT, S, Occ, false, Ragged>, lds, done[0], A, s, kt);
+// Stages: a tile has to be at least S - 1 K tiles long, so that a tile's rows are in LDS when the loads get to it,
+// and are not replaced before its results are out.
+template <int BN, int BT, int WN, int WT, int S, int PerCu, bool Ragged>
+static hipError_t tile_mx4(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+  return A.swiglu ? launch_grid<MxOp4<BN, BT, WN, WT, true, Ragged>, S, PerCu>(A, cus, s, kt)
+                  : launch_grid<MxOp4<BN, BT, WN, WT, false, Ragged>, S, PerCu>(A, cus, s, kt);
 }
 
-// bf16 x.
-template <int BN, int BT, int WN, int WT, int S, int Occ, bool Ragged>
-static hipError_t tile_bf16(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
-  static std::atomic<uint64_t> done[2];
-  constexpr int lds = MxBfShape<BN, BT, WN, WT, S, Ragged>::kLds;
-  return A.swiglu ? launch_tile<BN, BT, WN * WT, true>(k_mx4_tile_bf16<BN, BT, WN, WT, S, Occ, true, Ragged>, lds, done[1], A, s, kt)
-                  : launch_tile<BN, BT, WN * WT, false>(k_mx4_tile_bf16<BN, BT, WN, WT, S, Occ, false, Ragged>, lds, done[0], A, s, kt);
+template <int BN, int BT, int WN, int WT, int S, int PerCu, bool Ragged>
+static hipError_t tile_bf16(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+  return A.swiglu ? launch_grid<MxOp16<BN, BT, WN, WT, true, Ragged>, S, PerCu>(A, cus, s, kt)
+                  : launch_grid<MxOp16<BN, BT, WN, WT, false, Ragged>, S, PerCu>(A, cus, s, kt);
 }
 
-hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
   const int64_t n_out = A.swiglu ? A.n / 2 : A.n, avg = A.P / A.E;
   const bool dwords = ((reinterpret_cast<uintptr_t>(A.w_scales) | reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 3) == 0;
   if (A.x_mx4 && avg >= 64) {
-    if (!dwords || A.k % 256) return tile_mx4<256, 128, 2, 2, 2, 1, true>(A, s, kt);
-    if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 2, false>(A, s, kt);
-    return tile_mx4<256, 128, 2, 2, 3, 1, false>(A, s, kt);
+    if (!dwords || A.k % 256) return tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
+    if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
+    if (A.k <= 256) return tile_mx4<256, 128, 4, 2, 2, 1, false>(A, cus, s, kt);
+    return tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
   }
   if (!A.x_mx4 && avg >= 12) {
-    const bool ragged = !dwords || A.k % 128;
-    if (avg >= 64) return ragged ? tile_bf16<256, 128, 4, 2, 2, 2, true>(A, s, kt) : tile_bf16<256, 128, 4, 2, 3, 2, false>(A, s, kt);
-    return ragged ? tile_bf16<256, 32, 4, 1, 3, 2, true>(A, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, s, kt);
+    const bool ragged = !dwords || A.k % 128, two = A.k <= 128;
+    if (avg >= 64)
+      return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt)
+             : two  ? tile_bf16<256, 128, 4, 2, 2, 1, false>(A, cus, s, kt)
+                    : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt)
+           : two  ? tile_bf16<256, 32, 4, 1, 2, 2, false>(A, cus, s, kt)
+                  : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
   }
   const int64_t grid = max_tiles(A.P, A.E, 16) * ((n_out + kFewCols - 1) / kFewCols);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
