@@ -269,9 +269,6 @@ __device__ __forceinline__ int64_t mx4_w_row(const Mx4ExpertArgs& A, int e, int 
   return (int64_t)e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
 }
 
-// LDS bytes that a wave of mx4_store_tile needs for C columns, RT positions at a time.
-constexpr int mx4_store_bytes(int RT, int C) { return RT * (C * 4 + 16); }
-
 // A tile's positions in LDS.  src and dst hold what src_rows and dst_rows say
 // (or nothing, where the position itself is meant), fac row_scale's value.
 template <int BT>
@@ -284,17 +281,14 @@ struct MxRows {
 // blocks take turns), tile positions from q0 on of the `rows` from `row` on.  A
 // lane holds one position and 4 consecutive columns at a time, so its own
 // stores would be 8 or 16 bytes a row; RT positions at a time go through `buf`,
-// LDS of the wave's own, and out as whole rows of C columns.  (Element by
-// element from the registers, the stores took 210 of 355 us at
+// Store bytes of LDS of the wave's own, and out as whole rows of C columns.
+// (Element by element from the registers, the stores took 210 of 355 us at
 // 4096 x 8192 x 8192 with bf16 results.)
-template <int FN, int FT, int RT, int BT, bool Swiglu>
+template <int YT, int FN, int FT, int Store, int BT, bool Swiglu>
 __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t (&acc)[FN][FT], int n_out, int c0,
                                                const MxRows<BT>& R, int row, int rows, int q0, uint8_t* buf) {
   constexpr int FO = Swiglu ? FN / 2 : FN, C = FO * 32;
   const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
-  // 16-byte stores where every row of y starts at a multiple of 16 bytes.
-  const bool f32 = A.y_type == kMxTypeF32;
-  const bool wide = n_out % (f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 15) == 0;
   auto target = [&](int q) {
     const int d = A.dst_rows ? R.dst[q] : row + q;
     return q < rows && (unsigned)d < (unsigned)A.y_rows ? d : -1;
@@ -303,7 +297,6 @@ __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t 
   for (int j = 0; j < FT; j++) {
     const int q = q0 + j * 32 + r;
     const bool zero = mx4_src_of(A, A.src_rows ? R.src[q] : row + q) < 0;
-    const int dst = target(q);
     const float w = A.row_scale ? R.fac[q] : 1.f;
 #pragma unroll
     for (int i = 0; i < FO; i++)
@@ -312,82 +305,92 @@ __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t 
         const float z = acc[Swiglu ? 2 * i : i][j][l];
         acc[i][j][l] = zero ? 0.f : (Swiglu ? silu_mul(z, acc[Swiglu ? 2 * i + 1 : i][j][l]) : z) * w;
       }
+  }
+  // Element 4 g + l of a block is column 8 g + 4 h + l.
+  if constexpr (YT == kMxTypeMx4) {
 #pragma unroll
-    for (int half = 0; half < 32 / RT; half++) {
-      const bool turn = RT == 32 || r / RT == half;  // the lanes whose position passes through buf
+    for (int j = 0; j < FT; j++) {
+      const int dst = target(q0 + j * 32 + r);
 #pragma unroll
       for (int i = 0; i < FO; i++) {
-        const f32x16_t& f = acc[i][j];  // element 4 g + l is column 8 g + 4 h + l of the block
-        if (A.y_type == kMxTypeMx4) {
-          if (half > 0) continue;
-          float v[16];
+        float v[16];
+        uint32_t m = 0;
 #pragma unroll
-          for (int l = 0; l < 16; l++) v[l] = f[l];
-          uint32_t m = 0;
-#pragma unroll
-          for (int l = 0; l < 16; l++) m = max(m, f32_abs_bits(v[l]));
-          m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-          const int s = mx4_scale_byte(m);
-          const float inv = mx4_inv_scale(s);
-          // Half h has the 16-bit pieces h, 2 + h, 4 + h, 6 + h of the block's 8; it keeps those of its
-          // own 8 bytes and gets the others from the other half.
-          const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
-          const uint32_t own = h ? d1 : d0, got = (uint32_t)__shfl_xor((int)(h ? d0 : d1), 32);
-          const uint32_t lo = h ? got : own, hi = h ? own : got;
-          if (dst >= 0 && c0 + i * 32 < n_out) {
-            const int64_t block = (int64_t)dst * (n_out >> 5) + ((c0 + i * 32) >> 5);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes + 8 * h) =
-                make_uint2((lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u));
-            if (h == 0) A.y_scales[block] = (uint8_t)s;
-          }
-        } else if (!turn) {
-        } else if (f32) {
-#pragma unroll
-          for (int g = 0; g < 4; g++)
-            *reinterpret_cast<float4*>(buf + r % RT * (C * 4 + 16) + (i * 32 + 8 * g + 4 * h) * 4) =
-                make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]);
-        } else {
-#pragma unroll
-          for (int g = 0; g < 4; g++)
-            *reinterpret_cast<uint2*>(buf + r % RT * (C * 2 + 16) + (i * 32 + 8 * g + 4 * h) * 2) =
-                make_uint2(f32_to_bf16_bits(f[4 * g]) | f32_to_bf16_bits(f[4 * g + 1]) << 16,
-                           f32_to_bf16_bits(f[4 * g + 2]) | f32_to_bf16_bits(f[4 * g + 3]) << 16);
+        for (int l = 0; l < 16; l++) v[l] = acc[i][j][l], m = max(m, f32_abs_bits(v[l]));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+        const int s = mx4_scale_byte(m);
+        const float inv = mx4_inv_scale(s);
+        // Half h has the 16-bit pieces h, 2 + h, 4 + h, 6 + h of the block's 8; it keeps those of its
+        // own 8 bytes and gets the others from the other half.
+        const uint32_t d0 = mx4_pack8(v, inv), d1 = mx4_pack8(v + 8, inv);
+        const uint32_t own = h ? d1 : d0, got = (uint32_t)__shfl_xor((int)(h ? d0 : d1), 32);
+        const uint32_t lo = h ? got : own, hi = h ? own : got;
+        if (dst >= 0 && c0 + i * 32 < n_out) {
+          const int64_t block = (int64_t)dst * (n_out >> 5) + ((c0 + i * 32) >> 5);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(A.y) + block * kMxBlockBytes + 8 * h) =
+              make_uint2((lo & 0xFFFFu) | hi << 16, lo >> 16 | (hi & 0xFFFF0000u));
+          if (h == 0) A.y_scales[block] = (uint8_t)s;
         }
       }
-      if (A.y_type == kMxTypeMx4) continue;
-      // The wave's lanes exchange through LDS: writes before reads, and reads before the next round's writes.
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      const int qr = q0 + j * 32 + half * RT;
-      auto out = [&](auto size_c) {
-        constexpr int size = size_c.value, stride = C * size + 16, per = C * size / 16;  // lanes a row
-        if (wide) {
+    }
+  } else {
+    constexpr int size = YT == kMxTypeF32 ? 4 : 2, stride = C * size + 16;
+    constexpr int RT = 32 * stride <= Store ? 32 : 16;
+    static_assert(RT * stride <= Store, "the results pass through a stage");
+    constexpr int per = C * size / 16, kPass = RT * per / 64;  // lanes a row; instructions for RT rows
+    static_assert(RT * per % 64 == 0, "whole instructions");
+    // 16-byte stores where every row of y starts at a multiple of 16 bytes.
+    const bool wide = n_out % (16 / size) == 0 && (reinterpret_cast<uintptr_t>(A.y) & 15) == 0;
+    const int piece = lane % per, c = c0 + piece * (16 / size);
 #pragma unroll
-          for (int p = 0; p < (RT * per + 63) / 64; p++) {
-            const int rr = p * (64 / per) + lane / per, piece = lane % per, c = c0 + piece * (16 / size);
-            if (rr >= RT) continue;
-            const uint4 d = *reinterpret_cast<const uint4*>(buf + rr * stride + piece * 16);
-            const int to = target(qr + rr);
-            if (to >= 0 && c < n_out)
-              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + ((int64_t)to * n_out + c) * size) = d;
-          }
+    for (int j = 0; j < FT; j++)
+#pragma unroll
+      for (int half = 0; half < 32 / RT; half++) {
+        const int qr = q0 + j * 32 + half * RT;
+        int to[kPass];
+#pragma unroll
+        for (int p = 0; p < kPass; p++) to[p] = target(qr + p * (64 / per) + lane / per);
+        if (RT == 32 || r / RT == half) {  // the lanes whose position passes through buf
+#pragma unroll
+          for (int i = 0; i < FO; i++)
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+              const float v0 = acc[i][j][4 * g], v1 = acc[i][j][4 * g + 1], v2 = acc[i][j][4 * g + 2], v3 = acc[i][j][4 * g + 3];
+              uint8_t* at = buf + r % RT * stride + (i * 32 + 8 * g + 4 * h) * size;
+              if constexpr (size == 4) {
+                *reinterpret_cast<float4*>(at) = make_float4(v0, v1, v2, v3);
+              } else {
+                const bf16x2_t lo = {(__bf16)v0, (__bf16)v1}, hi = {(__bf16)v2, (__bf16)v3};
+                *reinterpret_cast<uint2*>(at) = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+              }
+            }
+        }
+        // The wave's lanes exchange through LDS: writes before reads, and reads before the next round's writes.
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (wide) {
+          uint4 d[kPass];
+#pragma unroll
+          for (int p = 0; p < kPass; p++)
+            d[p] = *reinterpret_cast<const uint4*>(buf + (p * (64 / per) + lane / per) * stride + piece * 16);
+#pragma unroll
+          for (int p = 0; p < kPass; p++)
+            if (to[p] >= 0 && c < n_out)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(A.y) + ((int64_t)to[p] * n_out + c) * size) = d[p];
         } else {
           for (int e = lane; e < RT * C; e += 64) {
-            const int rr = e / C, col = e % C, c = c0 + col, to = target(qr + rr);
-            if (to < 0 || c >= n_out) continue;
-            const int64_t at = (int64_t)to * n_out + c;
+            const int rr = e / C, col = e % C, t = target(qr + rr);
+            if (t < 0 || c0 + col >= n_out) continue;
+            const int64_t at = (int64_t)t * n_out + c0 + col;
             if constexpr (size == 4)
               static_cast<float*>(A.y)[at] = *reinterpret_cast<const float*>(buf + rr * stride + col * 4);
             else
               static_cast<uint16_t*>(A.y)[at] = *reinterpret_cast<const uint16_t*>(buf + rr * stride + col * 2);
           }
         }
-      };
-      if (f32) out(std::integral_constant<int, 4>{});
-      else out(std::integral_constant<int, 2>{});
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
   }
 }
 
@@ -631,8 +634,6 @@ struct MxGrid {
   static constexpr int kLds = kFrame + kRows + 513 * 4;
   static constexpr int kCols = Op::Swiglu ? Op::BN / 2 : Op::BN;
   static constexpr int kStore = Op::kStage / Op::NW;  // a wave's share of a stage
-  static constexpr int RT = mx4_store_bytes(32, kCols / Op::WN) <= kStore ? 32 : 16;
-  static_assert(mx4_store_bytes(RT, kCols / Op::WN) <= kStore, "the results pass through a stage");
   static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
   static_assert(Op::kLoads * (S - 2) < 64, "vmcnt");
   static_assert(!Op::Swiglu || Op::FN % 2 == 0, "gate and up blocks go in pairs");
@@ -787,9 +788,14 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
       kt = 0;
       // Every wave is done reading this stage; the results pass through it.
       asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      mx4_store_tile<Op::FN, Op::FT, G::RT, BT, Op::Swiglu>(
-          A, acc, n_out, out.col * kCols + wn * (kCols / Op::WN), rows3[out.slot], out.row, min(out.hi - out.row, BT),
-          wt * Op::FT * 32, st + wave * G::kStore);
+      auto store = [&](auto yt) {
+        mx4_store_tile<yt.value, Op::FN, Op::FT, G::kStore, BT, Op::Swiglu>(
+            A, acc, n_out, out.col * kCols + wn * (kCols / Op::WN), rows3[out.slot], out.row, min(out.hi - out.row, BT),
+            wt * Op::FT * 32, st + wave * G::kStore);
+      };
+      if (A.y_type == kMxTypeBf16) store(std::integral_constant<int, kMxTypeBf16>{});
+      else if (A.y_type == kMxTypeMx4) store(std::integral_constant<int, kMxTypeMx4>{});
+      else store(std::integral_constant<int, kMxTypeF32>{});
 #pragma unroll
       for (int i = 0; i < Op::FN; i++)
 #pragma unroll
