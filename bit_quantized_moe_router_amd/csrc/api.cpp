@@ -836,7 +836,13 @@ moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const 
   TRY(check_device());
   Mx4ExpertArgs A{w_codes,   w_scales, x,        x_scales,  expert_offsets, src_rows, dst_rows,
                   row_scale, y,        y_scales, d->n_experts, d->n,        d->k,     rows,
-                  x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1};
+                  x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1, 0,        0};
+  if (src_div > 1) {
+    int log2 = 1;
+    while ((1ll << log2) < src_div) log2++;
+    A.src_magic = (uint32_t)((1ull << (31 + log2)) / (uint32_t)src_div + 1);
+    A.src_shift = log2 - 1;
+  }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
   return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, cus, s, kt); });

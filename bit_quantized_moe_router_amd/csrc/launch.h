@@ -137,6 +137,10 @@ struct Mx4ExpertArgs {
   uint8_t* y_scales;         // [y_rows][n_out / 32] with y_type = kMxTypeMx4
   int E, n, k, P, x_rows, y_rows, src_div, y_type;
   bool x_mx4, swiglu;
+  // r / src_div = (r * src_magic >> 32) >> src_shift for 0 <= r < 2^31, src_div >= 2: with L = ceil(log2 src_div),
+  // src_magic = floor(2^(31 + L) / src_div) + 1 is off by less than 2^L / src_div <= ... of a unit in 2^(31 + L).
+  uint32_t src_magic;
+  int src_shift;
 };
 // cus: the device's compute units.
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt = KTime{});

@@ -70,7 +70,7 @@ __device__ __forceinline__ bool mx4_find_tile(const int32_t* __restrict__ offset
 
 // Row of x for what src_rows says (or the position, where there is none), or -1 for none.
 __device__ __forceinline__ int mx4_src_of(const Mx4ExpertArgs& A, int r) {
-  if (A.src_rows && r >= 0 && A.src_div > 1) r /= A.src_div;
+  if (A.src_rows && r >= 0 && A.src_div > 1) r = (int)(__umulhi((uint32_t)r, A.src_magic) >> A.src_shift);
   return (unsigned)r < (unsigned)A.x_rows ? r : -1;
 }
 __device__ __forceinline__ int mx4_src(const Mx4ExpertArgs& A, int i) {
@@ -226,8 +226,9 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // 128 bytes a row) through S stages in LDS, filled by direct loads that stay
 // in flight across the barriers.
 //
-// LDS.  A row's 8 blocks of 16 bytes are stored at slot (block ^ row % 8), so
-// that the 16-byte reads of 8 consecutive rows touch all banks; the direct
+// LDS.  A row's 8 blocks of 16 bytes are stored at slot (block ^ (row / 2) % 8),
+// so that the 16-byte reads of 16 consecutive rows (two share the 256 bytes of
+// the banks) touch every bank once; the direct
 // loads write consecutive lanes to consecutive addresses, so the exchange is
 // made on the memory side, inside the row's 128 bytes.  In step s of a tile a
 // lane of half h multiplies block 4 h + s: its four scale bytes of the tile are
@@ -269,12 +270,29 @@ __device__ __forceinline__ int64_t mx4_w_row(const Mx4ExpertArgs& A, int e, int 
   return (int64_t)e * A.n + (Swiglu && (q & 32) ? n_out : 0) + min(c, n_out - 1);
 }
 
-// A tile's positions in LDS.  src and dst hold what src_rows and dst_rows say
-// (or nothing, where the position itself is meant), fac row_scale's value.
+// x, of which the compiler knows nothing: what is computed from it inside a
+// loop stays there, instead of in registers that the products need.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// The products so far are computed here: without this they sink, being free of
+// side effects, below the barriers and into the next step, behind whose loads
+// they would have run.
+template <int FN, int FT>
+__device__ __forceinline__ void computed(f32x16_t (&acc)[FN][FT]) {
+#pragma unroll
+  for (int i = 0; i < FN; i++)
+#pragma unroll
+    for (int j = 0; j < FT; j++) asm volatile("" : "+v"(acc[i][j])::"memory");
+}
+
+// A tile's positions in LDS: what src_rows and dst_rows say (or nothing, where
+// the position itself is meant).
 template <int BT>
 struct MxRows {
   int src[BT], dst[BT];
-  float fac[BT];
 };
 
 // A wave's FN x FT results to y: C columns from c0 on (with SwiGLU gate and up
@@ -286,9 +304,9 @@ struct MxRows {
 // 4096 x 8192 x 8192 with bf16 results.)
 template <int YT, int FN, int FT, int Store, int BT, bool Swiglu>
 __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t (&acc)[FN][FT], int n_out, int c0,
-                                               const MxRows<BT>& R, int row, int rows, int q0, uint8_t* buf) {
+                                               const MxRows<BT>& R, const float* fac, int row, int rows, int q0, uint8_t* buf) {
   constexpr int FO = Swiglu ? FN / 2 : FN, C = FO * 32;
-  const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+  const int lane = here(threadIdx.x & 63), r = lane & 31, h = lane >> 5;
   auto target = [&](int q) {
     const int d = A.dst_rows ? R.dst[q] : row + q;
     return q < rows && (unsigned)d < (unsigned)A.y_rows ? d : -1;
@@ -297,7 +315,7 @@ __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t 
   for (int j = 0; j < FT; j++) {
     const int q = q0 + j * 32 + r;
     const bool zero = mx4_src_of(A, A.src_rows ? R.src[q] : row + q) < 0;
-    const float w = A.row_scale ? R.fac[q] : 1.f;
+    const float w = A.row_scale ? fac[q] : 1.f;
 #pragma unroll
     for (int i = 0; i < FO; i++)
 #pragma unroll
@@ -335,7 +353,7 @@ __device__ __forceinline__ void mx4_store_tile(const Mx4ExpertArgs& A, f32x16_t 
     }
   } else {
     constexpr int size = YT == kMxTypeF32 ? 4 : 2, stride = C * size + 16;
-    constexpr int RT = 32 * stride <= Store ? 32 : 16;
+    constexpr int RT = 32 * stride <= Store ? 32 : 16 * stride <= Store ? 16 : 8;
     static_assert(RT * stride <= Store, "the results pass through a stage");
     constexpr int per = C * size / 16, kPass = RT * per / 64;  // lanes a row; instructions for RT rows
     static_assert(RT * per % 64 == 0, "whole instructions");
@@ -401,22 +419,25 @@ struct MxOp4 {
   static constexpr bool Swiglu = Swiglu_;
   static constexpr int NW = WN * WT, FN = BN / 32 / WN, FT = BT / 32 / WT;
   static constexpr int kBlocks = 8;                          // of a K tile
+  static constexpr int kSteps = 4;
   static constexpr int kCodeLoads = (BN + BT) / 8 / NW;      // of 8 rows each, a wave
-  static constexpr int kScaleRows = Ragged ? 8 : 32;         // rows of a scale load
-  static constexpr int kScaleLoads = ((BN + BT) / kScaleRows + NW - 1) / NW;
-  static constexpr int kLoads = kCodeLoads + kScaleLoads;
-  static constexpr int kScaleRow = Ragged ? 32 : 8;          // LDS bytes of a row's scales
-  static constexpr int kStage = (BN + BT) * (128 + kScaleRow);
-  static_assert((BN + BT) / 8 % NW == 0, "code loads divide among the waves");
+  static constexpr int kLoads = kCodeLoads;                  // of every K tile, a wave
+  static constexpr int kScaleRows = Ragged ? 8 : 64;         // rows of a scale load
+  static constexpr int kScaleTiles = Ragged ? 1 : 2;         // K tiles of a scale load: 16 blocks
+  static constexpr int kScaleAll = (BN + BT) / kScaleRows, kScaleLoads = (kScaleAll + NW - 1) / NW;
+  static constexpr int kScaleRow = Ragged ? 32 : 16;         // LDS bytes of a row's scales
+  static constexpr int kStage = (BN + BT) * 128, kPanel = (BN + BT) * kScaleRow;
+  static_assert((BN + BT) / 8 % NW == 0 && (BN + BT) % kScaleRows == 0, "code loads divide among the waves");
 
   const uint8_t* code_p[kCodeLoads];
   const uint8_t* scale_p[kScaleLoads];
   int wave, lane, nb;
 
-  // Where the scale loads do not divide among the waves, the last ones are made twice.
-  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, (BN + BT) / kScaleRows - 1); }
+  // The last scale loads are not every wave's.
+  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, kScaleAll - 1); }
 
   __device__ __forceinline__ void set_w(const Mx4ExpertArgs& A, int e, int n_out, int c0) {
+    const int lane = here(this->lane);
 #pragma unroll
     for (int j = 0; j < kCodeLoads; j++) {
       const int q = (wave + NW * j) * 8 + (lane >> 3);
@@ -424,12 +445,13 @@ struct MxOp4 {
     }
 #pragma unroll
     for (int j = 0; j < kScaleLoads; j++) {
-      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
+      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane);
       if (scale_load(j) * kScaleRows < BN) scale_p[j] = A.w_scales + mx4_w_row<Swiglu>(A, e, n_out, c0, q) * nb;
     }
   }
   template <class Src>
   __device__ __forceinline__ void set_x(const Mx4ExpertArgs& A, Src src) {
+    const int lane = here(this->lane);
 #pragma unroll
     for (int j = 0; j < kCodeLoads; j++) {
       const int q = (wave + NW * j) * 8 + (lane >> 3);
@@ -438,107 +460,111 @@ struct MxOp4 {
     }
 #pragma unroll
     for (int j = 0; j < kScaleLoads; j++) {
-      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane >> 1);
+      const int q = scale_load(j) * kScaleRows + (Ragged ? lane >> 3 : lane);
       if (scale_load(j) * kScaleRows >= BN) scale_p[j] = A.x_scales + (int64_t)max(src(q - BN), 0) * nb;
     }
   }
-  __device__ __forceinline__ void issue(int kt, uint32_t base) const {
-    int cb = kt * kBlocks + ((lane & 7) ^ (lane >> 3));
-    int so = kt * kBlocks + (Ragged ? lane & 7 : (lane & 1) * 4);
-    if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
-#pragma unroll
-    for (int j = 0; j < kCodeLoads; j++) load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+  // The scales that begin with K tile kt, to LDS from `panel` on.
+  __device__ __forceinline__ void issue_scales(int kt, uint32_t panel) const {
+    int so = kt * kBlocks + (Ragged ? lane & 7 : 0);
+    if (Ragged) so = min(so, nb - 1);
 #pragma unroll
     for (int j = 0; j < kScaleLoads; j++)
-      load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + (BN + BT) * 128 + scale_load(j) * 256);
+      if (wave + NW * j < kScaleAll) load_to_lds<Ragged ? 1 : 16>(scale_p[j] + so, panel + (wave + NW * j) * (Ragged ? 256 : 1024));
   }
-  __device__ __forceinline__ void compute(int kt, const uint8_t* st, int wn, int wt, f32x16_t (&acc)[FN][FT]) const {
+  // Part `part` of kSteps of a K tile's loads.
+  template <int part>
+  __device__ __forceinline__ void issue(int kt, uint32_t base) const {
+    // Row 8 (wave + NW j) + lane / 8 has the exchange 4 (wave % 2) + lane / 16, NW being even.
+    static_assert(NW % 2 == 0, "the exchange does not depend on j");
+    int cb = kt * kBlocks + ((lane & 7) ^ ((wave & 1) * 4 + (lane >> 4)));
+    if (Ragged) cb = min(cb, nb - 1);
+#pragma unroll
+    for (int j = part; j < kCodeLoads; j += kSteps)
+      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+  }
+  // Step s of a K tile multiplies block 4 h + s.  The scales of a tile are read with its step 0, a ragged
+  // tile's with each step.
+  struct Frags {
+    uint4 w[FN], x[FT];
+    uint32_t ws[FN], xs[FT];  // ragged
+  };
+  struct Scales {
+    uint32_t w[FN], x[FT];
+  };
+  __device__ __forceinline__ void load_scales(int kt, const uint8_t* panel, int wn, int wt, Scales& d) const {
+    if constexpr (!Ragged) {
+      const int r = lane & 31, h = lane >> 5;
+      const uint8_t* s = panel + r * kScaleRow + (kt & 1) * 8 + h * 4;
+#pragma unroll
+      for (int f = 0; f < FN; f++) d.w[f] = *reinterpret_cast<const uint32_t*>(s + (wn * FN + f) * 32 * kScaleRow);
+#pragma unroll
+      for (int f = 0; f < FT; f++) d.x[f] = *reinterpret_cast<const uint32_t*>(s + (BN + (wt * FT + f) * 32) * kScaleRow);
+    }
+  }
+  template <int s>
+  __device__ __forceinline__ void load_step(const uint8_t* st, const uint8_t* panel, int wn, int wt, Frags& d) const {
     const int r = lane & 31, h = lane >> 5;
-    const uint8_t* wl = st + (wn * FN * 32 + r) * 128;
-    const uint8_t* xl = st + (BN + wt * FT * 32 + r) * 128;
-    const uint8_t* sw = st + (BN + BT) * 128 + (wn * FN * 32 + r) * kScaleRow + h * (kScaleRow / 2);
-    const uint8_t* sx = st + (BN + BT) * 128 + (BN + wt * FT * 32 + r) * kScaleRow + h * (kScaleRow / 2);
-    struct Frags {
-      uint4 w[FN], x[FT];
-      uint32_t ws[FN], xs[FT];
-    } a, b;
-    auto load = [&](auto sc, Frags& d) {
-      constexpr int s = sc.value;
-      const int slot = ((4 * h + s) ^ (r & 7)) * 16;
+    const uint8_t* at = st + r * 128 + ((4 * h + s) ^ ((r >> 1) & 7)) * 16;
+    const uint8_t* sc = panel + r * kScaleRow + h * 16 + s * 4;  // ragged
 #pragma unroll
-      for (int f = 0; f < FN; f++) d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 128 + slot);
+    for (int f = 0; f < FN; f++) d.w[f] = *reinterpret_cast<const uint4*>(at + (wn * FN + f) * 32 * 128);
 #pragma unroll
-      for (int f = 0; f < FT; f++) d.x[f] = *reinterpret_cast<const uint4*>(xl + f * 32 * 128 + slot);
-      // The tile's dword of scales is read in step 0; a ragged one's each step.
-      if (Ragged || s == 0) {
+    for (int f = 0; f < FT; f++) d.x[f] = *reinterpret_cast<const uint4*>(at + (BN + (wt * FT + f) * 32) * 128);
+    if constexpr (Ragged) {
 #pragma unroll
-        for (int f = 0; f < FN; f++)
-          d.ws[f] = *reinterpret_cast<const uint32_t*>(sw + f * 32 * kScaleRow + (Ragged ? s * 4 : 0));
+      for (int f = 0; f < FN; f++) d.ws[f] = *reinterpret_cast<const uint32_t*>(sc + (wn * FN + f) * 32 * kScaleRow);
 #pragma unroll
-        for (int f = 0; f < FT; f++)
-          d.xs[f] = *reinterpret_cast<const uint32_t*>(sx + f * 32 * kScaleRow + (Ragged ? s * 4 : 0));
-      }
-    };
-    auto mul = [&](auto sc, Frags& d, const Frags& sd) {
-      constexpr int s = sc.value;
-      uint32_t ws[FN], xs[FT];
-      const bool in = !Ragged || kt * kBlocks + 4 * h + s < nb;
+      for (int f = 0; f < FT; f++) d.xs[f] = *reinterpret_cast<const uint32_t*>(sc + (BN + (wt * FT + f) * 32) * kScaleRow);
+    }
+  }
+  template <int s>
+  __device__ __forceinline__ void mul_step(int kt, Frags& d, const Scales& sc, f32x16_t (&acc)[FN][FT]) const {
+    const bool in = !Ragged || kt * kBlocks + 4 * (lane >> 5) + s < nb;
+    uint32_t ws[FN], xs[FT];
 #pragma unroll
-      for (int f = 0; f < FN; f++) ws[f] = in ? sd.ws[f] : 0x7Fu;
+    for (int f = 0; f < FN; f++) ws[f] = !Ragged ? sc.w[f] : in ? d.ws[f] : 0x7Fu;
 #pragma unroll
-      for (int f = 0; f < FT; f++) {
-        xs[f] = in ? sd.xs[f] : 0x7Fu;
-        if (!in) d.x[f] = make_uint4(0, 0, 0, 0);
-      }
+    for (int f = 0; f < FT; f++) {
+      xs[f] = !Ragged ? sc.x[f] : in ? d.xs[f] : 0x7Fu;
+      if (!in) d.x[f] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-      for (int i = 0; i < FN; i++)
+    for (int i = 0; i < FN; i++)
 #pragma unroll
-        for (int j = 0; j < FT; j++)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(d.w[i]), mx4_operand(d.x[j]), acc[i][j],
-                                                                      kE2m1, kE2m1, Ragged ? 0 : s, ws[i], Ragged ? 0 : s,
-                                                                      xs[j]);
-    };
-    // The next step's operands are read while the present one's are multiplied.
-    const auto s0 = std::integral_constant<int, 0>{};
-    const auto s1 = std::integral_constant<int, 1>{};
-    const auto s2 = std::integral_constant<int, 2>{};
-    const auto s3 = std::integral_constant<int, 3>{};
-    load(s0, a);
-    load(s1, b);
-    mul(s0, a, a);
-    __builtin_amdgcn_sched_barrier(0);
-    load(s2, a);  // leaves the scales of step 0, but for a ragged tile
-    mul(s1, b, Ragged ? b : a);
-    __builtin_amdgcn_sched_barrier(0);
-    load(s3, b);
-    mul(s2, a, a);
-    __builtin_amdgcn_sched_barrier(0);
-    mul(s3, b, Ragged ? b : a);
+      for (int j = 0; j < FT; j++)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(mx4_operand(d.w[i]), mx4_operand(d.x[j]), acc[i][j],
+                                                                    kE2m1, kE2m1, Ragged ? 0 : s, ws[i], Ragged ? 0 : s,
+                                                                    xs[j]);
   }
 };
 
 // ---- the operands of a tile, bf16 x ----------------------------------------------
-template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged>
+// ST: K tiles of a scale load, 4 (16 bytes a row), or 1 (4 bytes) where LDS is short.
+template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged, int ST>
 struct MxOp16 {
   static constexpr int BN = BN_, BT = BT_, WN = WN_, WT = WT_;
   static constexpr bool Swiglu = Swiglu_;
   static constexpr int NW = WN * WT, FN = BN / 32 / WN, FT = BT / 32 / WT;
   static constexpr int kBlocks = 4;                   // of a K tile
+  static constexpr int kSteps = 2;
   static constexpr int kCodeLoads = BN / 16 / NW;     // of 16 rows each, a wave
   static constexpr int kXLoads = BT / 4 / NW;         // of 4 rows each
+  static constexpr int kLoads = kCodeLoads + kXLoads; // of every K tile, a wave
   static constexpr int kScaleRows = Ragged ? 16 : 64; // rows of a scale load
-  static constexpr int kScaleLoads = (BN / kScaleRows + NW - 1) / NW;
-  static constexpr int kLoads = kCodeLoads + kXLoads + kScaleLoads;
-  static constexpr int kScaleRow = Ragged ? 16 : 4;
-  static constexpr int kStage = BN * (64 + kScaleRow) + BT * 256;
+  static constexpr int kScaleTiles = Ragged ? 1 : ST;
+  static constexpr int kScaleAll = BN / kScaleRows, kScaleLoads = (kScaleAll + NW - 1) / NW;
+  static constexpr int kScaleRow = Ragged ? 16 : 4 * ST;  // LDS bytes of a row's scales
+  static constexpr int kStage = BN * 64 + BT * 256, kPanel = BN * kScaleRow;
   static_assert(BN / 16 % NW == 0 && BT / 4 % NW == 0, "loads divide among the waves");
 
   const uint8_t *code_p[kCodeLoads], *x_p[kXLoads], *scale_p[kScaleLoads];
   int wave, lane, nb;
 
-  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, BN / kScaleRows - 1); }
+  __device__ __forceinline__ int scale_load(int j) const { return min(wave + NW * j, kScaleAll - 1); }
 
   __device__ __forceinline__ void set_w(const Mx4ExpertArgs& A, int e, int n_out, int c0) {
+    const int lane = here(this->lane);
 #pragma unroll
     for (int j = 0; j < kCodeLoads; j++)
       code_p[j] = A.w_codes + mx4_w_row<Swiglu>(A, e, n_out, c0, (wave + NW * j) * 16 + (lane >> 2)) * nb * kMxBlockBytes;
@@ -548,90 +574,112 @@ struct MxOp16 {
   }
   template <class Src>
   __device__ __forceinline__ void set_x(const Mx4ExpertArgs& A, Src src) {
+    const int lane = here(this->lane);
 #pragma unroll
     for (int j = 0; j < kXLoads; j++)
       x_p[j] = static_cast<const uint8_t*>(A.x) + (int64_t)max(src((wave + NW * j) * 4 + (lane >> 4)), 0) * A.k * 2;
   }
+  __device__ __forceinline__ void issue_scales(int kt, uint32_t panel) const {
+    int so = kt * kBlocks + (Ragged ? lane & 3 : 0);
+    if (Ragged) so = min(so, nb - 1);
+#pragma unroll
+    for (int j = 0; j < kScaleLoads; j++)
+      if (wave + NW * j < kScaleAll) load_to_lds<Ragged ? 1 : 4 * ST>(scale_p[j] + so, panel + (wave + NW * j) * (Ragged ? 256 : 256 * ST));
+  }
+  template <int part>
   __device__ __forceinline__ void issue(int kt, uint32_t base) const {
     int cb = kt * kBlocks + ((lane & 3) ^ ((lane >> 4) & 3));
-    int so = kt * kBlocks + (Ragged ? lane & 3 : 0);
-    if (Ragged) cb = min(cb, nb - 1), so = min(so, nb - 1);
+    if (Ragged) cb = min(cb, nb - 1);
 #pragma unroll
-    for (int j = 0; j < kCodeLoads; j++) load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
+    for (int j = part; j < kCodeLoads; j += kSteps)
+      load_to_lds<16>(code_p[j] + cb * kMxBlockBytes, base + (wave + NW * j) * 1024);
 #pragma unroll
-    for (int j = 0; j < kXLoads; j++) {
-      int xb = kt * kBlocks * 4 + ((lane & 15) ^ ((4 * (wave + NW * j) + (lane >> 4)) & 7));
+    for (int j = part; j < kXLoads; j += kSteps) {
+      int xb = kt * kBlocks * 4 + ((lane & 15) ^ ((4 * (wave + NW * j) + (lane >> 4)) & 15));
       if (Ragged) xb = min(xb, nb * 4 - 1);
       load_to_lds<16>(x_p[j] + xb * 16, base + BN * 64 + (wave + NW * j) * 1024);
     }
-#pragma unroll
-    for (int j = 0; j < kScaleLoads; j++)
-      load_to_lds<Ragged ? 1 : 4>(scale_p[j] + so, base + BN * 64 + BT * 256 + scale_load(j) * 256);
   }
-  __device__ __forceinline__ void compute(int kt, const uint8_t* st, int wn, int wt, f32x16_t (&acc)[FN][FT]) const {
-    const int r = lane & 31, h = lane >> 5;
-    const uint8_t* wl = st + (wn * FN * 32 + r) * 64;
+  // Step s of a K tile multiplies block 2 s + h, 8 columns an instruction.
+  struct Frags {
+    uint4 w[FN], x[FT][4];
+    uint32_t s[FN];
+  };
+  struct Scales {
+    uint32_t w[FN];
+  };
+  __device__ __forceinline__ void load_scales(int kt, const uint8_t* panel, int wn, int, Scales& d) const {
+    if constexpr (!Ragged) {
+#pragma unroll
+      for (int f = 0; f < FN; f++)
+        d.w[f] = *reinterpret_cast<const uint32_t*>(panel + ((wn * FN + f) * 32 + (lane & 31)) * kScaleRow + kt % kScaleTiles * 4);
+    }
+  }
+  template <int s>
+  __device__ __forceinline__ void load_step(const uint8_t* st, const uint8_t* panel, int wn, int wt, Frags& d) const {
+    const int r = lane & 31, h = lane >> 5, blk = 2 * s + h;
+    const uint8_t* wl = st + (wn * FN * 32 + r) * 64 + ((blk ^ ((r >> 2) & 3)) * 16);
     const uint8_t* xl = st + BN * 64 + (wt * FT * 32 + r) * 256;
-    const uint8_t* sl = st + BN * 64 + BT * 256 + (wn * FN * 32 + r) * kScaleRow;
-    struct Frags {
-      uint4 w[FN], x[FT][4];
-      float s[FN];
-    } a, b;
-    auto load = [&](int p, Frags& d) {
-      const int blk = 2 * p + h;
-      const bool in = !Ragged || kt * kBlocks + blk < nb;
+    const uint8_t* sl = panel + (wn * FN * 32 + r) * kScaleRow + blk * 4;  // ragged
 #pragma unroll
-      for (int f = 0; f < FN; f++) {
-        d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 64 + ((blk ^ ((r >> 2) & 3)) * 16));
-        uint32_t sc = *reinterpret_cast<const uint32_t*>(sl + f * 32 * kScaleRow + (Ragged ? blk * 4 : 0));
-        if (!Ragged) sc >>= 8 * blk;
-        d.s[f] = mx4_scale_f32(in ? sc & 0xFFu : 127u);
+    for (int f = 0; f < FN; f++) {
+      d.w[f] = *reinterpret_cast<const uint4*>(wl + f * 32 * 64);
+      if (Ragged) d.s[f] = *reinterpret_cast<const uint32_t*>(sl + f * 32 * kScaleRow);
+    }
+#pragma unroll
+    for (int f = 0; f < FT; f++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) d.x[f][j] = *reinterpret_cast<const uint4*>(xl + f * 32 * 256 + (((4 * blk + j) ^ (r & 15)) * 16));
+  }
+  template <int s>
+  __device__ __forceinline__ void mul_step(int kt, Frags& d, const Scales& ts, f32x16_t (&acc)[FN][FT]) const {
+    const int blk = 2 * s + (lane >> 5);
+    const bool in = !Ragged || kt * kBlocks + blk < nb;
+    float sc[FN];
+#pragma unroll
+    for (int f = 0; f < FN; f++) sc[f] = mx4_scale_f32(!in ? 127u : Ragged ? d.s[f] & 0xFFu : (ts.w[f] >> (8 * blk)) & 0xFFu);
+#pragma unroll
+    for (int f = 0; f < FT; f++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (!in) d.x[f][j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      bf16x8_t w[FN];
+#pragma unroll
+      for (int i = 0; i < FN; i++) {
+        const uint32_t c = j == 0 ? d.w[i].x : j == 1 ? d.w[i].y : j == 2 ? d.w[i].z : d.w[i].w;
+        w[i] = __builtin_bit_cast(bf16x8_t, mx4_unpack8_bf16(c, sc[i]));
       }
 #pragma unroll
-      for (int f = 0; f < FT; f++)
+      for (int i = 0; i < FN; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          d.x[f][j] = *reinterpret_cast<const uint4*>(xl + f * 32 * 256 + (((4 * blk + j) ^ (r & 7)) * 16));
-          if (!in) d.x[f][j] = make_uint4(0, 0, 0, 0);
-        }
-    };
-    auto mul = [&](const Frags& d) {
-#pragma unroll
-      for (int j = 0; j < 4; j++) {
-        bf16x8_t w[FN];
-#pragma unroll
-        for (int i = 0; i < FN; i++) {
-          const uint32_t c = j == 0 ? d.w[i].x : j == 1 ? d.w[i].y : j == 2 ? d.w[i].z : d.w[i].w;
-          w[i] = __builtin_bit_cast(bf16x8_t, mx4_unpack8_bf16(c, d.s[i]));
-        }
-#pragma unroll
-        for (int i = 0; i < FN; i++)
-#pragma unroll
-          for (int f = 0; f < FT; f++)
-            acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], __builtin_bit_cast(bf16x8_t, d.x[f][j]), acc[i][f], 0, 0, 0);
-      }
-    };
-    load(0, a);
-    load(1, b);
-    mul(a);
-    mul(b);
+        for (int f = 0; f < FT; f++)
+          acc[i][f] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[i], __builtin_bit_cast(bf16x8_t, d.x[f][j]), acc[i][f], 0, 0, 0);
+    }
   }
 };
 
 // ---- the kernel ----------------------------------------------------------------------
-// Units are (tile of BT positions, BN weight rows), columns fastest.  A
-// workgroup takes a contiguous range of them, and its loads run through it
-// without a pause: while a unit's results are stored, the next unit's first K
-// tiles are on their way, and a tile's src, dst and factors are brought by the
-// same direct loads while the tile before it is worked on.  (With a workgroup a
-// unit, the chain offsets -> src -> x cost about 8 us each time: 116 and 121 us
-// for the products below where this takes ...)  Consecutive ranges share an
-// XCD, whose L2 then keeps an expert's weights for its tiles.
+// A unit is a tile of BT positions of an expert by BN weight rows.  A workgroup
+// goes through several, and its loads run through them without a pause: while
+// a unit's results are stored, the next unit's first K tiles are on their way,
+// and its src, dst and factors are brought by the same direct loads while the
+// unit before it is worked on.  (With a workgroup a unit, the chain
+// offsets -> src -> x cost about 8 us each time.)
+//
+// A workgroup has a range of the units in the order (expert, tile, column
+// tile), and consecutive ranges share an XCD, whose L2 then keeps an expert's
+// weights for its tiles.
 template <class Op, int S>
 struct MxGrid {
-  static constexpr int kFrame = S * Op::kStage;
-  static constexpr int kRows = 3 * (int)sizeof(MxRows<Op::BT>);
-  static constexpr int kLds = kFrame + kRows + 513 * 4;
+  static constexpr int kPanels = S * Op::kStage;                 // where the two scale panels begin,
+  // A panel is replaced that many later, when its last K tile is done.
+  static constexpr int kPanelSlots = Op::kScaleTiles >= S - 1 ? 2 : S;
+  static constexpr int kRows = kPanels + kPanelSlots * Op::kPanel;  // the rows of three units,
+  static constexpr int kFac = kRows + 3 * (int)sizeof(MxRows<Op::BT>);  // the factors of two
+  static constexpr int kLds = kFac + 2 * Op::BT * 4;
+  static_assert(513 * 4 <= Op::kStage, "the offsets, before the first loads");
   static constexpr int kCols = Op::Swiglu ? Op::BN / 2 : Op::BN;
   static constexpr int kStore = Op::kStage / Op::NW;  // a wave's share of a stage
   static_assert(S >= 2 && kLds <= 160 * 1024, "LDS");
@@ -639,13 +687,14 @@ struct MxGrid {
   static_assert(!Op::Swiglu || Op::FN % 2 == 0, "gate and up blocks go in pairs");
 };
 
-template <class Op, int S, int Occ>
+template <class Op, int S, int Occ, int YT>
 __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) {
   using G = MxGrid<Op, S>;
   constexpr int BT = Op::BT, NW = Op::NW, kCols = G::kCols;
   extern __shared__ __attribute__((aligned(16))) uint8_t sm[];
-  auto* rows3 = reinterpret_cast<MxRows<BT>*>(sm + G::kFrame);
-  int* s_off = reinterpret_cast<int*>(sm + G::kFrame + G::kRows);
+  auto* rows3 = reinterpret_cast<MxRows<BT>*>(sm + G::kRows);
+  auto* fac2 = reinterpret_cast<float*>(sm + G::kFac);
+  int* s_off = reinterpret_cast<int*>(sm);  // before the first loads
   const uint32_t lds0 = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t*)sm);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int n_out = Op::Swiglu ? A.n >> 1 : A.n, E = A.E;
@@ -665,48 +714,49 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
     const int v = __shfl_up(end, d);
     if (lane >= d) end += v;
   }
-  const int tiles = __builtin_amdgcn_readlane(end, 63);
-  const int64_t units = (int64_t)tiles * cols;
-  // Workgroup b runs on XCD b % 8: each XCD gets consecutive ranges.
+  const int units = __builtin_amdgcn_readlane(end, 63) * cols;  // below 2^28: P <= 2^24, n <= 2^16
+  // Workgroup b runs on XCD b % 8: consecutive ranges of units to the workgroups of one XCD.
   const int n_wg = gridDim.x, wg = (blockIdx.x & 7) * (n_wg >> 3) + (blockIdx.x >> 3);  // n_wg is a multiple of 8
-  const int64_t u0 = units * wg / n_wg, u1 = units * (wg + 1) / n_wg;
-  if (u0 >= u1) return;
+  auto cut = [&](int x) { return units / n_wg * x + units % n_wg * x / n_wg; };
+  const int u0 = cut(wg), u1 = cut(wg + 1), n_unit = u1 - u0;
+  if (n_unit <= 0) return;
 
-  // Position of a walk over the units.
-  struct Walk {
-    int e, row, hi, col, slot;  // expert, first position, its end, column tile, rows' slot
-    int tile;
+  // A unit: expert e, its tile's first position, the expert's positions' end, its column tile, its tile's slot.
+  struct Unit {
+    int e, row, hi, col, slot, turn;
   };
-  auto next_tile = [&](Walk& w) {
-    w.tile++;
+  auto next_tile = [&](Unit w) {
+    const auto* off = (const __attribute__((address_space(4))) int*)A.offsets;  // scalar loads
     w.slot = w.slot == 2 ? 0 : w.slot + 1;
+    w.turn ^= 1;
     w.row += BT;
-    if (w.row < w.hi) return;
-    do w.e++;
-    while (w.e < E - 1 && s_off[w.e + 1] <= s_off[w.e]);
-    w.row = __builtin_amdgcn_readfirstlane(s_off[w.e]);
-    w.hi = __builtin_amdgcn_readfirstlane(s_off[w.e + 1]);
+    while (w.row >= w.hi && w.e < E - 1) {
+      w.e++;
+      w.row = min(max(off[w.e], 0), A.P);
+      w.hi = min(max(off[w.e + 1], 0), A.P);
+    }
+    return w;
   };
-  Walk in;  // the loads' walk
+  Unit in;
   {
-    const int t0 = (int)(u0 / cols);
-    in.tile = t0;
-    in.col = (int)(u0 - (int64_t)t0 * cols);
-    in.slot = 0;
+    const int t0 = u0 / cols;
     int first = end - mine, e = 0;
     const int owner = __builtin_ctzll(__ballot(t0 >= first && t0 < end));
     if (lane == owner)
       for (e = e0; t0 >= first + tiles_of(e); e++) first += tiles_of(e);
+    in.slot = in.turn = 0;
     in.e = __builtin_amdgcn_readlane(e, owner);
-    first = __builtin_amdgcn_readlane(first, owner);
-    in.row = __builtin_amdgcn_readfirstlane(s_off[in.e]) + (t0 - first) * BT;
+    in.row = __builtin_amdgcn_readfirstlane(s_off[in.e]) + (t0 - __builtin_amdgcn_readlane(first, owner)) * BT;
     in.hi = __builtin_amdgcn_readfirstlane(s_off[in.e + 1]);
+    in.col = u0 - t0 * cols;
   }
-  const int last_tile = (int)((u1 - 1) / cols);
+  // The products' tile, the tile after it and the tile after that, as far as known.
+  Unit tile0 = in, tile1 = in, tile2 = in;
+  int out_col = in.col;
 
   // Direct loads of what src_rows and dst_rows say about a tile, 64 positions a wave.
-  const uint32_t rows_lds = lds0 + G::kFrame;
-  auto load_rows = [&](const Walk& w) {
+  const uint32_t rows_lds = lds0 + G::kRows;
+  auto load_rows = [&](const Unit& w) {
     for (int q = wave * 64; q < BT; q += NW * 64) {
       const int64_t at = min(w.row + q + lane, A.P - 1);
       const uint32_t to = rows_lds + w.slot * (int)sizeof(MxRows<BT>) + q * 4;
@@ -717,13 +767,13 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
     }
   };
   // The same for the factors, once the tile's dst are in LDS.
-  auto load_factors = [&](const Walk& w) {
+  auto load_factors = [&](const Unit& w) {
     if (!A.row_scale) return;
     for (int q = wave * 64; q < BT; q += NW * 64) {
       if (BT % 64 != 0 && q + lane >= BT) continue;
       const int d = A.dst_rows ? rows3[w.slot].dst[q + lane] : w.row + q + lane;
       load_to_lds<4>(A.row_scale + ((unsigned)d < (unsigned)A.y_rows ? d : 0),
-                     rows_lds + w.slot * (int)sizeof(MxRows<BT>) + (2 * BT + q) * 4);
+                     lds0 + G::kFac + (w.turn * BT + q) * 4);
     }
   };
 
@@ -732,80 +782,155 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
   op.lane = lane;
   op.nb = A.k >> 5;
   const int nkt = (op.nb + Op::kBlocks - 1) / Op::kBlocks;
-  const int n_it = (int)((u1 - u0) * nkt);  // nkt is at least S - 1 (launch_mx4_experts)
+  const int n_it = n_unit * nkt;  // nkt is at least S - 1 (launch_mx4_experts)
   load_rows(in);
   wait_loads<0>();
   __syncthreads();
-  Walk out = in;  // the products' walk
 
-  int in_kt = 0, in_stage = 0;
+  // A K tile's loads: begin() sets the addresses where a unit begins, issue() is called for each part, end_()
+  // moves on.  The loads are in the products' tile or the one after it.
+  int in_kt = 0, in_stage = 0, in_unit = 0, in_ahead = 0, in_panel = 0;
   bool in_new = true;
-  auto issue_next = [&] {
-    if (in_kt == 0) {
-      if (in_new) {
-        in_new = false;
-        const MxRows<BT>& R = rows3[in.slot];
-        op.set_x(A, [&](int q) { return mx4_src_of(A, A.src_rows ? R.src[q] : min(in.row + q, A.P - 1)); });
-        load_factors(in);
-        if (in.tile < last_tile) {
-          Walk w = in;
-          next_tile(w);
-          load_rows(w);
-        }
+  auto begin_unit = [&] {
+    if (in_new) {
+      in_new = false;
+      const MxRows<BT>& R = rows3[in.slot];
+      op.set_x(A, [&](int q) { return mx4_src_of(A, A.src_rows ? R.src[q] : min(in.row + q, A.P - 1)); });
+      load_factors(in);
+      if (in_unit + cols - in.col < n_unit) {  // a unit of the next tile is this workgroup's
+        const Unit w = next_tile(in);
+        load_rows(w);
+        if (in_ahead) tile2 = w;
+        else tile1 = w;
       }
-      op.set_w(A, in.e, n_out, in.col * kCols);
     }
-    op.issue(in_kt, lds0 + in_stage * Op::kStage);
+    op.set_w(A, in.e, n_out, in.col * kCols);
+  };
+  auto begin = [&] {
+    if (in_kt == 0) begin_unit();
+    if (in_kt % Op::kScaleTiles == 0) {
+      op.issue_scales(in_kt, lds0 + G::kPanels + in_panel * Op::kPanel);
+      in_panel = in_panel == G::kPanelSlots - 1 ? 0 : in_panel + 1;
+    }
+  };
+  auto end_ = [&] {
     in_stage = in_stage == S - 1 ? 0 : in_stage + 1;
     if (++in_kt == nkt) {
       in_kt = 0;
+      in_unit++;
       if (++in.col == cols) {
+        in = in_ahead ? tile2 : tile1;
         in.col = 0;
         in_new = true;
-        if (in.tile < last_tile) next_tile(in);
+        in_ahead++;
       }
     }
   };
+  auto issue = [&](auto part) { op.template issue<part.value>(in_kt, lds0 + in_stage * Op::kStage); };
 
   const int wn = wave % Op::WN, wt = wave / Op::WN;
   f32x16_t acc[Op::FN][Op::FT] = {};
-#pragma unroll
-  for (int i = 0; i < S - 1; i++)
-    if (i < n_it) issue_next();
-  int stage = 0, kt = 0;
-  for (int it = 0; it < n_it; it++) {
-    // The stage's loads have landed when at most those of the later stages are in flight.
-    const int later = min(S - 2, n_it - 1 - it);
+  typename Op::Frags frag[2];
+  typename Op::Scales scale, next_scale;
+  auto stage_ptr = [&](int i) { return sm + i * Op::kStage; };
+  int panel = 0;
+  auto panel_ptr = [&] { return sm + G::kPanels + panel * Op::kPanel; };
+  // Waits until at most `later` K tiles' loads are in flight, and for the other waves to have come as far.
+  auto arrive = [&](int later) {
+    later = min(later, S - 2);  // -1 after the last K tile
     if (S >= 4 && later >= 2) wait_loads<Op::kLoads * (S >= 4 ? 2 : 0)>();
     else if (S >= 3 && later == 1) wait_loads<Op::kLoads * (S >= 3 ? 1 : 0)>();
     else wait_loads<0>();
-    // Every wave's loads have landed, and every wave is done with the stage that is filled next.
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (it + S - 1 < n_it) issue_next();
-    uint8_t* st = sm + stage * Op::kStage;
-    op.compute(kt, st, wn, wt, acc);
-    if (++kt == nkt) {
-      kt = 0;
-      // Every wave is done reading this stage; the results pass through it.
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      auto store = [&](auto yt) {
-        mx4_store_tile<yt.value, Op::FN, Op::FT, G::kStore, BT, Op::Swiglu>(
-            A, acc, n_out, out.col * kCols + wn * (kCols / Op::WN), rows3[out.slot], out.row, min(out.hi - out.row, BT),
-            wt * Op::FT * 32, st + wave * G::kStore);
-      };
-      if (A.y_type == kMxTypeBf16) store(std::integral_constant<int, kMxTypeBf16>{});
-      else if (A.y_type == kMxTypeMx4) store(std::integral_constant<int, kMxTypeMx4>{});
-      else store(std::integral_constant<int, kMxTypeF32>{});
+  };
+  const auto s0 = std::integral_constant<int, 0>{};
+  const auto s1 = std::integral_constant<int, 1>{};
+  const auto s2 = std::integral_constant<int, Op::kSteps == 4 ? 2 : 0>{};
+  const auto s3 = std::integral_constant<int, Op::kSteps == 4 ? 3 : 0>{};
+#pragma unroll 1
+  for (int i = 0; i < S - 1 && i < n_it; i++) {
+    begin();
+    issue(s0);
+    issue(s1);
+    if constexpr (Op::kSteps == 4) {
+      issue(s2);
+      issue(s3);
+    }
+    end_();
+  }
+  arrive(n_it - 1);
+  op.load_scales(0, panel_ptr(), wn, wt, next_scale);
+  op.template load_step<0>(stage_ptr(0), panel_ptr(), wn, wt, frag[0]);
+  int stage = 0, kt = 0;
+  for (int it = 0; it < n_it; it++) {
+    uint8_t* st = stage_ptr(stage);
+    stage = stage == S - 1 ? 0 : stage + 1;
+    scale = next_scale;
+    const bool last = it == n_it - 1, unit = kt == nkt - 1;
+    // K tile it + S - 1 goes where K tile it - 1 was, a part with each step, so that the loads queue up behind
+    // products and not behind each other.
+    const bool more = it + S - 1 < n_it;
+    if (more) begin();
+    if (S == 2 && more) {  // they have this K tile's time to arrive
+      issue(s0);
+      issue(s1);
+      if constexpr (Op::kSteps == 4) {
+        issue(s2);
+        issue(s3);
+      }
+    }
+    // While a step is multiplied the next one's operands are read.
+    auto step = [&](auto sc) {
+      constexpr int s = sc.value;
+      op.template load_step<s + 1>(st, panel_ptr(), wn, wt, frag[(s + 1) & 1]);
+      if (S > 2 && more) issue(sc);
+      __builtin_amdgcn_sched_barrier(0);
+      op.template mul_step<s>(kt, frag[s & 1], scale, acc);
+      computed(acc);
+    };
+    step(s0);
+    if constexpr (Op::kSteps == 4) {
+      step(s1);
+      step(s2);
+      if (S > 2 && more) issue(s3);
+    } else {
+      if (S > 2 && more) issue(s1);
+    }
+    if (more) end_();
+    auto last_step = [&] {
+      __builtin_amdgcn_sched_barrier(0);
+      op.template mul_step<Op::kSteps - 1>(kt, frag[1], scale, acc);
+      computed(acc);
+    };
+    // The last step's operands are in registers: when every wave is here, this stage is free and the next
+    // one is complete.  Its first operands are read during the last step; but at a unit's end the results go
+    // out through this stage first.
+    arrive(n_it - 2 - it);
+    if (unit) {
+      last_step();
+      mx4_store_tile<YT, Op::FN, Op::FT, G::kStore, BT, Op::Swiglu>(
+          A, acc, n_out, out_col * kCols + wn * (kCols / Op::WN), rows3[tile0.slot], fac2 + tile0.turn * BT, tile0.row,
+          min(tile0.hi - tile0.row, BT),
+          wt * Op::FT * 32, st + wave * G::kStore);
+      if (last) break;
 #pragma unroll
       for (int i = 0; i < Op::FN; i++)
 #pragma unroll
         for (int j = 0; j < Op::FT; j++) acc[i][j] = f32x16_t{};
-      if (++out.col == cols) {
-        out.col = 0;
-        if (out.tile < last_tile) next_tile(out);
+      if (++out_col == cols) {
+        out_col = 0;
+        tile0 = tile1;
+        tile1 = tile2;
+        in_ahead--;
       }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
-    stage = stage == S - 1 ? 0 : stage + 1;
+    const int next_kt = unit ? 0 : kt + 1;
+    if (next_kt % Op::kScaleTiles == 0) panel = panel == G::kPanelSlots - 1 ? 0 : panel + 1;
+    op.load_scales(next_kt, panel_ptr(), wn, wt, next_scale);
+    op.template load_step<0>(stage_ptr(stage), panel_ptr(), wn, wt, frag[0]);
+    if (!unit) last_step();
+    kt = next_kt;
   }
 }
 
@@ -813,10 +938,10 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
 static int64_t max_tiles(int64_t P, int64_t E, int64_t bt) { return P / bt + (E < P ? E : P); }
 
 // PerCu workgroups a compute unit, or as many as there may be units.
-template <class Op, int S, int PerCu>
-static hipError_t launch_grid(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+template <class Op, int S, int PerCu, int YT>
+static hipError_t launch_grid_as(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
   using G = MxGrid<Op, S>;
-  auto* f = k_mx4_grid<Op, S, Op::NW * PerCu / 4>;
+  auto* f = k_mx4_grid<Op, S, Op::NW * PerCu / 4, YT>;
   static_assert(G::kLds * PerCu <= 160 * 1024, "LDS");
   static std::atomic<uint64_t> done{0};
   hipError_t e = lds_limit_once(reinterpret_cast<const void*>(f), G::kLds, done);
@@ -826,6 +951,13 @@ static hipError_t launch_grid(const Mx4ExpertArgs& A, int cus, hipStream_t s, co
   const int64_t most = ((int64_t)cus * PerCu + 7) / 8 * 8, want = (units + 7) / 8 * 8;
   MOE_LAUNCH(f, dim3((unsigned)(want < most ? want : most)), dim3(64 * Op::NW), G::kLds, s, kt.start, kt.stop, A);
   return hipGetLastError();
+}
+
+template <class Op, int S, int PerCu>
+static hipError_t launch_grid(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+  if (A.y_type == kMxTypeF32) return launch_grid_as<Op, S, PerCu, kMxTypeF32>(A, cus, s, kt);
+  if (A.y_type == kMxTypeMx4) return launch_grid_as<Op, S, PerCu, kMxTypeMx4>(A, cus, s, kt);
+  return launch_grid_as<Op, S, PerCu, kMxTypeBf16>(A, cus, s, kt);
 }
 
 // Stages: a tile has to be at least S - 1 K tiles long, so that a tile's rows are in LDS when the loads get to it,
@@ -838,28 +970,25 @@ static hipError_t tile_mx4(const Mx4ExpertArgs& A, int cus, hipStream_t s, const
 
 template <int BN, int BT, int WN, int WT, int S, int PerCu, bool Ragged>
 static hipError_t tile_bf16(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
-  return A.swiglu ? launch_grid<MxOp16<BN, BT, WN, WT, true, Ragged>, S, PerCu>(A, cus, s, kt)
-                  : launch_grid<MxOp16<BN, BT, WN, WT, false, Ragged>, S, PerCu>(A, cus, s, kt);
+  constexpr int ST = BT == 32 ? 1 : 4;
+  return A.swiglu ? launch_grid<MxOp16<BN, BT, WN, WT, true, Ragged, ST>, S, PerCu>(A, cus, s, kt)
+                  : launch_grid<MxOp16<BN, BT, WN, WT, false, Ragged, ST>, S, PerCu>(A, cus, s, kt);
 }
 
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
   const int64_t n_out = A.swiglu ? A.n / 2 : A.n, avg = A.P / A.E;
-  const bool dwords = ((reinterpret_cast<uintptr_t>(A.w_scales) | reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 3) == 0;
+  // Scales by 16 bytes, two or four K tiles at a time, where every row of them allows it.
+  const bool ragged = A.k % 512 != 0 || ((reinterpret_cast<uintptr_t>(A.w_scales) |
+                                          reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 15) != 0;
   if (A.x_mx4 && avg >= 64) {
-    if (!dwords || A.k % 256) return tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
+    if (ragged) return tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
     if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
-    if (A.k <= 256) return tile_mx4<256, 128, 4, 2, 2, 1, false>(A, cus, s, kt);
     return tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
   }
   if (!A.x_mx4 && avg >= 12) {
-    const bool ragged = !dwords || A.k % 128, two = A.k <= 128;
     if (avg >= 64)
-      return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt)
-             : two  ? tile_bf16<256, 128, 4, 2, 2, 1, false>(A, cus, s, kt)
-                    : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
-    return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt)
-           : two  ? tile_bf16<256, 32, 4, 1, 2, 2, false>(A, cus, s, kt)
-                  : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
+      return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
   }
   const int64_t grid = max_tiles(A.P, A.E, 16) * ((n_out + kFewCols - 1) / kFewCols);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
