@@ -25,17 +25,26 @@ struct MxTile {
 // every wave from the offsets alone: lane l sums the tiles of E/64 consecutive
 // experts, a scan over the lanes gives each its first tile.  Offsets are held
 // inside [0, P] and made increasing, so that whatever they are no position
-// outside the arrays is reached.
+// outside the arrays is reached.  The loads do not wait for each other: this
+// stands before everything else a small call does.
 template <int BT>
 __device__ __forceinline__ bool mx4_find_tile(const int32_t* __restrict__ offsets, int E, int P, int tile, MxTile* out) {
   const int lane = threadIdx.x & 63;
-  const int per = (E + 63) >> 6;
+  const int per = (E + 63) >> 6;  // at most 8
   const int e0 = lane * per;
-  int mine = 0;
-  for (int j = 0; j < per; j++) {
-    if (e0 + j >= E) break;
-    const int lo = min(max(offsets[e0 + j], 0), P), hi = min(max(offsets[e0 + j + 1], lo), P);
-    mine += (hi - lo + BT - 1) / BT;
+  int off[9];
+#pragma unroll
+  for (int j = 0; j <= 8; j++)
+    if (j <= per) off[j] = offsets[min(e0 + j, E)];  // past the last expert: no tiles
+  int n[8], mine = 0;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    n[j] = 0;
+    if (j < per) {
+      const int lo = min(max(off[j], 0), P), hi = min(max(off[j + 1], lo), P);
+      n[j] = (hi - lo + BT - 1) / BT;
+    }
+    mine += n[j];
   }
   int end = mine;
 #pragma unroll
@@ -43,24 +52,20 @@ __device__ __forceinline__ bool mx4_find_tile(const int32_t* __restrict__ offset
     const int v = __shfl_up(end, d);
     if (lane >= d) end += v;
   }
-  int first = end - mine;
+  const int first = end - mine;
   const uint64_t hit = __ballot(tile >= first && tile < end);
   if (hit == 0) return false;
   const int owner = __builtin_ctzll(hit);
-  int e = 0, row = 0, rows = 0;
-  if (lane == owner) {
-    for (int j = 0; j < per; j++) {
-      if (e0 + j >= E) break;
-      const int lo = min(max(offsets[e0 + j], 0), P), hi = min(max(offsets[e0 + j + 1], lo), P);
-      const int n = (hi - lo + BT - 1) / BT;
-      if (tile < first + n) {
-        e = e0 + j;
-        row = lo + (tile - first) * BT;
-        rows = min(hi - row, BT);
-        break;
-      }
-      first += n;
+  int e = 0, row = 0, rows = 0, t = tile - first;
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    if (t >= 0 && t < n[j]) {
+      const int lo = min(max(off[j], 0), P), hi = min(max(off[j + 1], lo), P);
+      e = e0 + j;
+      row = lo + t * BT;
+      rows = min(hi - row, BT);
     }
+    t -= n[j];
   }
   out->e = __builtin_amdgcn_readlane(e, owner);
   out->row = __builtin_amdgcn_readlane(row, owner);
@@ -88,75 +93,79 @@ __device__ __forceinline__ i32x8_t mx4_operand(uint4 v) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows an expert: a workgroup of four waves takes 32 output columns of one
-// tile of 16 positions.  The waves split K (chunks of 128 columns in turn) and
-// their sums are joined through LDS in a fixed order.  Weights go straight
-// from memory to registers, 16 bytes a lane: lane (r, q) holds block q of row
-// r of a chunk, which is the operand layout of the 16x16x128 instruction.
-// bf16 rows: the block's 32 weights are converted (exactly) to bf16 and go
-// through four 16x16x32 instructions; both operands number the columns of the
-// block the same way, so their order inside an instruction does not matter.
+// Few rows an expert: a wave takes 32 output columns of one tile of 16
+// positions.  Weights go straight from memory to registers, 16 bytes a lane:
+// lane (r, q) holds block q of row r of a chunk of 128 columns, which is the
+// operand layout of the 16x16x128 instruction.  bf16 rows: the block's 32
+// weights are converted (exactly) to bf16 and go through four 16x16x32
+// instructions; both operands number the columns of the block the same way, so
+// their order inside an instruction does not matter.
+//
+// Split: the four waves of a workgroup share the columns and split K (chunks
+// in turn), and their sums are joined through LDS in a fixed order; otherwise
+// they take 32 columns each and all of K.  A single token's call has so few
+// columns that only the first fills the device; with more tiles it would only
+// pay the way to the tile (offsets, src) four times as often.
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 32;
 
-template <bool XMx, bool Swiglu>
+template <bool XMx, bool Swiglu, bool Split>
 __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
   constexpr int kFrag = Swiglu ? 4 : 2;  // 16-row weight fragments: columns (, then the up half's)
-  __shared__ float red[4][kFrag * 4][64];
+  constexpr int kCols = Split ? kFewCols : 4 * kFewCols, kStep = Split ? 4 : 1;
+  __shared__ float red[Split ? 4 : 1][kFrag * 4][64];
   const int n_out = Swiglu ? A.n >> 1 : A.n;
-  const int cols = (n_out + kFewCols - 1) / kFewCols;
-  const int tile = blockIdx.x / cols, n0 = (blockIdx.x - tile * cols) * kFewCols;
+  const int cols = (n_out + kCols - 1) / kCols;
+  const int tile = blockIdx.x / cols, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int n0 = (blockIdx.x - tile * cols) * kCols + (Split ? 0 : wave * kFewCols);
   MxTile t;
   if (!mx4_find_tile<16>(A.offsets, A.E, A.P, tile, &t)) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (!Split && n0 >= n_out) return;
   const int r = lane & 15, q = lane >> 4;
   const int nb = A.k >> 5;  // blocks a row
 
   const int pos = t.row + r;
   const int src = r < t.rows ? mx4_src(A, pos) : -1;
+  const int dst = r < t.rows ? mx4_dst(A, pos) : -1;
+  const float factor = A.row_scale && dst >= 0 ? A.row_scale[dst] : 1.f;
   const uint8_t* wc[kFrag];
   const uint8_t* ws[kFrag];
-  bool live[kFrag];
 #pragma unroll
   for (int f = 0; f < kFrag; f++) {
-    const int c = n0 + (f & 1) * 16 + r;
-    live[f] = c < n_out;
-    const int64_t row = (int64_t)t.e * A.n + (f >= 2 ? n_out : 0) + (live[f] ? c : 0);
+    // A column past the last one reads the last one's weights and is not stored.
+    const int c = min(n0 + (f & 1) * 16 + r, n_out - 1);
+    const int64_t row = (int64_t)t.e * A.n + (f >= 2 ? n_out : 0) + c;
     wc[f] = A.w_codes + row * nb * kMxBlockBytes;
     ws[f] = A.w_scales + row * nb;
   }
+  const int64_t xrow = (int64_t)max(src, 0) * nb;
   f32x4_t acc[kFrag] = {};
-  for (int c = wave; c * 4 < nb; c += 4) {
-    const int b = c * 4 + q;
-    const bool in = b < nb;
+  for (int c = Split ? wave : 0; c * 4 < nb; c += kStep) {
+    // A block past the row's end is read as the last one and multiplied as zeros.
+    const int b = min(c * 4 + q, nb - 1);
+    const bool in = c * 4 + q < nb;
     uint4 w[kFrag];
     uint32_t s[kFrag];
 #pragma unroll
     for (int f = 0; f < kFrag; f++) {
-      w[f] = make_uint4(0, 0, 0, 0);
-      s[f] = 127;
-      if (in && live[f]) {
-        w[f] = *reinterpret_cast<const uint4*>(wc[f] + b * kMxBlockBytes);
-        s[f] = ws[f][b];
-      }
+      w[f] = *reinterpret_cast<const uint4*>(wc[f] + b * kMxBlockBytes);
+      s[f] = ws[f][b];
     }
     if constexpr (XMx) {
-      uint4 x = make_uint4(0, 0, 0, 0);
-      uint32_t xs = 127;
-      if (in && src >= 0) {
-        x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(A.x) + ((int64_t)src * nb + b) * kMxBlockBytes);
-        xs = A.x_scales[(int64_t)src * nb + b];
-      }
+      uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(A.x) + (xrow + b) * kMxBlockBytes);
+      uint32_t xs = A.x_scales[xrow + b];
+      if (!in) x = make_uint4(0, 0, 0, 0), xs = 127;
 #pragma unroll
       for (int f = 0; f < kFrag; f++)
         acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(mx4_operand(w[f]), mx4_operand(x), acc[f], kE2m1,
-                                                                  kE2m1, 0, s[f], 0, xs);
+                                                                  kE2m1, 0, in ? s[f] : 127, 0, xs);
     } else {
-      uint4 x[4] = {};
-      if (in && src >= 0) {
-        const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.x) + (int64_t)src * A.k + b * 32);
+      const uint4* xp = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(A.x) + (xrow + b) * 32);
+      uint4 x[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) x[j] = xp[j];
+      for (int j = 0; j < 4; j++) {
+        x[j] = xp[j];
+        if (!in) x[j] = make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int f = 0; f < kFrag; f++) {
@@ -164,30 +173,31 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 #pragma unroll
         for (int j = 0; j < 4; j++)
           acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8_t, mx4_unpack8_bf16(d[j], mx4_scale_f32(s[f]))),
+              __builtin_bit_cast(bf16x8_t, mx4_unpack8_bf16(d[j], mx4_scale_f32(in ? s[f] : 127))),
               __builtin_bit_cast(bf16x8_t, x[j]), acc[f], 0, 0, 0);
       }
     }
   }
-#pragma unroll
-  for (int f = 0; f < kFrag; f++)
-#pragma unroll
-    for (int i = 0; i < 4; i++) red[wave][f * 4 + i][lane] = acc[f][i];
-  __syncthreads();
-
-  // Wave 0 joins the sums: lane (r, q) has position r, columns 16 f + 4 q + i.
-  if (wave != 0) return;
+  // Lane (r, q) has position r, columns 16 f + 4 q + i.
   float z[kFrag * 4];
+  if constexpr (Split) {
 #pragma unroll
-  for (int i = 0; i < kFrag * 4; i++) z[i] = (red[0][i][lane] + red[1][i][lane]) + (red[2][i][lane] + red[3][i][lane]);
+    for (int f = 0; f < kFrag; f++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) red[wave][f * 4 + i][lane] = acc[f][i];
+    __syncthreads();
+    if (wave != 0) return;
+#pragma unroll
+    for (int i = 0; i < kFrag * 4; i++) z[i] = (red[0][i][lane] + red[1][i][lane]) + (red[2][i][lane] + red[3][i][lane]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kFrag * 4; i++) z[i] = acc[i >> 2][i & 3];
+  }
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) v[i] = Swiglu ? silu_mul(z[i], z[i + (kFrag - 2) * 4]) : z[i];
-  const int dst = r < t.rows ? mx4_dst(A, pos) : -1;
-  if (A.row_scale && dst >= 0) {
-    const float w = A.row_scale[dst];
-#pragma unroll
-    for (int i = 0; i < 8; i++) v[i] *= w;
+  for (int i = 0; i < 8; i++) {
+    v[i] = (Swiglu ? silu_mul(z[i], z[i + (kFrag - 2) * 4]) : z[i]) * factor;
+    if (src < 0) v[i] = 0.f;
   }
   if (A.y_type == kMxTypeMx4) {
     // The block's 32 columns are 8 in each of the lanes r, r + 16, r + 32, r + 48.
@@ -207,6 +217,22 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
     return;
   }
   if (dst < 0) return;
+  // Four columns at once where rows of y begin at a multiple of them.
+  if (n_out % 4 == 0 && (reinterpret_cast<uintptr_t>(A.y) & 15) == 0) {
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+      const int c = n0 + g * 16 + 4 * q;
+      if (c >= n_out) continue;
+      const int64_t at = (int64_t)dst * n_out + c;
+      const float* u = v + 4 * g;
+      if (A.y_type == kMxTypeF32)
+        *reinterpret_cast<float4*>(static_cast<float*>(A.y) + at) = make_float4(u[0], u[1], u[2], u[3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(A.y) + at) =
+            make_uint2(f32_to_bf16_bits(u[0]) | f32_to_bf16_bits(u[1]) << 16, f32_to_bf16_bits(u[2]) | f32_to_bf16_bits(u[3]) << 16);
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < 8; i++) {
     const int c = n0 + (i >> 2) * 16 + 4 * q + (i & 3);
@@ -985,15 +1011,23 @@ hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, co
     if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
     return tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
   }
+  if (A.x_mx4 && avg >= 12)
+    return ragged ? tile_mx4<256, 64, 4, 1, 2, 1, true>(A, cus, s, kt) : tile_mx4<256, 64, 4, 1, 3, 1, false>(A, cus, s, kt);
   if (!A.x_mx4 && avg >= 12) {
     if (avg >= 64)
       return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
     return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
   }
-  const int64_t grid = max_tiles(A.P, A.E, 16) * ((n_out + kFewCols - 1) / kFewCols);
+  const int64_t tiles = max_tiles(A.P, A.E, 16), wide_grid = tiles * ((n_out + 4 * kFewCols - 1) / (4 * kFewCols));
+  const bool split = wide_grid < 2 * cus;
+  const int64_t grid = split ? tiles * ((n_out + kFewCols - 1) / kFewCols) : wide_grid;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  auto* f = A.x_mx4 ? (A.swiglu ? k_mx4_few<true, true> : k_mx4_few<true, false>)
-                    : (A.swiglu ? k_mx4_few<false, true> : k_mx4_few<false, false>);
+  auto pick = [&](auto sp) {
+    constexpr bool Sp = sp.value;
+    return A.x_mx4 ? (A.swiglu ? k_mx4_few<true, true, Sp> : k_mx4_few<true, false, Sp>)
+                   : (A.swiglu ? k_mx4_few<false, true, Sp> : k_mx4_few<false, false, Sp>);
+  };
+  auto* f = split ? pick(std::true_type{}) : pick(std::false_type{});
   MOE_LAUNCH(f, dim3((unsigned)grid), dim3(256), 0, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
