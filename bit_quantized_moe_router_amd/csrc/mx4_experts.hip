@@ -856,7 +856,10 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
 
   const int wn = wave % Op::WN, wt = wave / Op::WN;
   f32x16_t acc[Op::FN][Op::FT] = {};
-  typename Op::Frags frag[2];
+  // Operands are read one step ahead, or two where registers allow it: the barrier between K tiles then stands
+  // amid the steps, with two steps' products behind it for the next tile's first reads to hide under.
+  constexpr bool kTwo = Op::kSteps == 4 && Op::FN * Op::FT <= 4;
+  typename Op::Frags frag[kTwo ? 4 : 2];
   typename Op::Scales scale, next_scale;
   auto stage_ptr = [&](int i) { return sm + i * Op::kStage; };
   int panel = 0;
@@ -887,6 +890,7 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
   arrive(n_it - 1);
   op.load_scales(0, panel_ptr(), wn, wt, next_scale);
   op.template load_step<0>(stage_ptr(0), panel_ptr(), wn, wt, frag[0]);
+  if constexpr (kTwo) op.template load_step<1>(stage_ptr(0), panel_ptr(), wn, wt, frag[1]);
   int stage = 0, kt = 0;
   for (int it = 0; it < n_it; it++) {
     uint8_t* st = stage_ptr(stage);
@@ -905,35 +909,42 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
         issue(s3);
       }
     }
-    // While a step is multiplied the next one's operands are read.
-    auto step = [&](auto sc) {
-      constexpr int s = sc.value;
-      op.template load_step<s + 1>(st, panel_ptr(), wn, wt, frag[(s + 1) & 1]);
-      if (S > 2 && more) issue(sc);
+    auto mul = [&](auto sc) {
       __builtin_amdgcn_sched_barrier(0);
-      op.template mul_step<s>(kt, frag[s & 1], scale, acc);
+      op.template mul_step<sc.value>(kt, frag[kTwo ? sc.value : sc.value & 1], scale, acc);
       computed(acc);
     };
-    step(s0);
-    if constexpr (Op::kSteps == 4) {
-      step(s1);
-      step(s2);
-      if (S > 2 && more) issue(s3);
+    if constexpr (kTwo) {
+      op.template load_step<2>(st, panel_ptr(), wn, wt, frag[2]);
+      if (S > 2 && more) issue(s0), issue(s1);
+      mul(s0);
+      op.template load_step<3>(st, panel_ptr(), wn, wt, frag[3]);
+      if (S > 2 && more) issue(s2), issue(s3);
+      mul(s1);
     } else {
-      if (S > 2 && more) issue(s1);
+      auto step = [&](auto sc) {
+        constexpr int s = sc.value;
+        op.template load_step<s + 1>(st, panel_ptr(), wn, wt, frag[(s + 1) & 1]);
+        if (S > 2 && more) issue(sc);
+        mul(sc);
+      };
+      step(s0);
+      if constexpr (Op::kSteps == 4) {
+        step(s1);
+        step(s2);
+        if (S > 2 && more) issue(s3);
+      } else {
+        if (S > 2 && more) issue(s1);
+      }
     }
     if (more) end_();
-    auto last_step = [&] {
-      __builtin_amdgcn_sched_barrier(0);
-      op.template mul_step<Op::kSteps - 1>(kt, frag[1], scale, acc);
-      computed(acc);
-    };
-    // The last step's operands are in registers: when every wave is here, this stage is free and the next
-    // one is complete.  Its first operands are read during the last step; but at a unit's end the results go
+    // The last steps' operands are in registers: when every wave is here, this stage is free and the next
+    // one is complete.  Its first operands are read during the last steps; but at a unit's end the results go
     // out through this stage first.
     arrive(n_it - 2 - it);
     if (unit) {
-      last_step();
+      if constexpr (kTwo) mul(s2);
+      mul(std::integral_constant<int, Op::kSteps - 1>{});
       mx4_store_tile<YT, Op::FN, Op::FT, G::kStore, BT, Op::Swiglu>(
           A, acc, n_out, out_col * kCols + wn * (kCols / Op::WN), rows3[tile0.slot], fac2 + tile0.turn * BT, tile0.row,
           min(tile0.hi - tile0.row, BT),
@@ -955,7 +966,11 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
     if (next_kt % Op::kScaleTiles == 0) panel = panel == G::kPanelSlots - 1 ? 0 : panel + 1;
     op.load_scales(next_kt, panel_ptr(), wn, wt, next_scale);
     op.template load_step<0>(stage_ptr(stage), panel_ptr(), wn, wt, frag[0]);
-    if (!unit) last_step();
+    if constexpr (kTwo) {
+      if (!unit) mul(s2);
+      op.template load_step<1>(stage_ptr(stage), panel_ptr(), wn, wt, frag[1]);
+    }
+    if (!unit) mul(std::integral_constant<int, Op::kSteps - 1>{});
     kt = next_kt;
   }
 }
@@ -963,7 +978,9 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
 // Tiles of BT positions that E experts with P positions in all can have.
 static int64_t max_tiles(int64_t P, int64_t E, int64_t bt) { return P / bt + (E < P ? E : P); }
 
-// PerCu workgroups a compute unit, or as many as there may be units.
+// PerCu workgroups a compute unit, or as many as there may be units.  Tiles of
+// 32 positions: twice that many, as their units are few and short: 67 against
+// 73 us for 512 tokens' gate/up, where 512 workgroups have 2 or 3 units each.
 template <class Op, int S, int PerCu, int YT>
 static hipError_t launch_grid_as(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
   using G = MxGrid<Op, S>;
@@ -974,7 +991,7 @@ static hipError_t launch_grid_as(const Mx4ExpertArgs& A, int cus, hipStream_t s,
   if (e != hipSuccess) return e;
   const int64_t n_out = Op::Swiglu ? A.n / 2 : A.n;
   const int64_t units = max_tiles(A.P, A.E, Op::BT) * ((n_out + G::kCols - 1) / G::kCols);
-  const int64_t most = ((int64_t)cus * PerCu + 7) / 8 * 8, want = (units + 7) / 8 * 8;
+  const int64_t most = ((int64_t)cus * PerCu * (Op::BT == 32 ? 2 : 1) + 7) / 8 * 8, want = (units + 7) / 8 * 8;
   MOE_LAUNCH(f, dim3((unsigned)(want < most ? want : most)), dim3(64 * Op::NW), G::kLds, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
