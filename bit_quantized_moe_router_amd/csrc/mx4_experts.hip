@@ -6,6 +6,7 @@
 //
 // The weights are the matrix instructions' first operand, so that a lane of
 // the result holds one row of x and four consecutive columns of y.
+#include <cmath>
 #include <type_traits>
 
 #include "launch.h"
@@ -1018,22 +1019,60 @@ static hipError_t tile_bf16(const Mx4ExpertArgs& A, int cus, hipStream_t s, cons
                   : launch_grid<MxOp16<BN, BT, WN, WT, false, Ragged, ST>, S, PerCu>(A, cus, s, kt);
 }
 
+// The kernels' times in us, from sizes alone, to choose the shortest.  Fitted to
+// 156 products on 256 compute units: one matrix with 16 to 2048 rows, n = 256 to
+// 4096, K = 512 to 8192, and 16 to 256 experts with up to 256 rows each.  Over
+// those the choice is 1% slower than the best one on average and 21% at most.
+// Both sides, measured us: 4-bit x, 1024 x 4096 x 2048 few 88, tiles of 128
+// positions 17; 256 x 1024 x 2048 few 9, tiles 14; 256 experts with 4 rows each,
+// n = 1024, K = 2048: few 77, tiles 58.  bf16 x, 64 experts with 8 rows each,
+// n = 1024, K = 2048: few 30, tiles of 32 positions 24, of 128 36; 2048 x 4096 x
+// 8192: few 893, 32 positions 203, 128 x 128 156, 256 x 128 132.
+struct MxCost {
+  double P, E, n, K;
+  bool ragged;
+  double start;  // a workgroup's way to its first products: offsets, src and dst, factors
+  // Tiles of bt positions, for positions spread evenly over the experts.
+  double tiles(double bt) const {
+    if (E == 1) return std::ceil(P / bt);
+    const double active = E * (1.0 - std::exp(-P / E)), avg = P / active;
+    return avg <= bt ? active : P / bt + active / 2;
+  }
+  // 16 x 32 products over 128 columns go by at `rate` a us; one wave's chain takes `chain` us a column.
+  double few(double rate, double chain) const {
+    return std::fmax(4.0 + K * chain, 1.0 + tiles(16) * std::ceil(n / 32) * std::ceil(K / 128) / rate);
+  }
+  // A K tile of kt columns takes lo us, or hi where the other compute units are at work too; a unit `own` us more.
+  // slots: units under way at one time.
+  double grid(double bn, double bt, double kt, double lo, double hi, double own, double slots) const {
+    const double units = tiles(bt) * std::ceil(n / bn), full = std::fmin(1.0, units / slots);
+    const double tile = (lo + (hi - lo) * full) * (ragged ? 1.5 : 1.0);
+    return start + std::ceil(units / slots) * (std::ceil(K / kt) * tile + own);
+  }
+};
+
 hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
-  const int64_t n_out = A.swiglu ? A.n / 2 : A.n, avg = A.P / A.E;
+  const int64_t n_out = A.swiglu ? A.n / 2 : A.n;
   // Scales by 16 bytes, two or four K tiles at a time, where every row of them allows it.
   const bool ragged = A.k % 512 != 0 || ((reinterpret_cast<uintptr_t>(A.w_scales) |
                                           reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 15) != 0;
-  if (A.x_mx4 && avg >= 64) {
-    if (ragged) return tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
-    if (A.P >= 1024 && A.E == 1) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
-    return tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
-  }
-  if (A.x_mx4 && avg >= 12)
-    return ragged ? tile_mx4<256, 64, 4, 1, 2, 1, true>(A, cus, s, kt) : tile_mx4<256, 64, 4, 1, 3, 1, false>(A, cus, s, kt);
-  if (!A.x_mx4 && avg >= 12) {
-    if (avg >= 64)
+  const MxCost C{(double)A.P, (double)A.E, (double)A.n, (double)A.k, ragged,
+                 5.0 + (A.src_rows || A.dst_rows ? 2 : 0) + (A.row_scale ? 2 : 0)};
+  if (A.x_mx4) {
+    const double few = C.few(1550 / 256.0 * cus, 1.1e-3), mid = C.grid(256, 128, 256, 1.05, 1.4, 1.7, cus);
+    const double big = ragged ? 1e30 : C.grid(256, 256, 256, 1.7, 2.4, 1.7, cus);
+    if (big < few && big < mid) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
+    if (mid < few)
+      return ragged ? tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+  } else {
+    const double few = C.few(1130 / 256.0 * cus, 1.6e-3), low = C.grid(256, 32, 128, 0.7, 1.6, 1.0, 2 * cus);
+    const double mid = ragged ? 1e30 : C.grid(128, 128, 128, 0.86, 1.2, 1.0, cus);
+    const double big = C.grid(256, 128, 128, 1.4, 2.0, 1.0, cus);
+    if (low < few && low <= mid && low <= big)
+      return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
+    if (mid < few && mid <= big) return tile_bf16<128, 128, 2, 4, 3, 1, false>(A, cus, s, kt);
+    if (big < few)
       return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
-    return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
   }
   const int64_t tiles = max_tiles(A.P, A.E, 16), wide_grid = tiles * ((n_out + 4 * kFewCols - 1) / (4 * kFewCols));
   const bool split = wide_grid < 2 * cus;
