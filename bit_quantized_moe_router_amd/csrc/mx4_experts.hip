@@ -741,7 +741,8 @@ __global__ __launch_bounds__(64 * Op::NW, Occ) void k_mx4_grid(Mx4ExpertArgs A) 
     const int v = __shfl_up(end, d);
     if (lane >= d) end += v;
   }
-  const int units = __builtin_amdgcn_readlane(end, 63) * cols;  // below 2^28: P <= 2^24, n <= 2^16
+  // Rising offsets have no more tiles than that; below 2^28 units, as P <= 2^24 and n <= 2^16.
+  const int units = min(__builtin_amdgcn_readlane(end, 63), A.P / BT + min(E, A.P)) * cols;
   // Workgroup b runs on XCD b % 8: consecutive ranges of units to the workgroups of one XCD.
   const int n_wg = gridDim.x, wg = (blockIdx.x & 7) * (n_wg >> 3) + (blockIdx.x >> 3);  // n_wg is a multiple of 8
   auto cut = [&](int x) { return units / n_wg * x + units % n_wg * x / n_wg; };
@@ -1040,7 +1041,7 @@ struct MxCost {
   }
   // 16 x 32 products over 128 columns go by at `rate` a us; one wave's chain takes `chain` us a column.
   double few(double rate, double chain) const {
-    return std::fmax(4.0 + K * chain, 1.0 + tiles(16) * std::ceil(n / 32) * std::ceil(K / 128) / rate);
+    return std::fmax(4.0 + K * chain, 2.0 + tiles(16) * std::ceil(n / 32) * std::ceil(K / 128) / rate);
   }
   // A K tile of kt columns takes lo us, or hi where the other compute units are at work too; a unit `own` us more.
   // slots: units under way at one time.

@@ -38,32 +38,36 @@ def dequantize(codes, scales):
 
 
 def experts(w, x, offsets, src, dst, row_scale, y_rows, swiglu):
-    """w [E, n, k], x [x_rows, k] float64; src[i], dst[i] rows or out of range.
+    """w[e] [n, k], x [x_rows, k] float64; src[i], dst[i] rows or out of range.
     -> y [y_rows, n_out] (NaN: not written), and a bound of its fp32 rounding errors."""
-    E, n, K = w.shape
+    n, K = w[0].shape
     n_out = n // 2 if swiglu else n
     y = np.full((y_rows, n_out), np.nan)
     err = np.zeros((y_rows, n_out))
     u = 2.0 ** -24
-    for e in range(E):
-        for i in range(offsets[e], offsets[e + 1]):
-            if not 0 <= dst[i] < y_rows:
-                continue
-            row = x[src[i]] if 0 <= src[i] < len(x) else np.zeros(K)
-            z = w[e] @ row
-            # K exact products summed in fp32 in some order: K roundings, each of at most one step (2 u)
-            # of a partial sum that sum |w x| bounds.
-            dz = 2 * (K + 8) * u * (np.abs(w[e]) @ np.abs(row))
-            if swiglu:
-                g, p, dg, dp = z[:n_out], z[n_out:], dz[:n_out], dz[n_out:]
+    for e in range(len(offsets) - 1):
+        i = np.arange(offsets[e], offsets[e + 1])
+        i = i[(0 <= dst[i]) & (dst[i] < y_rows)]
+        if len(i) == 0:
+            continue
+        there = (0 <= src[i]) & (src[i] < len(x))
+        rows, to, we = np.where(there[:, None], x[np.where(there, src[i], 0)], 0), dst[i], w[e].T
+        z = rows @ we
+        # K exact products summed in fp32 in some order: K roundings, each of at most one step (2 u)
+        # of a partial sum that sum |w x| bounds.
+        dz = 2 * (K + 8) * u * (np.abs(rows) @ np.abs(we))
+        if swiglu:
+            g, p, dg, dp = z[:, :n_out], z[:, n_out:], dz[:, :n_out], dz[:, n_out:]
+            with np.errstate(over="ignore"):
                 s = g / (1 + np.exp(-g))
-                h = s * p
-                # |silu'| <= 1.1; exp and reciprocal instructions a few steps, exp's argument |g| steps more.
-                dh = 1.1 * dg * (np.abs(p) + dp) + np.abs(s) * dp + (16 + 4 * np.abs(g)) * u * np.abs(h)
-                z, dz = h, dh
-            if row_scale is not None:
-                z, dz = z * row_scale[dst[i]], dz * np.abs(row_scale[dst[i]]) + u * np.abs(z * row_scale[dst[i]])
-            y[dst[i]], err[dst[i]] = z, dz
+            h = s * p
+            # |silu'| <= 1.1; exp and reciprocal instructions a few steps, exp's argument |g| steps more.
+            dh = 1.1 * dg * (np.abs(p) + dp) + np.abs(s) * dp + (16 + 4 * np.abs(g)) * u * np.abs(h)
+            z, dz = h, dh
+        if row_scale is not None:
+            f = row_scale[to].astype(np.float64)[:, None]
+            z, dz = z * f, dz * np.abs(f) + u * np.abs(z * f)
+        y[to], err[to] = z, dz
     return y, err
 
 

@@ -214,11 +214,21 @@ def test_storage_offsets_past_32_bits(gpu):
 # ---- the expert product ------------------------------------------------------------------------------------
 
 
+class Experts:
+    """Weights [E, n, k] by their codes, read back an expert at a time."""
+
+    def __init__(self, codes, scales, E):
+        self.codes, self.scales = codes.reshape(E, -1, codes.shape[-1]), scales.reshape(E, -1, scales.shape[-1])
+
+    def __getitem__(self, e):
+        return ref.dequantize(self.codes[e], self.scales[e])
+
+
 class Product:
     """Weights, rows and routing of one call, on the CPU and the GPU."""
 
     def __init__(self, gpu, counts, n, k, x_kind, seed, x_rows=None, src=None, src_div=1, dst=None, y_rows=None,
-                 row_scale=False, slack=0):
+                 row_scale=False, slack=0, random_codes=False):
         rng = np.random.default_rng(seed)
         E = len(counts)
         self.E, self.n, self.k, self.x_kind = E, n, k, x_kind
@@ -227,9 +237,12 @@ class Product:
         self.rows = self.used + slack  # positions behind the last expert's range belong to nobody
         self.x_rows = x_rows or self.rows
         self.y_rows = y_rows or self.rows
-        w = (rng.standard_normal((E * n, k)) * 0.05).astype(np.float32)
-        self.wc, self.ws = ref.quantize(w)
-        self.w = ref.dequantize(self.wc, self.ws).reshape(E, n, k)
+        if random_codes:
+            self.wc = rng.integers(0, 256, (E * n, k // 2), np.uint8)
+            self.ws = rng.integers(118, 126, (E * n, k // 32), np.uint8)
+        else:
+            self.wc, self.ws = ref.quantize((rng.standard_normal((E * n, k)) * 0.05).astype(np.float32))
+        self.w = Experts(self.wc, self.ws, E)
         x = torch.from_numpy((rng.standard_normal((self.x_rows, k)) * np.exp(rng.standard_normal((self.x_rows, 1)))
                               ).astype(np.float32)).bfloat16()
         self.src, self.src_div, self.dst = src, src_div, dst
@@ -356,6 +369,120 @@ def test_experts_offsets_are_held_inside(gpu):
     assert (p.run("f32", 0) == 7).all()
 
 
+def around(E, rows, seed):
+    """Counts of E experts, `rows` on average, some of them none."""
+    c = np.random.default_rng(seed).integers(0, 2 * rows + 1, E)
+    c[E // 3] = 0
+    return c
+
+
+# Sizes large enough for the kernels with tiles of their own shapes: experts' positions, n, k.  k that is no multiple
+# of 512, down to a single block, takes their forms for odd lengths.
+TILED = [
+    ("mx4", [150, 0, 1, 300, 129, 400], 4098, 512),   # 256 x 128
+    ("mx4", around(300, 30, 1), 256, 512),            # several tiles of one unit a workgroup
+    ("mx4", [700, 3, 1200, 900], 2112, 1536),
+    ("mx4", [2050], 4100, 512),                       # 256 x 256
+    ("mx4", [4000, 0, 1900, 257, 2500], 2112, 512),
+    ("mx4", [1300], 4100, 32),                        # 256 x 128, odd
+    ("mx4", [700, 1, 1400, 900], 2112, 288),
+    ("mx4", [900, 1, 0, 140], 4098, 544),
+    ("bf16", [200], 4100, 1024),                      # 256 x 32
+    ("bf16", around(64, 8, 2), 4100, 512),
+    ("bf16", around(300, 30, 3), 1026, 32),           # the same, odd
+    ("bf16", [600, 0, 33, 300], 4098, 160),
+    ("bf16", [4100], 258, 512),                       # 128 x 128
+    ("bf16", [500, 0, 1, 129, 1400], 1056, 1024),
+    ("bf16", around(40, 70, 4), 1058, 512),           # 256 x 128
+    ("bf16", [2100], 2112, 1536),
+    ("bf16", [300, 0, 1, 640], 4224, 32),             # the same, odd
+    ("bf16", [1500, 130, 1700], 2050, 544),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("swiglu", [0, 1])
+@pytest.mark.parametrize("x_kind,counts,n,k", TILED, ids=[f"{x}-{len(c)}x{sum(c)}-{n}-{k}" for x, c, n, k in TILED])
+def test_experts_tiled(gpu, x_kind, counts, n, k, swiglu):
+    Product(gpu, counts, n, k, x_kind, n + k, random_codes=True).check(swiglu)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_kind,counts,n,k", [
+    ("mx4", around(12, 170, 5), 2112, 512), ("mx4", around(6, 1100, 6), 2112, 512), ("mx4", around(12, 300, 7), 2112, 288),
+    ("bf16", around(64, 9, 8), 4160, 512), ("bf16", around(4, 500, 9), 4160, 160), ("bf16", around(6, 150, 10), 2112, 1024),
+    ("bf16", around(40, 70, 11), 2112, 512), ("bf16", around(6, 900, 12), 2112, 288)])
+def test_experts_tiled_gather_and_scatter(gpu, x_kind, counts, n, k):
+    """Sources by token, targets by assignment, factors, rows outside on either side and behind the last range."""
+    rng = np.random.default_rng(n + k + len(counts))
+    rows = int(sum(counts)) + 9
+    tokens = (rows + 2) // 3
+    src = rng.permutation(3 * tokens)[:rows]
+    src[rng.integers(0, rows, 20)] = rng.choice([-1, 3 * tokens, 1 << 30, -(1 << 31)], 20)
+    dst = rng.permutation(rows + 7)[:rows]
+    dst[rng.choice(rows, 20, replace=False)] = rng.choice([-1, rows + 7, 1 << 30, -(1 << 31)], 20)
+    p = Product(gpu, counts, n, k, x_kind, 13, x_rows=tokens, src=src, src_div=3, dst=dst, y_rows=rows + 7, row_scale=True,
+                slack=9, random_codes=True)
+    p.check(1)
+    p.check(0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_kind,rows,n,k", [("mx4", 1000, 2112, 512), ("mx4", 2304, 4100, 512), ("bf16", 200, 4100, 1024),
+                                             ("bf16", 1024, 2112, 512), ("bf16", 2304, 2112, 1536)])
+def test_experts_tiled_unaligned(gpu, x_kind, rows, n, k):
+    """Scales and results that begin at no multiple of 16 bytes."""
+    p = Product(gpu, [rows // 2, rows - rows // 2], n, k, x_kind, 14, random_codes=True)
+
+    def moved(t, by):
+        buf = torch.empty(t.numel() + by, dtype=t.dtype, device=gpu)
+        buf[by:].copy_(t.reshape(-1))
+        return buf[by:].view(t.shape)
+
+    want, err = p.want(0)
+    aligned = p.run("f32", 0)
+    y = moved(p.outputs("f32", 0)[0], 1)
+    p.call(y, None, "f32", 0)
+    assert torch.equal(y, aligned)
+    p.gws = moved(p.gws, 1)
+    if x_kind == "mx4":
+        p.gxs = moved(p.gxs, 2)
+    p.call(y, None, "f32", 0)
+    assert (np.abs(y.double().cpu().numpy() - want) <= err + 2.0 ** -24 * np.abs(want)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_kind,rows,n,k", [("mx4", 1000, 2112, 512), ("mx4", 2304, 4100, 512), ("mx4", 2304, 4100, 96),
+                                             ("bf16", 200, 4100, 1024), ("bf16", 1024, 2112, 512), ("bf16", 2304, 2112, 1536),
+                                             ("bf16", 900, 4100, 96)])
+def test_experts_tiled_nan_stays_in_its_row(gpu, x_kind, rows, n, k):
+    p = Product(gpu, [rows], n, k, x_kind, 15, random_codes=True)
+    clean = p.run("f32", 0)
+    if x_kind == "mx4":
+        p.gxs[1, 2] = 255
+    else:
+        p.gx[1, 70] = float("nan")
+    p.gws[5, 1] = 255  # a weight block: its column in every row
+    y = p.run("f32", 0)
+    rest, cols = torch.arange(rows, device=gpu) != 1, torch.arange(n, device=gpu) != 5
+    assert y[1].isnan().all() and y[:, 5].isnan().all()
+    assert torch.equal(y[rest][:, cols], clean[rest][:, cols])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_kind", ["bf16", "mx4"])
+def test_experts_tiled_offsets_are_held_inside(gpu, x_kind):
+    """Offsets that rise and fall or lie outside reach no memory outside the arrays."""
+    p = Product(gpu, [500] * 6, 2112, 512, x_kind, 16, random_codes=True)
+    p.run("f32", 0)
+    for off in ([0, 3000, 0, 3000, 0, 3000, 0], [-5, 1 << 30, 7, 7, -(1 << 31), 900, 1], [3000] * 7, [0] * 7):
+        p.goff = torch.tensor(off, dtype=torch.int32, device=gpu)
+        y = p.run("f32", 0)
+        assert y.isfinite().all()
+        if off[0] == off[-1]:
+            assert off[1] != off[0] or (y == 7).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("x_kind", ["bf16", "mx4"])
 def test_experts_many(gpu, x_kind):
@@ -363,6 +490,18 @@ def test_experts_many(gpu, x_kind):
     rng = np.random.default_rng(8)
     Product(gpu, rng.integers(0, 10, 512), 32, 64, x_kind, 5).check(0)
     Product(gpu, [0] * 511 + [50], 32, 64, x_kind, 6).check(0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("x_kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("n,k", [(64, 32), (192, 160), (322, 64)])
+def test_experts_many_swiglu(gpu, n, k, x_kind):
+    """512 experts with 0 to 9 rows: more tiles than compute units, columns shared out among the waves."""
+    rng = np.random.default_rng(n)
+    counts = rng.integers(0, 10, 512)
+    rows = int(counts.sum())
+    Product(gpu, counts, n, k, x_kind, 17, x_rows=rows // 2, src=rng.permutation(rows), src_div=2,
+            dst=rng.permutation(rows), row_scale=True).check(1)
 
 
 @pytest.mark.gpu
