@@ -137,8 +137,10 @@ struct Mx4ExpertArgs {
   uint8_t* y_scales;         // [y_rows][n_out / 32] with y_type = kMxTypeMx4
   int E, n, k, P, x_rows, y_rows, src_div, y_type;
   bool x_mx4, swiglu;
-  // r / src_div = (r * src_magic >> 32) >> src_shift for 0 <= r < 2^31, src_div >= 2: with L = ceil(log2 src_div),
-  // src_magic = floor(2^(31 + L) / src_div) + 1 is off by less than 2^L / src_div <= ... of a unit in 2^(31 + L).
+  // r / src_div = (r * src_magic >> 32) >> src_shift for 0 <= r < 2^31, src_div >= 2.  With L = ceil(log2 src_div),
+  // src_shift = L - 1 and src_magic = floor(2^(31 + L) / src_div) + 1, so src_magic * src_div = 2^(31 + L) + e with
+  // 0 < e <= src_div: the quotient is off by r e / (src_div 2^(31 + L)) < 2^-L <= 1 / src_div, too little to reach
+  // the next whole number.
   uint32_t src_magic;
   int src_shift;
 };

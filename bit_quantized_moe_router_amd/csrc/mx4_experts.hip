@@ -6,6 +6,10 @@
 //
 // The weights are the matrix instructions' first operand, so that a lane of
 // the result holds one row of x and four consecutive columns of y.
+//
+// Two kernels: k_mx4_few, for few rows an expert, is bound by the weights'
+// bytes; k_mx4_grid goes through tiles of weights and rows in LDS and comes
+// to be bound by the matrix instructions.  MxCost chooses.
 #include <cmath>
 #include <type_traits>
 
@@ -107,6 +111,11 @@ __device__ __forceinline__ i32x8_t mx4_operand(uint4 v) {
 // they take 32 columns each and all of K.  A single token's call has so few
 // columns that only the first fills the device; with more tiles it would only
 // pay the way to the tile (offsets, src) four times as often.
+//
+// Bound by the weights' bytes, in the smallest calls by the chain offsets ->
+// src -> x and weights -> sum: 8 rows, n = 1024, K = 2048 bf16 with SwiGLU take
+// 8.6 us (9 MB), 64 rows of 58 experts, n = 2048, K = 512 take 12.8 us (33 MB,
+// 2.6 TB/s; split over K 16 us).
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 32;
 
@@ -261,10 +270,20 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // lane of half h multiplies block 4 h + s: its four scale bytes of the tile are
 // then one dword, of which the instruction picks byte s.
 //
-// Ragged: k is no multiple of 256, or the scale arrays are not dword aligned.
+// A row's scales are brought 16 blocks, two K tiles, at a time by one 16-byte
+// load a row: as many instructions as a dword a K tile would take for a fourth
+// of the bytes (with those, down at 4096 tokens took 72 us, now 69).
+//
+// Ragged: k is no multiple of 512, or the scale arrays are not 16-byte aligned.
 // The scales are then staged a byte a lane, each in a dword of its own, and
 // blocks past the row's end, for which the loads bring the last block again,
-// are multiplied as zeros.
+// are multiplied as zeros.  About 1.5 times the time a K tile.
+//
+// The matrix instructions alone reach 6.0 PFLOP/s with random operands (32 x 32
+// x 64); 4096 x 8192 x 8192 takes 155 us, 3.5 PFLOP/s, with tiles of 256 x 256,
+// 1 % less with 256 x 128.  What is left is the barrier a K tile and the issue of
+// loads and LDS reads beside the products: a K tile of 256 columns takes about
+// 2600 cycles for 1152 of products a SIMD.
 // ---------------------------------------------------------------------------
 // 16, 4 or 1 bytes a lane from memory to lds + lane * max(size, 4), not waited
 // for: the compiler's own form of this load makes it wait for every load in
@@ -567,6 +586,13 @@ struct MxOp4 {
 };
 
 // ---- the operands of a tile, bf16 x ----------------------------------------------
+// As above with K tiles of 128 columns.  The weights stay codes in LDS and are
+// converted, exactly, on their way into the 32x32x16 bf16 instruction: a
+// quarter of the LDS and of the reads that converted weights would need, for
+// four conversions an operand, which each wave repeats for its own rows.
+// 2085 x 4096 x 2048 takes 52 us, 0.67 PFLOP/s (a library's product of bf16
+// matrices reaches 1.2 at 8192 x 8192 x 8192), 4096 rows of 256 experts at n =
+// 1024, K = 2048, bound by their 285 MB of weights, 66 to 74 us, 4.0 TB/s.
 // ST: K tiles of a scale load, 4 (16 bytes a row), or 1 (4 bytes) where LDS is short.
 template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged, int ST>
 struct MxOp16 {
@@ -697,7 +723,9 @@ struct MxOp16 {
 //
 // A workgroup has a range of the units in the order (expert, tile, column
 // tile), and consecutive ranges share an XCD, whose L2 then keeps an expert's
-// weights for its tiles.
+// weights for its tiles.  (Every n_wg-th unit instead, or column tiles first: 3
+// and 10 % slower at 4096 tokens, as more units begin a tile.)  4096 tokens' gate/up
+// with 4-bit rows: 90 us, from 116 with a workgroup a unit.
 template <class Op, int S>
 struct MxGrid {
   static constexpr int kPanels = S * Op::kStage;                 // where the two scale panels begin,
@@ -1005,8 +1033,8 @@ static hipError_t launch_grid(const Mx4ExpertArgs& A, int cus, hipStream_t s, co
   return launch_grid_as<Op, S, PerCu, kMxTypeBf16>(A, cus, s, kt);
 }
 
-// Stages: a tile has to be at least S - 1 K tiles long, so that a tile's rows are in LDS when the loads get to it,
-// and are not replaced before its results are out.
+// Stages: a unit has to be at least S - 1 K tiles long, so that a tile's rows are in LDS when the loads get to it,
+// and are not replaced before its results are out.  With S = 3 k is a multiple of 512: two K tiles, or four, at least.
 template <int BN, int BT, int WN, int WT, int S, int PerCu, bool Ragged>
 static hipError_t tile_mx4(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
   return A.swiglu ? launch_grid<MxOp4<BN, BT, WN, WT, true, Ragged>, S, PerCu>(A, cus, s, kt)

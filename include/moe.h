@@ -365,7 +365,9 @@ typedef struct {
  *                      (moe_route's topk_weights beside dst_rows = sorted_assign)
  *   y, y_scales        [y_rows] rows of n (with swiglu n/2) values of y_type
  *                      (y_scales NULL but for MOE_MX4)
- * w_codes, x and a MOE_MX4 y are 16-byte aligned, another y to its type.  A src(i) outside x reads as a row of
+ * w_codes, x and a MOE_MX4 y are 16-byte aligned, another y to its type;
+ * k a multiple of 512 with 16-byte aligned scales, and rows of y that are
+ * multiples of 16 bytes, are faster.  A src(i) outside x reads as a row of
  * zeros and a dst(i) outside y is not written.  Rows of y that no position
  * maps to, those of positions behind expert_offsets[E] among them, stay as
  * they were.  y must not overlap an input.
