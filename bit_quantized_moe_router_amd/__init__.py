@@ -27,7 +27,7 @@ KERNEL_NAMES = {K_LOGITS: "k_screen|k_logits_small", K_TOPK: "k_route_exact", K_
                 K_GATEUP_GEMV: "k_gemv_experts", K_DOWN_GEMV: "k_gemv_reduce", K_COMBINE: "k_combine",
                 K_DEQUANT: "k_dequant_active", K_PROBE_READ: "k_stream_read", K_PROBE_MFMA: "k_mfma_rate",
                 K_MX4_QUANTIZE: "k_mx4_quantize", K_MX4_DEQUANTIZE: "k_mx4_dequantize",
-                K_MX4_EXPERTS: "k_mx4_few",
+                K_MX4_EXPERTS: "k_mx4_few|k_mx4_grid",
                 K_BALANCE: "k_balance_rows|k_balance_sum", K_BALANCE_GRAD: "k_balance_grad"}
 
 # Element types of the microscaled 4-bit and balance-loss calls.

@@ -114,8 +114,8 @@ __device__ __forceinline__ i32x8_t mx4_operand(uint4 v) {
 //
 // Bound by the weights' bytes, in the smallest calls by the chain offsets ->
 // src -> x and weights -> sum: 8 rows, n = 1024, K = 2048 bf16 with SwiGLU take
-// 8.6 us (9 MB), 64 rows of 58 experts, n = 2048, K = 512 take 12.8 us (33 MB,
-// 2.6 TB/s; split over K 16 us).
+// 8.6 us (9 MB; 19.6 without the split), 64 rows of 58 experts, n = 2048, K =
+// 512 take 12.8 us (33 MB, 2.6 TB/s; 15.0 with it).
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 32;
 
@@ -271,8 +271,7 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // then one dword, of which the instruction picks byte s.
 //
 // A row's scales are brought 16 blocks, two K tiles, at a time by one 16-byte
-// load a row: as many instructions as a dword a K tile would take for a fourth
-// of the bytes (with those, down at 4096 tokens took 72 us, now 69).
+// load a row.
 //
 // Ragged: k is no multiple of 512, or the scale arrays are not 16-byte aligned.
 // The scales are then staged a byte a lane, each in a dword of its own, and
@@ -280,8 +279,8 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // are multiplied as zeros.  About 1.5 times the time a K tile.
 //
 // The matrix instructions alone reach 6.0 PFLOP/s with random operands (32 x 32
-// x 64); 4096 x 8192 x 8192 takes 155 us, 3.5 PFLOP/s, with tiles of 256 x 256,
-// 1 % less with 256 x 128.  What is left is the barrier a K tile and the issue of
+// x 64); 4096 x 8192 x 8192 takes 155 us, 3.5 PFLOP/s, with tiles of 256 x 256
+// (in one run 165 us against 196 with 256 x 128).  What is left is the barrier a K tile and the issue of
 // loads and LDS reads beside the products: a K tile of 256 columns takes about
 // 2600 cycles for 1152 of products a SIMD.
 // ---------------------------------------------------------------------------
@@ -592,7 +591,7 @@ struct MxOp4 {
 // four conversions an operand, which each wave repeats for its own rows.
 // 2085 x 4096 x 2048 takes 52 us, 0.67 PFLOP/s (a library's product of bf16
 // matrices reaches 1.2 at 8192 x 8192 x 8192), 4096 rows of 256 experts at n =
-// 1024, K = 2048, bound by their 285 MB of weights, 66 to 74 us, 4.0 TB/s.
+// 1024, K = 2048, bound by their 285 MB of weights, 64 us, 4.4 TB/s.
 // ST: K tiles of a scale load, 4 (16 bytes a row), or 1 (4 bytes) where LDS is short.
 template <int BN_, int BT_, int WN_, int WT_, bool Swiglu_, bool Ragged, int ST>
 struct MxOp16 {
@@ -723,9 +722,8 @@ struct MxOp16 {
 //
 // A workgroup has a range of the units in the order (expert, tile, column
 // tile), and consecutive ranges share an XCD, whose L2 then keeps an expert's
-// weights for its tiles.  (Every n_wg-th unit instead, or column tiles first: 3
-// and 10 % slower at 4096 tokens, as more units begin a tile.)  4096 tokens' gate/up
-// with 4-bit rows: 90 us, from 116 with a workgroup a unit.
+// weights for its tiles.  4096 tokens' gate/up with 4-bit rows: 90 us, from 116
+// with a workgroup a unit.
 template <class Op, int S>
 struct MxGrid {
   static constexpr int kPanels = S * Op::kStage;                 // where the two scale panels begin,
