@@ -316,7 +316,8 @@ enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_MX4 = 2 };
  *          ldx values apart (ldx >= cols); any alignment of its type, 16-byte
  *          aligned rows are faster
  *   cols   a positive multiple of 32, at most 2^24; rows = 0 is a no-op
- *   codes, scales  as above, contiguous; codes 16-byte aligned
+ *   codes, scales  as above, contiguous; codes 16-byte aligned; neither may
+ *          overlap x
  */
 moe_status moe_mx4_quantize(const void *x, int32_t x_type, int64_t rows, int64_t cols, int64_t ldx,
                             uint8_t *codes, uint8_t *scales, void *stream);
@@ -367,7 +368,7 @@ typedef struct {
  *                      (y_scales NULL but for MOE_MX4)
  * w_codes, x and a MOE_MX4 y are 16-byte aligned, another y to its type;
  * k a multiple of 512 with 16-byte aligned scales, and rows of y that are
- * multiples of 16 bytes, are faster.  A src(i) outside x reads as a row of
+ * multiples of 16 bytes, are faster.  A src(i) outside x gives a row of
  * zeros and a dst(i) outside y is not written.  Rows of y that no position
  * maps to, those of positions behind expert_offsets[E] among them, stay as
  * they were.  y must not overlap an input.

@@ -524,6 +524,55 @@ def test_experts_nan_stays_in_its_row(gpu, x_kind, rows):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("small", ["w", "x"])
+@pytest.mark.parametrize("x_kind,rows,n,k", [("bf16", 3, 64, 96), ("mx4", 3, 64, 96), ("bf16", 200, 4100, 1024),
+                                             ("bf16", 1024, 2112, 512), ("bf16", 2304, 2112, 1536), ("bf16", 900, 4100, 96),
+                                             ("mx4", 1000, 2112, 512), ("mx4", 2304, 4100, 512), ("mx4", 2304, 4100, 96)])
+def test_experts_smallest_and_largest_values(gpu, x_kind, rows, n, k, small):
+    """One side near 2^-127, subnormal where it is bf16, the other near 2^115: products of ordinary size, none lost."""
+    p = Product(gpu, [rows], n, k, x_kind, 18, random_codes=True)
+    rng = np.random.default_rng(19)
+    scales = lambda lo, shape: rng.integers(lo, lo + 4, shape).astype(np.uint8)  # noqa: E731
+    lo, hi = 0, 240
+    p.ws = scales(lo if small == "w" else hi, p.ws.shape)
+    p.gws = torch.from_numpy(p.ws).to(gpu)
+    p.w = Experts(p.wc, p.ws, 1)
+    if x_kind == "mx4":
+        xs = scales(hi if small == "w" else lo, (rows, k // 32))
+        p.gxs = torch.from_numpy(xs).to(gpu)
+        p.x = ref.dequantize(p.gx.cpu().numpy(), xs)
+    else:
+        bits = rng.integers(1, 0x180, (rows, k)) if small == "x" else rng.integers(0x7780, 0x7900, (rows, k))
+        x = torch.from_numpy((bits | rng.integers(0, 2, (rows, k)) << 15).astype(np.int32)).to(torch.int16).view(torch.bfloat16)
+        p.gx, p.x = x.to(gpu), x.double().numpy()
+    p.check(0)
+
+
+@pytest.mark.gpu
+def test_experts_tiled_in_a_graph(gpu):
+    """Large products on two streams of one graph, replayed amid eager calls with other rows."""
+    a = Product(gpu, [1300, 0, 1100], 2112, 512, "mx4", 20, random_codes=True)
+    b = Product(gpu, [600, 5, 800], 2112, 512, "bf16", 21, random_codes=True)
+    outs = [q.outputs("bf16", 0)[0] for q in (a, b)]
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g):
+        side.wait_stream(torch.cuda.current_stream())
+        a.call(outs[0], None, "bf16", 0)
+        with torch.cuda.stream(side):
+            b.call(outs[1], None, "bf16", 0)
+        torch.cuda.current_stream().wait_stream(side)
+    for turn in range(4):
+        a.gx.copy_(a.gx.flip(0))
+        b.gx.neg_()
+        want = [q.run("bf16", 0) for q in (a, b)]
+        for y in outs:
+            y.fill_(7)
+        torch.cuda.synchronize()
+        g.replay()
+        assert all(torch.equal(y, w) for y, w in zip(outs, want)), turn
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("x_kind", ["bf16", "mx4"])
 @pytest.mark.parametrize("rows", [3, 150])
 def test_experts_weights_past_32_bits(gpu, x_kind, rows):
