@@ -549,6 +549,26 @@ def test_experts_smallest_and_largest_values(gpu, x_kind, rows, n, k, small):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("x_kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("n", [1, 160])
+def test_experts_most_rows(gpu, x_kind, n):
+    """2^24 positions of a few rows of x, and results past 2^31 values: every row is its source's row of a small call."""
+    P_, E, k = 1 << 24, 3, 32
+    p = Product(gpu, [7, 7, 7], n, k, x_kind, 22, x_rows=7, src=np.tile(np.arange(7), 3), y_rows=21, random_codes=True)
+    table = p.run("f32", 0)  # [expert * 7 + row]
+    p.check(0, ("f32",))
+    p.goff = torch.tensor([0, 5000001, 5000002, P_], dtype=torch.int32, device=gpu)
+    p.rows = p.y_rows = P_
+    p.gsrc = torch.arange(P_, dtype=torch.int32, device=gpu) * 5 % 7
+    y = p.run("f32", 0)
+    step = 1 << 21
+    for at in range(0, P_, step):
+        i = torch.arange(at, at + step, device=gpu)
+        e = (i >= 5000001).long() + (i >= 5000002).long()
+        assert torch.equal(y[at:at + step], table[e * 7 + p.gsrc[at:at + step].long()]), at
+
+
+@pytest.mark.gpu
 def test_experts_tiled_in_a_graph(gpu):
     """Large products on two streams of one graph, replayed amid eager calls with other rows."""
     a = Product(gpu, [1300, 0, 1100], 2112, 512, "mx4", 20, random_codes=True)
