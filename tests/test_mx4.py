@@ -211,6 +211,21 @@ def test_storage_offsets_past_32_bits(gpu):
     assert torch.equal(x.double().cpu(), torch.from_numpy(ref.dequantize(*want)))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_storage_of_more_than_the_caches_hold(gpu, dtype):
+    """256 MB of values and more, a few rows of every kind over and over: equal rows give equal codes."""
+    few = torch.from_numpy(spread(64, 2048, 6)).to(dtype)
+    x = few.to(gpu).repeat(2048, 1)
+    codes, scales = quantized(x, gpu)
+    want_c, want_s = (torch.from_numpy(a).to(gpu) for a in ref.quantize(few.float().numpy()))
+    assert (codes.view(2048, 64, -1) == want_c).all() and (scales.view(2048, 64, -1) == want_s).all()
+    y = torch.full_like(x, 7.0)
+    moe.moe_mx4_dequantize(codes, scales, y)
+    want = torch.from_numpy(ref.dequantize(want_c.cpu().numpy(), want_s.cpu().numpy())).to(dtype).to(gpu)
+    assert (y.view(2048, 64, -1) == want).all()
+
+
 # ---- the expert product ------------------------------------------------------------------------------------
 
 
