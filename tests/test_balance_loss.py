@@ -168,6 +168,64 @@ def test_loss_and_gradient(gpu, T, E, k, dtype):
     Loss(*make(gpu, T, E, k, dtype, T + E, masked=0.4)).check()
 
 
+# More than 64 experts (up to 64, up to 32): the forward pass takes workgroups of 1024 threads and 256 partial rows from
+# 8192 (16384, 32768) tokens on; from twice as many on a group of lanes goes through more than one row there, as it
+# does in the gradient from 16384 (32768, 65536) on.  Rows of each width with 16-byte loads and without.
+MANY = [(8193, 100, 4), (16385, 48, 2), (32769, 20, 2), (16390, 256, 8), (33333, 255, 8), (24001, 512, 8), (16389, 511, 16),
+        (33001, 128, 2), (17003, 127, 1), (33001, 64, 2), (40001, 63, 5), (70001, 24, 2), (65601, 21, 3)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", MANY)
+def test_many_tokens(gpu, T, E, k, dtype):
+    Loss(*make(gpu, T, E, k, dtype, T + E, masked=0.3)).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,k", [(33001, 100, 4), (70001, 24, 2)])
+def test_many_tokens_in_place_repeated_and_on_two_streams(gpu, T, E, k, dtype):
+    """Every row is loaded before its gradient replaces it, and bits repeat, also of two calls at once."""
+    xs = [Loss(*make(gpu, T, E, k, dtype, seed, masked=0.2)) for seed in (1, 2)]
+    wants = []
+    for x in xs:
+        x.check()
+        wants.append([t.clone() for t in (x.losses, x.counts, x.mean, x.d)])
+    logits = [x.logits.clone() for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for x, s, l in zip(xs, streams, logits):
+            with torch.cuda.stream(s):
+                x.logits.copy_(l)
+                x.d = x.logits
+                x.forward()
+                x.backward()
+        torch.cuda.synchronize()
+        for x, want in zip(xs, wants):
+            assert all(torch.equal(t, w) for t, w in zip((x.losses, x.counts, x.mean, x.d), want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_many_tokens_nan_stays_in_its_row(gpu, bad):
+    """A row that a group of lanes comes to after others, and what it comes to after it."""
+    logits, ids, _ = make(gpu, 33001, 100, 2, torch.float32, 3)
+    logits[20000, 3] = bad
+    x = Loss(logits, ids, None)
+    x.forward()
+    x.backward()
+    assert x.losses.isnan().all() and x.d[20000].isnan().all()
+    assert not x.d[:20000].isnan().any() and not x.d[20001:].isnan().any()
+    valid = torch.ones(33001, dtype=torch.bool, device=gpu)
+    valid[20000] = False
+    y = Loss(logits, ids, valid)
+    y.forward()
+    y.backward()
+    assert not y.losses.isnan().any() and not y.d.isnan().any() and not y.d[20000].any()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [3, 700])
 def test_no_valid_token_and_no_token(gpu, T):
