@@ -157,10 +157,13 @@ def _value_type(t, name):
     return MOE_F32 if t.dtype is torch.float32 else _bad(f"{name} must be bfloat16 or float32 (got {t.dtype})")
 
 
-def _arg(t, name, dtype, numel, dev):
-    """The address of a contiguous tensor of this type, size and device index."""
-    if t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous():
-        _bad(f"{name} must be a contiguous {dtype} tensor of {numel} elements on the call's device "
+def _arg(t, name, dtype, numel, dev, width=None):
+    """The address of a contiguous tensor of this type, size and device index; a matrix has rows of `width`
+    elements (whatever stands before them), or is flat."""
+    if (t.dtype is not dtype or t.numel() != numel or t.get_device() != dev or not t.is_contiguous()
+            or width is not None and t.dim() > 1 and t.shape[-1] != width):
+        rows = "" if width is None else f" in rows of {width}"
+        _bad(f"{name} must be a contiguous {dtype} tensor of {numel} elements{rows} on the call's device "
              f"(got {t.dtype}, {tuple(t.shape)}, strides {t.stride()}, {t.device})")
     return t.data_ptr()
 
@@ -193,8 +196,8 @@ def _mx4_rows(v, name, codes, scales):
         _bad(f"cols must be a positive multiple of 32 (got {cols})", 2)
     dev = v.get_device()
     return (_value_type(v, name), rows, cols, ld if rows > 1 else cols, dev,
-            _arg(codes, "codes", torch.uint8, rows * cols // 2, dev),
-            _arg(scales, "scales", torch.uint8, rows * cols // 32, dev))
+            _arg(codes, "codes", torch.uint8, rows * cols // 2, dev, cols // 2),
+            _arg(scales, "scales", torch.uint8, rows * cols // 32, dev, cols // 32))
 
 
 def moe_mx4_quantize(x, codes, scales, stream=None):
@@ -227,7 +230,7 @@ def _rows(t, name, kind, cols, scales, dev):
     if kind == MOE_MX4:
         if scales is None:
             _bad(f"{name}_scales is missing")
-        return rows, p, _arg(scales, name + "_scales", torch.uint8, rows * (cols // 32), dev)
+        return rows, p, _arg(scales, name + "_scales", torch.uint8, rows * (cols // 32), dev, cols // 32)
     if scales is not None:
         _bad(f"{name}_scales goes with a MOE_MX4 {name} only")
     return rows, p, None
@@ -243,8 +246,8 @@ def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, 
     if k <= 0 or k % 32:
         _bad(f"k must be a positive multiple of 32 (got {k})", 2)
     dev, i32 = x.get_device(), torch.int32
-    wc = _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev)
-    ws = _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev)
+    wc = _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev, k // 2)
+    ws = _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev, k // 32)
     off = _arg(expert_offsets, "expert_offsets", i32, E + 1, dev)
     x_rows, xp, xs = _rows(x, "x", x_type, k, x_scales, dev)
     y_rows, yp, ys = _rows(y, "y", y_type, n // 2 if desc.swiglu else n, y_scales, dev)
@@ -297,7 +300,7 @@ def moe_balance_loss_backward(logits, top_k, valid, balance_coef, z_coef, counts
     _on_device(dev, stream, lib().moe_balance_loss_backward, p, kind, T, E, top_k, v, balance_coef, z_coef,
                _arg(counts, "counts", torch.int32, E, dev), _arg(n_valid, "n_valid", torch.int32, 1, dev),
                None if grad_loss is None else _arg(grad_loss, "grad_loss", torch.float32, 1, dev),
-               _arg(dlogits, "dlogits", logits.dtype, T * E, dev))
+               _arg(dlogits, "dlogits", logits.dtype, T * E, dev, E))
 
 
 def make_desc(hidden, n_experts, top_k, inter, shared_inter, gemv_max_rows=-1, max_chunk=2048,

@@ -91,6 +91,15 @@ def test_binding_checks_tensors():
         assert "GPU" not in str(ei.value), kw
 
 
+def test_binding_checks_the_gradients_layout():
+    z, i = torch.zeros, torch.int32
+    back = dict(logits=z(4, 8), top_k=2, valid=None, balance_coef=0.1, z_coef=0.1, counts=z(8, dtype=i),
+                n_valid=z(1, dtype=i), grad_loss=None)
+    for shape, match in (((8, 4), "dlogits"), ((2, 16), "dlogits"), ((32,), "GPU"), ((4, 8), "GPU")):
+        with pytest.raises(moe.MoEError, match=match):
+            moe.moe_balance_loss_backward(dlogits=z(shape), **back)
+
+
 # ---- on the GPU ------------------------------------------------------------------------------------------
 
 

@@ -117,6 +117,27 @@ def test_binding_checks_tensors():
         assert "GPU" not in str(ei.value), kw
 
 
+def test_binding_checks_layouts():
+    """A matrix with its rows along another dimension has as many elements, and is refused; flat ones are taken."""
+    z = lambda *shape: torch.zeros(*shape, dtype=torch.uint8)  # noqa: E731
+    x, c, s = torch.zeros(4, 128), z(4, 64), z(4, 4)
+    for call, args in ((moe.moe_mx4_quantize, (x, z(64, 4), s)), (moe.moe_mx4_quantize, (x, c, z(2, 8))),
+                       (moe.moe_mx4_dequantize, (z(64, 4), s, x)), (moe.moe_mx4_dequantize, (c, z(8, 2), x))):
+        with pytest.raises(moe.MoEError, match="codes|scales"):
+            call(*args)
+    off = torch.zeros(3, dtype=torch.int32)
+    d = moe.make_mx4_desc(2, 96, 128, moe.MOE_MX4, moe.MOE_MX4)
+    good = dict(w_codes=z(2, 96, 64), w_scales=z(2, 96, 4), x=z(5, 64), x_scales=z(5, 4), expert_offsets=off, rows=5,
+                y=z(5, 48), y_scales=z(5, 3))
+    for kw in (dict(w_codes=z(2, 64, 96)), dict(w_codes=z(64, 192)), dict(w_scales=z(2, 4, 96)), dict(w_scales=z(4, 192)),
+               dict(x_scales=z(4, 5)), dict(y_scales=z(3, 5))):
+        with pytest.raises(moe.MoEError, match=next(iter(kw))):
+            moe.moe_mx4_experts(d, **{**good, **kw})
+    for kw in ({}, dict(w_codes=z(192, 64), w_scales=z(192, 4)), dict(w_codes=z(2 * 96 * 64), x_scales=z(20))):
+        with pytest.raises(moe.MoEError, match="GPU"):
+            moe.moe_mx4_experts(d, **{**good, **kw})
+
+
 # ---- storage -------------------------------------------------------------------------------------------
 
 
