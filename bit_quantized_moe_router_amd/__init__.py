@@ -150,6 +150,11 @@ def _bad(message, status=1):
     raise MoEError(status, message)
 
 
+def _int32(value, name):
+    """value, for an int32_t of the library, of which ctypes would pass the low 32 bits alone."""
+    return value if -0x80000000 <= value <= 0x7FFFFFFF else _bad(f"{name} does not fit 32 bits (got {value})", 2)
+
+
 def _value_type(t, name):
     torch = _torch()
     if t.dtype is torch.bfloat16:
@@ -213,7 +218,7 @@ def moe_mx4_dequantize(codes, scales, y, stream=None):
 
 
 def make_mx4_desc(n_experts, n, k, x_type, y_type, swiglu=0) -> Mx4Desc:
-    return Mx4Desc(n_experts, n, k, x_type, y_type, swiglu)
+    return Mx4Desc(_int32(n_experts, "n_experts"), _int32(n, "n"), _int32(k, "k"), x_type, y_type, swiglu)
 
 
 def _rows(t, name, kind, cols, scales, dev):
@@ -225,7 +230,7 @@ def _rows(t, name, kind, cols, scales, dev):
         dtype, width = torch.float32 if kind == MOE_F32 else torch.bfloat16, cols
     if t.dim() != 2 or t.shape[1] != width:
         _bad(f"{name} must be 2-D with {width} columns (got {tuple(t.shape)})")
-    rows = t.shape[0]
+    rows = _int32(t.shape[0], f"the number of {name}'s rows")
     p = _arg(t, name, dtype, rows * width, dev)
     if kind == MOE_MX4:
         if scales is None:
@@ -249,6 +254,7 @@ def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, 
     wc = _arg(w_codes, "w_codes", torch.uint8, E * n * (k // 2), dev, k // 2)
     ws = _arg(w_scales, "w_scales", torch.uint8, E * n * (k // 32), dev, k // 32)
     off = _arg(expert_offsets, "expert_offsets", i32, E + 1, dev)
+    rows, src_div = _int32(rows, "rows"), _int32(src_div, "src_div")
     x_rows, xp, xs = _rows(x, "x", x_type, k, x_scales, dev)
     y_rows, yp, ys = _rows(y, "y", y_type, n // 2 if desc.swiglu else n, y_scales, dev)
     src = None if src_rows is None else _arg(src_rows, "src_rows", i32, rows, dev)
@@ -260,7 +266,7 @@ def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, 
 
 def moe_balance_loss_workspace_bytes(T: int, n_experts: int) -> int:
     n = C.c_size_t()
-    _check(lib().moe_balance_loss_workspace_bytes(T, n_experts, C.byref(n)))
+    _check(lib().moe_balance_loss_workspace_bytes(_int32(T, "T"), _int32(n_experts, "n_experts"), C.byref(n)))
     return n.value
 
 
@@ -270,6 +276,7 @@ def _logits(logits, valid):
     if logits.dim() != 2 or not logits.is_contiguous():
         _bad(f"logits must be 2-D and contiguous (got {tuple(logits.shape)}, strides {logits.stride()})")
     T, E = logits.shape
+    _int32(T, "T"), _int32(E, "n_experts")
     dev = logits.get_device()
     v = None
     if valid is not None:
@@ -285,7 +292,7 @@ def moe_balance_loss_forward(logits, topk_ids, valid, balance_coef, z_coef, loss
     T, E, kind, dev, p, v = _logits(logits, valid)
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         _bad(f"topk_ids must be [T, k] (got {tuple(topk_ids.shape)} for T = {T})")
-    k, i32, f32 = topk_ids.shape[1], torch.int32, torch.float32
+    k, i32, f32 = _int32(topk_ids.shape[1], "top_k"), torch.int32, torch.float32
     _on_device(dev, stream, lib().moe_balance_loss_forward, p, kind, T, E, _arg(topk_ids, "topk_ids", i32, T * k, dev),
                k, v, balance_coef, z_coef, _arg(losses, "losses", f32, 3, dev), _arg(counts, "counts", i32, E, dev),
                _arg(mean_prob, "mean_prob", f32, E, dev), _arg(n_valid, "n_valid", i32, 1, dev),
@@ -297,7 +304,7 @@ def moe_balance_loss_backward(logits, top_k, valid, balance_coef, z_coef, counts
     """Gradient of moe_balance_loss_forward's loss; grad_loss [1] float32 or None (1)."""
     torch = _torch()
     T, E, kind, dev, p, v = _logits(logits, valid)
-    _on_device(dev, stream, lib().moe_balance_loss_backward, p, kind, T, E, top_k, v, balance_coef, z_coef,
+    _on_device(dev, stream, lib().moe_balance_loss_backward, p, kind, T, E, _int32(top_k, "top_k"), v, balance_coef, z_coef,
                _arg(counts, "counts", torch.int32, E, dev), _arg(n_valid, "n_valid", torch.int32, 1, dev),
                None if grad_loss is None else _arg(grad_loss, "grad_loss", torch.float32, 1, dev),
                _arg(dlogits, "dlogits", logits.dtype, T * E, dev, E))

@@ -100,6 +100,23 @@ def test_binding_checks_the_gradients_layout():
             moe.moe_balance_loss_backward(dlogits=z(shape), **back)
 
 
+def test_binding_refuses_what_32_bits_do_not_hold():
+    """Sizes reach the library as 32-bit numbers: none is cut to its low bits.  Tensors without memory."""
+    T = (1 << 32) + 4
+    e = lambda *shape, t=torch.float32: torch.empty(*shape, dtype=t, device="meta")  # noqa: E731
+    i = torch.int32
+    forward = dict(valid=None, balance_coef=0.1, z_coef=0.1, losses=e(3), n_valid=e(1, t=i), ws=e(1 << 16, t=torch.uint8))
+    back = dict(valid=None, balance_coef=0.1, z_coef=0.1, n_valid=e(1, t=i), grad_loss=None)
+    for t, E, k in ((T, 1, 1), (4, T, 1), (4, 1, T)):
+        with pytest.raises(moe.MoEError, match="32 bits"):
+            moe.moe_balance_loss_forward(logits=e(t, E), topk_ids=e(t, k, t=i), counts=e(E, t=i), mean_prob=e(E), **forward)
+        with pytest.raises(moe.MoEError, match="32 bits"):
+            moe.moe_balance_loss_backward(logits=e(t, E), top_k=k, counts=e(E, t=i), dlogits=e(t, E), **back)
+    for bad in ((T, 8), (8, T)):
+        with pytest.raises(moe.MoEError, match="32 bits"):
+            moe.moe_balance_loss_workspace_bytes(*bad)
+
+
 # ---- on the GPU ------------------------------------------------------------------------------------------
 
 

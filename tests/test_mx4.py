@@ -138,6 +138,26 @@ def test_binding_checks_layouts():
             moe.moe_mx4_experts(d, **{**good, **kw})
 
 
+def test_binding_refuses_what_32_bits_do_not_hold():
+    """Sizes reach the library as 32-bit numbers: none is cut to its low bits.  Tensors without memory."""
+    far = 1 << 32
+    for at in range(3):
+        with pytest.raises(moe.MoEError, match="32 bits"):
+            moe.make_mx4_desc(*(far + v if i == at else v for i, v in enumerate((2, 96, 128))), moe.MOE_MX4, moe.MOE_MX4)
+    z = lambda *shape: torch.empty(*shape, dtype=torch.uint8, device="meta")  # noqa: E731
+    f = lambda *shape, t=torch.int32: torch.empty(*shape, dtype=t, device="meta")  # noqa: E731
+    d = moe.make_mx4_desc(2, 32, 32, moe.MOE_MX4, moe.MOE_MX4)
+    good = dict(w_codes=z(2, 32, 16), w_scales=z(2, 32, 1), x=z(5, 16), x_scales=z(5, 1), expert_offsets=f(3), rows=5,
+                y=z(5, 16), y_scales=z(5, 1))
+    with pytest.raises(moe.MoEError, match="GPU"):
+        moe.moe_mx4_experts(d, **good)
+    for kw in (dict(rows=far + 5), dict(rows=far + 5, src_rows=f(far + 5)), dict(rows=far + 5, dst_rows=f(far + 5)),
+               dict(src_div=far + 1), dict(src_div=-far + 1), dict(x=z(far + 5, 16), x_scales=z(far + 5, 1)),
+               dict(y=z(far + 5, 16), y_scales=z(far + 5, 1))):
+        with pytest.raises(moe.MoEError, match="32 bits"):
+            moe.moe_mx4_experts(d, **{**good, **kw})
+
+
 # ---- storage -------------------------------------------------------------------------------------------
 
 
