@@ -91,6 +91,8 @@ def lib():
         L.moe_status_str.restype = C.c_char_p
         L.moe_last_error.argtypes = []
         L.moe_last_error.restype = C.c_char_p
+        L.moe_mx4_experts_kernel.argtypes = []
+        L.moe_mx4_experts_kernel.restype = C.c_char_p
         L.moe_probe_stream_read.argtypes = [vp, sz, vp, i32, vp]
         L.moe_probe_mfma_rate.argtypes = [i32, i32, vp, vp, vp]
         L.moe_profile_enable.argtypes = [i32]
@@ -262,6 +264,11 @@ def moe_mx4_experts(desc, w_codes, w_scales, x, x_scales, expert_offsets, rows, 
     fac = None if row_scale is None else _arg(row_scale, "row_scale", torch.float32, y_rows, dev)
     _on_device(dev, stream, lib().moe_mx4_experts, C.byref(desc), wc, ws, xp, xs, x_rows, off, rows, src, src_div, dst,
                fac, yp, ys, y_rows)
+
+
+def moe_mx4_experts_kernel() -> str:
+    """The kernel that this thread's last moe_mx4_experts call took (moe.h lists them)."""
+    return lib().moe_mx4_experts_kernel().decode()
 
 
 def moe_balance_loss_workspace_bytes(T: int, n_experts: int) -> int:

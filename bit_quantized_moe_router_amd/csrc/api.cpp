@@ -797,6 +797,8 @@ moe_status moe_mx4_dequantize(const uint8_t* codes, const uint8_t* scales, int64
   return timed(12, s, "4-bit read-back", [&](const KTime& kt) { return launch_mx4_dequantize(A, s, kt); });
 }
 
+static thread_local const char* g_experts_kernel = "";  // of the last product
+
 moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const uint8_t* w_scales, const void* x,
                            const uint8_t* x_scales, int32_t x_rows, const int32_t* expert_offsets, int32_t rows,
                            const int32_t* src_rows, int32_t src_div, const int32_t* dst_rows, const float* row_scale,
@@ -845,8 +847,12 @@ moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const 
   }
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
-  return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, cus, s, kt); });
+  const MxKernel m = mx4_experts_kernel(A, cus);
+  g_experts_kernel = mx4_experts_kernel_name(m);
+  return timed(13, s, "4-bit expert product", [&](const KTime& kt) { return launch_mx4_experts(A, m, cus, s, kt); });
 }
+
+const char* moe_mx4_experts_kernel(void) { return g_experts_kernel; }
 
 static moe_status balance_shape(int32_t T, int32_t E, int32_t k) {
   if (T < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %d)", T);

@@ -144,8 +144,13 @@ struct Mx4ExpertArgs {
   uint32_t src_magic;
   int src_shift;
 };
-// cus: the device's compute units.
-hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt = KTime{});
+// The kernels of the product: few rows an expert (kFewSplit: the waves split K); tiles of 256 weight rows (k16Half:
+// 128) by 256, 128 or 32 positions for rows of 4 or 16 bits, Odd where the scales' rows are no whole 16-byte pieces.
+enum class MxKernel { kFew, kFewSplit, k4By256, k4By128, k4By128Odd, k16By32, k16By32Odd, k16Half, k16By128, k16By128Odd };
+// The one to take.  cus: the device's compute units.
+MxKernel mx4_experts_kernel(const Mx4ExpertArgs& A, int cus);
+const char* mx4_experts_kernel_name(MxKernel m);
+hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, MxKernel m, int cus, hipStream_t s, const KTime& kt = KTime{});
 
 // The router's balance loss (balance.hip).
 constexpr int kBalMaxParts = 256;  // partial rows of the forward pass

@@ -1078,41 +1078,75 @@ struct MxCost {
   }
 };
 
-hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, int cus, hipStream_t s, const KTime& kt) {
+// Columns of few-row tiles go to the waves of a workgroup where that leaves two workgroups a compute unit.
+static bool few_by_columns(const Mx4ExpertArgs& A, int cus) {
   const int64_t n_out = A.swiglu ? A.n / 2 : A.n;
+  return max_tiles(A.P, A.E, 16) * ((n_out + 4 * kFewCols - 1) / (4 * kFewCols)) >= 2 * cus;
+}
+
+MxKernel mx4_experts_kernel(const Mx4ExpertArgs& A, int cus) {
   // Scales by 16 bytes, two or four K tiles at a time, where every row of them allows it.
-  const bool ragged = A.k % 512 != 0 || ((reinterpret_cast<uintptr_t>(A.w_scales) |
-                                          reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 15) != 0;
-  const MxCost C{(double)A.P, (double)A.E, (double)A.n, (double)A.k, ragged,
+  const bool odd = A.k % 512 != 0 || ((reinterpret_cast<uintptr_t>(A.w_scales) |
+                                       reinterpret_cast<uintptr_t>(A.x_mx4 ? A.x_scales : nullptr)) & 15) != 0;
+  const MxCost C{(double)A.P, (double)A.E, (double)A.n, (double)A.k, odd,
                  5.0 + (A.src_rows || A.dst_rows ? 2 : 0) + (A.row_scale ? 2 : 0)};
   if (A.x_mx4) {
     const double few = C.few(1550 / 256.0 * cus, 1.1e-3), mid = C.grid(256, 128, 256, 1.05, 1.4, 1.7, cus);
-    const double big = ragged ? 1e30 : C.grid(256, 256, 256, 1.7, 2.4, 1.7, cus);
-    if (big < few && big < mid) return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
-    if (mid < few)
-      return ragged ? tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    const double big = odd ? 1e30 : C.grid(256, 256, 256, 1.7, 2.4, 1.7, cus);
+    if (big < few && big < mid) return MxKernel::k4By256;
+    if (mid < few) return odd ? MxKernel::k4By128Odd : MxKernel::k4By128;
   } else {
     const double few = C.few(1130 / 256.0 * cus, 1.6e-3), low = C.grid(256, 32, 128, 0.7, 1.6, 1.0, 2 * cus);
-    const double mid = ragged ? 1e30 : C.grid(128, 128, 128, 0.86, 1.2, 1.0, cus);
+    const double mid = odd ? 1e30 : C.grid(128, 128, 128, 0.86, 1.2, 1.0, cus);
     const double big = C.grid(256, 128, 128, 1.4, 2.0, 1.0, cus);
-    if (low < few && low <= mid && low <= big)
-      return ragged ? tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt) : tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
-    if (mid < few && mid <= big) return tile_bf16<128, 128, 2, 4, 3, 1, false>(A, cus, s, kt);
-    if (big < few)
-      return ragged ? tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt) : tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    if (low < few && low <= mid && low <= big) return odd ? MxKernel::k16By32Odd : MxKernel::k16By32;
+    if (mid < few && mid <= big) return MxKernel::k16Half;
+    if (big < few) return odd ? MxKernel::k16By128Odd : MxKernel::k16By128;
   }
-  const int64_t tiles = max_tiles(A.P, A.E, 16), wide_grid = tiles * ((n_out + 4 * kFewCols - 1) / (4 * kFewCols));
-  const bool split = wide_grid < 2 * cus;
-  const int64_t grid = split ? tiles * ((n_out + kFewCols - 1) / kFewCols) : wide_grid;
+  return few_by_columns(A, cus) ? MxKernel::kFew : MxKernel::kFewSplit;
+}
+
+const char* mx4_experts_kernel_name(MxKernel m) {
+  switch (m) {
+    case MxKernel::kFew: return "few";
+    case MxKernel::kFewSplit: return "few split";
+    case MxKernel::k4By256: return "4-bit 256x256";
+    case MxKernel::k4By128: return "4-bit 256x128";
+    case MxKernel::k4By128Odd: return "4-bit 256x128 odd";
+    case MxKernel::k16By32: return "bf16 256x32";
+    case MxKernel::k16By32Odd: return "bf16 256x32 odd";
+    case MxKernel::k16Half: return "bf16 128x128";
+    case MxKernel::k16By128: return "bf16 256x128";
+    case MxKernel::k16By128Odd: return "bf16 256x128 odd";
+  }
+  return "";
+}
+
+template <bool Split>
+static hipError_t launch_few(const Mx4ExpertArgs& A, hipStream_t s, const KTime& kt) {
+  constexpr int cols = Split ? kFewCols : 4 * kFewCols;
+  const int64_t n_out = A.swiglu ? A.n / 2 : A.n, grid = max_tiles(A.P, A.E, 16) * ((n_out + cols - 1) / cols);
   if (grid > 0x7FFFFFFF) return hipErrorInvalidConfiguration;
-  auto pick = [&](auto sp) {
-    constexpr bool Sp = sp.value;
-    return A.x_mx4 ? (A.swiglu ? k_mx4_few<true, true, Sp> : k_mx4_few<true, false, Sp>)
-                   : (A.swiglu ? k_mx4_few<false, true, Sp> : k_mx4_few<false, false, Sp>);
-  };
-  auto* f = split ? pick(std::true_type{}) : pick(std::false_type{});
+  auto* f = A.x_mx4 ? (A.swiglu ? k_mx4_few<true, true, Split> : k_mx4_few<true, false, Split>)
+                    : (A.swiglu ? k_mx4_few<false, true, Split> : k_mx4_few<false, false, Split>);
   MOE_LAUNCH(f, dim3((unsigned)grid), dim3(256), 0, s, kt.start, kt.stop, A);
   return hipGetLastError();
+}
+
+hipError_t launch_mx4_experts(const Mx4ExpertArgs& A, MxKernel m, int cus, hipStream_t s, const KTime& kt) {
+  switch (m) {
+    case MxKernel::kFew: return launch_few<false>(A, s, kt);
+    case MxKernel::kFewSplit: return launch_few<true>(A, s, kt);
+    case MxKernel::k4By256: return tile_mx4<256, 256, 2, 4, 2, 1, false>(A, cus, s, kt);
+    case MxKernel::k4By128: return tile_mx4<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    case MxKernel::k4By128Odd: return tile_mx4<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
+    case MxKernel::k16By32: return tile_bf16<256, 32, 4, 1, 3, 2, false>(A, cus, s, kt);
+    case MxKernel::k16By32Odd: return tile_bf16<256, 32, 4, 1, 2, 2, true>(A, cus, s, kt);
+    case MxKernel::k16Half: return tile_bf16<128, 128, 2, 4, 3, 1, false>(A, cus, s, kt);
+    case MxKernel::k16By128: return tile_bf16<256, 128, 4, 2, 3, 1, false>(A, cus, s, kt);
+    case MxKernel::k16By128Odd: return tile_bf16<256, 128, 4, 2, 2, 1, true>(A, cus, s, kt);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace moe

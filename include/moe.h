@@ -460,6 +460,16 @@ moe_status moe_profile_enable(int32_t mask);
 moe_status moe_profile_reset(void);
 moe_status moe_profile_read(int32_t kernel_id, double *total_ms, int32_t *launches);
 
+/*
+ * The kernel that the calling thread's last moe_mx4_experts call took, for
+ * measurement tools and tests ("" before the first): "few" (rows an expert;
+ * "few split" where the waves split K), or weight rows x positions of a tile,
+ * "4-bit 256x256", "4-bit 256x128", "bf16 256x128", "bf16 128x128" or "bf16
+ * 256x32", with " odd" where k is no multiple of 512 or a scale array begins at
+ * no multiple of 16 bytes.  A static string.
+ */
+const char *moe_mx4_experts_kernel(void);
+
 #ifdef __cplusplus
 }
 #endif

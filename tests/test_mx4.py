@@ -117,6 +117,16 @@ def test_binding_checks_tensors():
         assert "GPU" not in str(ei.value), kw
 
 
+def test_kernel_name_before_any_call():
+    import threading
+
+    names = []
+    t = threading.Thread(target=lambda: names.append(moe.moe_mx4_experts_kernel()))
+    t.start()
+    t.join()
+    assert names == [""]
+
+
 def test_binding_checks_layouts():
     """A matrix with its rows along another dimension has as many elements, and is refused; flat ones are taken."""
     z = lambda *shape: torch.zeros(*shape, dtype=torch.uint8)  # noqa: E731
@@ -537,6 +547,63 @@ def test_experts_tiled_offsets_are_held_inside(gpu, x_kind):
         assert y.isfinite().all()
         if off[0] == off[-1]:
             assert off[1] != off[0] or (y == 7).all()
+
+
+def shifted(t, by):
+    """A copy of t that begins `by` elements into its memory."""
+    buf = torch.empty(t.numel() + by, dtype=t.dtype, device=t.device)
+    buf[by:].copy_(t.reshape(-1))
+    return buf[by:].view(t.shape)
+
+
+# Each kernel: what it is taken for, and which one takes the same product where scales begin at no multiple of 16 bytes.
+KERNELS = [
+    ("few", "few", "bf16", around(100, 4, 104), 1058, 288),
+    ("few", "few", "mx4", around(80, 4, 84), 2112, 288),
+    ("few split", "few split", "bf16", [1, 0, 3], 576, 512),
+    ("few split", "few split", "mx4", [1, 0, 3], 578, 160),
+    ("bf16 256x32", "bf16 256x32 odd", "bf16", around(40, 30, 70), 2112, 512),
+    ("bf16 256x32 odd", "bf16 256x32 odd", "bf16", around(40, 30, 70), 2114, 288),
+    ("bf16 128x128", "bf16 256x32 odd", "bf16", around(6, 300, 306), 2112, 512),
+    ("bf16 128x128", "few", "bf16", around(3, 150, 153), 4864, 512),
+    ("bf16 256x128", "bf16 256x128 odd", "bf16", around(12, 150, 162), 2112, 512),
+    ("bf16 256x128", "bf16 256x128 odd", "bf16", around(40, 150, 190), 578, 1024),
+    ("bf16 256x128 odd", "bf16 256x128 odd", "bf16", around(12, 150, 162), 2114, 160),
+    ("4-bit 256x128", "4-bit 256x128 odd", "mx4", around(64, 70, 134), 578, 512),
+    ("4-bit 256x128", "few", "mx4", around(6, 300, 306), 2112, 512),
+    ("4-bit 256x128 odd", "4-bit 256x128 odd", "mx4", around(40, 70, 110), 2112, 160),
+    ("4-bit 256x256", "4-bit 256x128 odd", "mx4", around(12, 300, 312), 2112, 512),
+    ("4-bit 256x256", "4-bit 256x128 odd", "mx4", around(64, 150, 214), 578, 512),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel,unaligned,x_kind,counts,n,k", KERNELS,
+                         ids=[f"{m}-{x}-{sum(c)}-{n}-{k}".replace(" ", "_") for m, _, x, c, n, k in KERNELS])
+def test_experts_kernels(gpu, kernel, unaligned, x_kind, counts, n, k):
+    """Every kernel by its name, plain; and gathered, scattered and weighted with rows outside on either side, also
+    with scales at other addresses, where that takes another kernel."""
+    def check(want):
+        for swiglu in (0, 1):
+            p.check(swiglu)
+            # The sizes are chosen for an MI355X's compute units.
+            assert moe.moe_mx4_experts_kernel() == want or torch.cuda.get_device_properties(0).multi_processor_count != 256
+
+    p = Product(gpu, counts, n, k, x_kind, n + k, random_codes=True)
+    check(kernel)
+    rng = np.random.default_rng(n + k + len(counts))
+    rows = p.rows + 9
+    tokens = (rows + 2) // 3
+    src, dst = rng.permutation(3 * tokens)[:rows], rng.permutation(rows + 7)[:rows]
+    src[rng.integers(0, rows, 3)] = [-1, 3 * tokens, -(1 << 31)]
+    dst[rng.choice(rows, 3, replace=False)] = [-1, rows + 7, 1 << 30]
+    p = Product(gpu, counts, n, k, x_kind, 23, x_rows=tokens, src=src, src_div=3, dst=dst, y_rows=rows + 7, row_scale=True,
+                slack=9, random_codes=True)
+    check(kernel)
+    p.gws = shifted(p.gws, 1)
+    if x_kind == "mx4":
+        p.gxs = shifted(p.gxs, 3)
+    check(unaligned)
 
 
 @pytest.mark.gpu
