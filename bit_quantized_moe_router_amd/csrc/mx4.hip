@@ -1,13 +1,11 @@
 // Quantisation to the microscaled 4-bit format and back (format: mx4.h).
 //
 // Both are bound by memory: 2.53 or 4.53 bytes a value (bf16 or fp32 on the
-// wide side), a handful of instructions each.  131072 x 2048 bf16 values there
-// and back take 224 us, 6.1 TB/s; a 2 GiB copy reaches 4.9.  A thread takes eight values, so
-// a wave's wide side is 1 or 2 KB of consecutive bytes, its codes are one
-// dword a lane, and the four lanes of a block find its largest magnitude with
-// two lane moves.
-#include <type_traits>
-
+// wide side), a handful of instructions each.  131072 x 2048 values there and
+// back take 224 us in bf16, 6.1 TB/s, and 602 us in fp32, 4.0 TB/s; a 2 GiB
+// copy reaches 4.9.  A thread takes eight values, so a wave's wide side is 1 or
+// 2 KB of consecutive bytes, its codes are one dword a lane, and the four lanes
+// of a block find its largest magnitude with two lane moves.
 #include "launch.h"
 #include "mx4.h"
 
@@ -16,11 +14,17 @@ namespace moe {
 constexpr int kMxThreads = 256;
 
 // How a row's values are reached: one by one, by 16 bytes (which need that
-// alignment), or by 16 bytes past the caches, for more values than these hold:
-// the codes and what is still to be read then keep their place there.
-// 131072 x 2048 bf16: quantised 121 us, 128 through the caches; read back 105
-// against 129, with a reader after it 285 against 305.  But 16384 x 2048 read
-// back with a reader after it: 36.5 against 34.3.
+// alignment), or, for more bf16 values than the caches hold, by 16 bytes past
+// them: the codes and what is still to be read then keep their place there.
+// us past the caches / through them, 2048 columns:
+//   rows            quantised   read back   both in turn  read back, then a reader
+//   16384   bf16     17 /  15    11 /  14     28 /  29       44 /  38
+//   65536   bf16     56 /  59    50 /  63    107 / 138      134 / 144
+//   131072  bf16    119 / 130   104 / 128    224 / 268      272 / 286
+//   32768   fp32     58 /  46   101 /  76    162 / 134      154 / 140
+//   131072  fp32    259 / 241   466 / 340    724 / 605      589 / 630
+// fp32 goes through them: a lane's eight values are two 16-byte stores there, a
+// wave's 32 bytes apart, which only the caches make whole lines of.
 enum { kByOne = 0, kWide = 1, kPast = 2 };
 constexpr int64_t kCacheBytes = (int64_t)256 << 20;  // the last-level cache
 
@@ -132,7 +136,7 @@ __global__ __launch_bounds__(kMxThreads) void k_mx4_dequantize(Mx4RowArgs A) {
 static int row_mode(const Mx4RowArgs& A) {
   const int64_t size = A.f32 ? 4 : 2;
   if (((reinterpret_cast<uintptr_t>(A.wide) | (uintptr_t)(A.ld * size)) & 15) != 0) return kByOne;
-  return A.rows * A.cols * size >= kCacheBytes ? kPast : kWide;
+  return !A.f32 && A.rows * A.cols * size >= kCacheBytes ? kPast : kWide;
 }
 
 static dim3 row_grid(const Mx4RowArgs& A) {
@@ -141,23 +145,21 @@ static dim3 row_grid(const Mx4RowArgs& A) {
 }
 
 hipError_t launch_mx4_quantize(const Mx4RowArgs& A, hipStream_t s, const KTime& kt) {
-  auto pick = [&](auto f32) {
-    constexpr bool F = f32.value;
-    const int m = row_mode(A);
-    return m == kPast ? k_mx4_quantize<F, kPast> : m == kWide ? k_mx4_quantize<F, kWide> : k_mx4_quantize<F, kByOne>;
-  };
-  auto* f = A.f32 ? pick(std::true_type{}) : pick(std::false_type{});
+  const int m = row_mode(A);
+  auto* f = A.f32         ? (m == kWide ? k_mx4_quantize<true, kWide> : k_mx4_quantize<true, kByOne>)
+            : m == kPast  ? k_mx4_quantize<false, kPast>
+            : m == kWide  ? k_mx4_quantize<false, kWide>
+                          : k_mx4_quantize<false, kByOne>;
   MOE_LAUNCH(f, row_grid(A), dim3(kMxThreads), 0, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
 
 hipError_t launch_mx4_dequantize(const Mx4RowArgs& A, hipStream_t s, const KTime& kt) {
-  auto pick = [&](auto f32) {
-    constexpr bool F = f32.value;
-    const int m = row_mode(A);
-    return m == kPast ? k_mx4_dequantize<F, kPast> : m == kWide ? k_mx4_dequantize<F, kWide> : k_mx4_dequantize<F, kByOne>;
-  };
-  auto* f = A.f32 ? pick(std::true_type{}) : pick(std::false_type{});
+  const int m = row_mode(A);
+  auto* f = A.f32         ? (m == kWide ? k_mx4_dequantize<true, kWide> : k_mx4_dequantize<true, kByOne>)
+            : m == kPast  ? k_mx4_dequantize<false, kPast>
+            : m == kWide  ? k_mx4_dequantize<false, kWide>
+                          : k_mx4_dequantize<false, kByOne>;
   MOE_LAUNCH(f, row_grid(A), dim3(kMxThreads), 0, s, kt.start, kt.stop, A);
   return hipGetLastError();
 }
