@@ -108,14 +108,17 @@ __device__ __forceinline__ i32x8_t mx4_operand(uint4 v) {
 //
 // Split: the four waves of a workgroup share the columns and split K (chunks
 // in turn), and their sums are joined through LDS in a fixed order; otherwise
-// they take 32 columns each and all of K.  A single token's call has so few
-// columns that only the first fills the device; with more tiles it would only
-// pay the way to the tile (offsets, src) four times as often.
+// they take 32 columns each and all of K.  A single token's gate/up has few
+// columns: 8 rows, n = 1024 with SwiGLU are 128 workgroups with the split, half
+// the number of compute units, and 32 without.  With more tiles the split would
+// only pay the way to the tile (offsets, src) four times as often.
 //
 // Bound by the weights' bytes, in the smallest calls by the chain offsets ->
-// src -> x and weights -> sum: 8 rows, n = 1024, K = 2048 bf16 with SwiGLU take
-// 8.6 us (9 MB; 19.6 without the split), 64 rows of 58 experts, n = 2048, K =
-// 512 take 12.8 us (33 MB, 2.6 TB/s; 15.0 with it).
+// src -> x and weights -> sum, and by the compute units that they leave idle:
+// 8 rows, n = 1024, K = 2048 bf16 with SwiGLU take 8.6 us (9 MB; 19.6 without
+// the split), 64 rows of 58 experts, n = 2048, K = 512 take 12.8 us (33 MB, 2.6
+// TB/s; 15.0 with it).  Both with weights that the last-level cache holds; 9.8
+// and 14.4 us with copies of them in turn, 512 MB in all.
 // ---------------------------------------------------------------------------
 constexpr int kFewCols = 32;
 
@@ -274,20 +277,23 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
 // load a row.
 //
 // Ragged: k is no multiple of 512, or the scale arrays are not 16-byte aligned.
-// The scales are then staged a byte a lane, each in a dword of its own, and
-// blocks past the row's end, for which the loads bring the last block again,
-// are multiplied as zeros.  About 1.5 times the time a K tile.
+// The scales are then staged a byte a lane, each in a dword of its own, through
+// two stages, and blocks past the row's end, for which the loads bring the last
+// block again, are multiplied as zeros.  On 162 products that both forms can
+// take this one took 1.05 to 1.47 times as long, 1.25 in the middle (bf16 rows:
+// 256 x 32 0.92 to 1.46, 1.08; 256 x 128 0.99 to 1.17, 1.06).
 //
 // The matrix instructions alone reach 6.0 PFLOP/s with random operands (32 x 32
 // x 64); 4096 x 8192 x 8192 takes 155 us, 3.5 PFLOP/s, with tiles of 256 x 256
-// (in one run 165 us against 196 with 256 x 128).  What is left is the barrier a K tile and the issue of
-// loads and LDS reads beside the products: a K tile of 256 columns takes about
-// 2600 cycles for 1152 of products a SIMD.
+// (in one run 165 us against 196 with 256 x 128).  A workgroup goes through 64 K
+// tiles of 2.4 us there, of which 1.4 would be matrix instructions (2048 cycles
+// a SIMD); the rest goes to the barrier and to loads and LDS reads beside them.
 // ---------------------------------------------------------------------------
 // 16, 4 or 1 bytes a lane from memory to lds + lane * max(size, 4), not waited
 // for: the compiler's own form of this load makes it wait for every load in
-// flight before the next read of LDS.  m0 holds the LDS address; nothing else
-// in these kernels uses it.
+// flight before the next read of LDS.  m0 holds the LDS address.  It is the
+// compiler's own (a clobber list does not take it), set by it right before an
+// instruction that reads it; in these kernels there is none but these loads.
 template <int Size>
 __device__ __forceinline__ void load_to_lds(const void* p, uint32_t lds) {
   static_assert(Size == 16 || Size == 4 || Size == 1, "a direct load's size");
@@ -1046,10 +1052,17 @@ static hipError_t tile_bf16(const Mx4ExpertArgs& A, int cus, hipStream_t s, cons
                   : launch_grid<MxOp16<BN, BT, WN, WT, false, Ragged, ST>, S, PerCu>(A, cus, s, kt);
 }
 
-// The kernels' times in us, from sizes alone, to choose the shortest.  Fitted to
-// 156 products on 256 compute units: one matrix with 16 to 2048 rows, n = 256 to
-// 4096, K = 512 to 8192, and 16 to 256 experts with up to 256 rows each.  Over
-// those the choice is 1% slower than the best one on average and 21% at most.
+// The kernels' times in us, from sizes alone, to choose the shortest.  Over 204
+// products on 256 compute units (one matrix with 16 to 2048 rows, n = 256 to
+// 4096, K = 512 to 8192, and 16 to 256 experts with up to 256 rows each) the
+// choice is 1% slower than the best one on average and 25% at most; over 84 with
+// K = 768, 1408 and 2880 1% and 40%.  Those are what the factor for a ragged K
+// is for (with 1.3 the choice is 3% slower, with 1.7 0.4%); where both forms can
+// be taken the ragged one costs less.  The 2 us each for gathered or scattered
+// rows and for factors are no fit: over 120 such products, half of them with
+// skewed routing, the choice is 4% slower on average and 58% at most; without
+// these terms 2% and 43%, but 8 tokens' skewed down product would take 10.0 us
+// instead of 8.1.
 // Both sides, measured us: 4-bit x, 1024 x 4096 x 2048 few 88, tiles of 128
 // positions 17; 256 x 1024 x 2048 few 9, tiles 14; 256 experts with 4 rows each,
 // n = 1024, K = 2048: few 77, tiles 58.  bf16 x, 64 experts with 8 rows each,

@@ -355,8 +355,9 @@ typedef struct {
  *                      MOE_BF16)
  *   expert_offsets     [E+1] int32, increasing from 0 to the number of
  *                      positions, as moe_route writes them
- *   rows               the positions' upper bound on the host: expert_offsets[E]
- *                      is at most rows (offsets are held inside [0, rows])
+ *   rows               the positions' upper bound on the host, at most 2^24:
+ *                      expert_offsets[E] is at most rows (offsets are held
+ *                      inside [0, rows])
  *   src_rows, src_div  src(i) = src_rows[i] / src_div, or i where src_rows is
  *                      NULL; moe_route's sorted_assign with src_div = k gives
  *                      each assignment its token's row
