@@ -373,8 +373,9 @@ typedef struct {
  * zeros and a dst(i) outside y is not written.  Rows of y that no position
  * maps to, those of positions behind expert_offsets[E] among them, stay as
  * they were.  y must not overlap an input.
- * Products are summed in fp32 (bf16 x with the weights' exact bf16 values;
- * MOE_MX4 x in the scaled matrix instructions), SwiGLU and row_scale are
+ * Products are summed in fp32 (bf16 x with the weights' exact bf16 values,
+ * infinity for 2^128 and more, which moe_mx4_quantize never writes; MOE_MX4 x
+ * in the scaled matrix instructions), SwiGLU and row_scale are
  * applied in fp32, and the result is rounded once to y_type, for MOE_MX4 as
  * moe_mx4_quantize does.  Repeated calls give identical bits.  No workspace.
  * rows = 0 is a no-op.
