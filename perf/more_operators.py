@@ -292,7 +292,7 @@ def plain_adapters(s):
         wide[which, slot] = x
         h = torch.bmm(wide, a.transpose(1, 2).contiguous())
         d = torch.bmm(h, b.transpose(1, 2).contiguous())[which, slot]
-    y = s["base"].float()
+    y = s["base"].to(torch.float32, copy=True)
     y[row] += scale[:, None] * d
     out = {"y": y.to(TYPES[c["out"]])}
     if c["train"]:
