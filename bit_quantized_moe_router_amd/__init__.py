@@ -3,9 +3,9 @@
 Argument marshalling only: every function forwards device pointers (taken
 from torch tensors with ``.data_ptr()``) and the current HIP stream to the C
 ABI declared in include/moe.h, and raises MoEError on a non-OK status.  The
-microscaled 4-bit and balance-loss calls check their tensors' types, sizes and
-device as well.  All
-computation happens in the library's HIP kernels; there is no fallback.
+calls beside the layer (microscaled 4-bit, balance loss, routing from scores,
+combination, adapters) check their tensors' types, sizes and device as well.
+All computation happens in the library's HIP kernels; there is no fallback.
 """
 from __future__ import annotations
 
@@ -21,17 +21,25 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED_SH
 # Kernel ids of moe_profile_read.
 (K_LOGITS, K_TOPK, K_META, K_GATEUP_GEMM, K_DOWN_GEMM, K_GATEUP_GEMV, K_DOWN_GEMV, K_COMBINE, K_DEQUANT,
  K_PROBE_READ, K_PROBE_MFMA, K_MX4_QUANTIZE, K_MX4_DEQUANTIZE,
- K_MX4_EXPERTS, K_BALANCE, K_BALANCE_GRAD) = range(16)
+ K_MX4_EXPERTS, K_BALANCE, K_BALANCE_GRAD, K_SELECT, K_SELECT_GRAD, K_SORT, K_COMBINE_ROWS, K_COMBINE_GRAD,
+ K_ADAPTERS, K_ADAPTERS_GRAD) = range(23)
 KERNEL_NAMES = {K_LOGITS: "k_screen|k_logits_small", K_TOPK: "k_route_exact", K_META: "k_meta|k_topk_meta",
                 K_GATEUP_GEMM: "k_gateup_gemm", K_DOWN_GEMM: "k_down_gemm",
                 K_GATEUP_GEMV: "k_gemv_experts", K_DOWN_GEMV: "k_gemv_reduce", K_COMBINE: "k_combine",
                 K_DEQUANT: "k_dequant_active", K_PROBE_READ: "k_stream_read", K_PROBE_MFMA: "k_mfma_rate",
                 K_MX4_QUANTIZE: "k_mx4_quantize", K_MX4_DEQUANTIZE: "k_mx4_dequantize",
                 K_MX4_EXPERTS: "k_mx4_few|k_mx4_grid",
-                K_BALANCE: "k_balance_rows|k_balance_sum", K_BALANCE_GRAD: "k_balance_grad"}
+                K_BALANCE: "k_balance_rows|k_balance_sum", K_BALANCE_GRAD: "k_balance_grad",
+                K_SELECT: "k_select|k_sort_scan|k_sort_place", K_SELECT_GRAD: "k_select_grad",
+                K_SORT: "k_sort_count|k_sort_scan|k_sort_place", K_COMBINE_ROWS: "k_combine_rows",
+                K_COMBINE_GRAD: "k_combine_grad", K_ADAPTERS: "k_adapters_rows",
+                K_ADAPTERS_GRAD: "k_adapters_rows|k_adapters_sums"}
 
-# Element types of the microscaled 4-bit and balance-loss calls.
+# Element types of the calls beside the layer.
 MOE_F32, MOE_BF16, MOE_MX4 = range(3)
+
+# Scores of moe_select_forward.
+MOE_SOFTMAX, MOE_SIGMOID = range(2)
 
 
 class MoEError(RuntimeError):
@@ -48,6 +56,15 @@ class LayerDesc(C.Structure):
 
 class Mx4Desc(C.Structure):
     _fields_ = [(n, C.c_int32) for n in ("n_experts", "n", "k", "x_type", "y_type", "swiglu")]
+
+
+class SelectDesc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_experts", "top_k", "scores", "n_groups", "top_groups", "group_best",
+                                         "renormalise")] + [("scale", C.c_float)]
+
+
+class AdapterDesc(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("n_adapters", "rank", "n_in", "n_out", "y_type")]
 
 
 class QMatrix(C.Structure):
@@ -106,7 +123,21 @@ def lib():
         L.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, P(sz)]
         L.moe_balance_loss_forward.argtypes = [vp, i32, i32, i32, vp, i32, vp, f32, f32, vp, vp, vp, vp, vp, sz, vp]
         L.moe_balance_loss_backward.argtypes = [vp, i32, i32, i32, i32, vp, f32, f32, vp, vp, vp, vp, vp]
-        for name in ("moe_balance_loss_workspace_bytes", "moe_balance_loss_forward", "moe_balance_loss_backward",
+        S, A = P(SelectDesc), P(AdapterDesc)
+        L.moe_select_workspace_bytes.argtypes = [i32, i32, i32, P(sz)]
+        L.moe_select_forward.argtypes = [S, vp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_select_backward.argtypes = [S, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+        L.moe_sort_workspace_bytes.argtypes = [i32, i32, P(sz)]
+        L.moe_sort_assignments.argtypes = [vp, i32, i32, vp, vp, vp, vp, sz, vp]
+        L.moe_combine_forward.argtypes = [vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]
+        L.moe_combine_backward.argtypes = [vp, i32, vp, i32, i32, i32, i32, vp, vp, vp, vp, vp]
+        L.moe_adapters_forward.argtypes = [A, vp, vp, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, i32, vp, vp]
+        L.moe_adapters_workspace_bytes.argtypes = [A, i32, P(sz)]
+        L.moe_adapters_backward.argtypes = [A, vp, vp, vp, vp, i32, vp, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, vp,
+                                            sz, vp]
+        for name in ("moe_select_workspace_bytes", "moe_select_forward", "moe_select_backward", "moe_sort_workspace_bytes",
+                     "moe_sort_assignments", "moe_combine_forward", "moe_combine_backward", "moe_adapters_forward",
+                     "moe_adapters_workspace_bytes", "moe_adapters_backward", "moe_balance_loss_workspace_bytes", "moe_balance_loss_forward", "moe_balance_loss_backward",
                      "moe_mx4_experts", "moe_mx4_quantize", "moe_mx4_dequantize", "moe_packed_bytes", "moe_workspace_bytes", "moe_max_tiles", "moe_pack_weights",
                      "moe_route", "moe_forward_prefill", "moe_forward_decode", "moe_forward_decode_static",
                      "moe_probe_stream_read", "moe_probe_mfma_rate", "moe_profile_enable",
@@ -315,6 +346,214 @@ def moe_balance_loss_backward(logits, top_k, valid, balance_coef, z_coef, counts
                _arg(counts, "counts", torch.int32, E, dev), _arg(n_valid, "n_valid", torch.int32, 1, dev),
                None if grad_loss is None else _arg(grad_loss, "grad_loss", torch.float32, 1, dev),
                _arg(dlogits, "dlogits", logits.dtype, T * E, dev, E))
+
+
+def _bytes(ws, dev):
+    """(address, bytes) of a workspace, None for none."""
+    return (None, 0) if ws is None else (_arg(ws, "ws", _torch().uint8, ws.numel(), dev), ws.numel())
+
+
+def _matrix(t, name, rows, cols, dev=None):
+    """(type, address) of a contiguous float32 or bfloat16 matrix of this shape, (None, None) of None."""
+    if t is None:
+        return None, None
+    kind = _value_type(t, name)
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or not t.is_contiguous() or t.get_device() != dev:
+        _bad(f"{name} must be a contiguous [{rows}, {cols}] tensor on the call's device (got {tuple(t.shape)}, strides "
+             f"{t.stride()}, {t.device})")
+    return kind, t.data_ptr()
+
+
+def _same_type(kind, of, names):
+    if kind is not None and kind != of:
+        _bad(f"{names} must have one type")
+
+
+def make_select_desc(n_experts, top_k, scores=MOE_SOFTMAX, n_groups=1, top_groups=1, group_best=1, renormalise=1,
+                     scale=1.0) -> SelectDesc:
+    return SelectDesc(_int32(n_experts, "n_experts"), _int32(top_k, "top_k"), scores, _int32(n_groups, "n_groups"),
+                      _int32(top_groups, "top_groups"), group_best, renormalise, scale)
+
+
+def moe_select_workspace_bytes(T: int, n_experts: int, top_k: int) -> int:
+    n = C.c_size_t()
+    _check(lib().moe_select_workspace_bytes(_int32(T, "T"), _int32(n_experts, "n_experts"), _int32(top_k, "top_k"),
+                                            C.byref(n)))
+    return n.value
+
+
+def _select_logits(desc, logits):
+    """(T, E, k, type, device index, address)."""
+    if logits.dim() != 2 or logits.shape[1] != desc.n_experts or not logits.is_contiguous():
+        _bad(f"logits must be a contiguous [T, {desc.n_experts}] tensor (got {tuple(logits.shape)}, strides "
+             f"{logits.stride()})")
+    return (_int32(logits.shape[0], "T"), desc.n_experts, desc.top_k, _value_type(logits, "logits"), logits.get_device(),
+            logits.data_ptr())
+
+
+def moe_select_forward(desc, logits, bias, valid, topk_ids, topk_weights, expert_counts=None, expert_offsets=None,
+                       sorted_assign=None, ws=None, stream=None):
+    """logits [T, E], bias [E] float32 or None, valid [T] uint8/bool or None -> topk_ids [T, k] int32, topk_weights [T, k],
+    and, or all None, expert_counts [E], expert_offsets [E + 1], sorted_assign [T * k] int32."""
+    torch = _torch()
+    T, E, k, kind, dev, p = _select_logits(desc, logits)
+    i32, f32 = torch.int32, torch.float32
+    b = None if bias is None else _arg(bias, "bias", f32, E, dev)
+    v = None if valid is None else _arg(valid, "valid", torch.bool if valid.dtype is torch.bool else torch.uint8, T, dev)
+    order = (None, None, None)
+    if expert_counts is not None or expert_offsets is not None or sorted_assign is not None:
+        if expert_counts is None or expert_offsets is None or sorted_assign is None:
+            _bad("expert_counts, expert_offsets and sorted_assign go together")
+        order = (_arg(expert_counts, "expert_counts", i32, E, dev), _arg(expert_offsets, "expert_offsets", i32, E + 1, dev),
+                 _arg(sorted_assign, "sorted_assign", i32, T * k, dev, k if sorted_assign.dim() > 1 else None))
+    _on_device(dev, stream, lib().moe_select_forward, C.byref(desc), p, kind, T, b, v,
+               _arg(topk_ids, "topk_ids", i32, T * k, dev, k), _arg(topk_weights, "topk_weights", f32, T * k, dev, k), *order,
+               *_bytes(ws, dev))
+
+
+def moe_select_backward(desc, logits, topk_ids, topk_weights, dweights, base, dlogits, stream=None):
+    """dlogits = base (or zeros) + the gradient of moe_select_forward's weights for dweights [T, k]."""
+    torch = _torch()
+    T, E, k, kind, dev, p = _select_logits(desc, logits)
+    f32 = torch.float32
+    base_kind, bp = _matrix(base, "base", T, E, dev)
+    d_kind, dp = _matrix(dlogits, "dlogits", T, E, dev)
+    _same_type(base_kind, kind, "base and logits")
+    _same_type(d_kind, kind, "dlogits and logits")
+    _on_device(dev, stream, lib().moe_select_backward, C.byref(desc), p, kind, T,
+               _arg(topk_ids, "topk_ids", torch.int32, T * k, dev, k), _arg(topk_weights, "topk_weights", f32, T * k, dev, k),
+               _arg(dweights, "dweights", f32, T * k, dev, k), bp, dp)
+
+
+def moe_sort_workspace_bytes(n: int, n_experts: int) -> int:
+    b = C.c_size_t()
+    _check(lib().moe_sort_workspace_bytes(_int32(n, "n"), _int32(n_experts, "n_experts"), C.byref(b)))
+    return b.value
+
+
+def moe_sort_assignments(ids, n_experts, expert_counts, expert_offsets, sorted_assign, ws, stream=None):
+    """int32 ids (any shape) -> expert_counts [E], expert_offsets [E + 1], sorted_assign [ids.numel()] int32."""
+    torch = _torch()
+    n, E, i32, dev = _int32(ids.numel(), "the number of ids"), _int32(n_experts, "n_experts"), torch.int32, ids.get_device()
+    _on_device(dev, stream, lib().moe_sort_assignments, _arg(ids, "ids", i32, n, dev), n, E,
+               _arg(expert_counts, "expert_counts", i32, E, dev), _arg(expert_offsets, "expert_offsets", i32, E + 1, dev),
+               _arg(sorted_assign, "sorted_assign", i32, n, dev), *_bytes(ws, dev))
+
+
+def _combine_shape(rows, y, name, *by_place):
+    """(T, k, width, device index) from rows [T * k, width] and y or dy [T, width]; without tokens k is that of the first
+    [T, k] tensor."""
+    if rows.dim() != 2 or y.dim() != 2 or (rows.shape[0] % y.shape[0] if y.shape[0] else rows.shape[0]):
+        _bad(f"rows must be [T * k, width] and {name} [T, width] (got {tuple(rows.shape)}, {tuple(y.shape)})")
+    T = y.shape[0]
+    k = rows.shape[0] // T if T else next((t.shape[-1] for t in by_place if t is not None and t.dim() > 1), 1)
+    return _int32(T, "T"), _int32(k, "k"), _int32(y.shape[1], "width"), y.get_device()
+
+
+def moe_combine_forward(rows, topk_ids, weights, base, y, stream=None):
+    """y [T, width] = base (or zeros) + the sum over j of weights[t, j] * rows[t * k + j], without the rows whose id is
+    negative; rows [T * k, width], topk_ids [T, k] int32 or None, weights [T, k] float32 or None (1)."""
+    torch = _torch()
+    T, k, H, dev = _combine_shape(rows, y, "y", topk_ids, weights)
+    rows_kind, rp = _matrix(rows, "rows", T * k, H, dev)
+    kind, yp = _matrix(y, "y", T, H, dev)
+    base_kind, bp = _matrix(base, "base", T, H, dev)
+    _same_type(base_kind, kind, "base and y")
+    ids = None if topk_ids is None else _arg(topk_ids, "topk_ids", torch.int32, T * k, dev, k)
+    w = None if weights is None else _arg(weights, "weights", torch.float32, T * k, dev, k)
+    _on_device(dev, stream, lib().moe_combine_forward, rp, rows_kind, T, k, H, ids, w, bp, yp, kind)
+
+
+def moe_combine_backward(dy, rows, topk_ids, weights, drows, dweights, stream=None):
+    """The gradients drows [T * k, width] (of rows' type) and dweights [T, k] float32 for dy [T, width]; either may be
+    None, and rows where dweights is."""
+    torch = _torch()
+    like = rows if rows is not None else drows
+    if like is None:
+        _bad("rows is missing" if dweights is not None else "drows and dweights are both missing")
+    T, k, H, dev = _combine_shape(like, dy, "dy", topk_ids, weights, dweights)
+    kind, dp = _matrix(dy, "dy", T, H, dev)
+    rows_kind, rp = _matrix(rows, "rows", T * k, H, dev)
+    drows_kind, drp = _matrix(drows, "drows", T * k, H, dev)
+    if rows_kind is None:
+        rows_kind = drows_kind
+    _same_type(drows_kind, rows_kind, "drows and rows")
+    ids = None if topk_ids is None else _arg(topk_ids, "topk_ids", torch.int32, T * k, dev, k)
+    w = None if weights is None else _arg(weights, "weights", torch.float32, T * k, dev, k)
+    dw = None if dweights is None else _arg(dweights, "dweights", torch.float32, T * k, dev, k)
+    _on_device(dev, stream, lib().moe_combine_backward, dp, kind, rp, rows_kind, T, k, H, ids, w, drp, dw)
+
+
+def make_adapter_desc(n_adapters, rank, n_in, n_out, y_type) -> AdapterDesc:
+    return AdapterDesc(_int32(n_adapters, "n_adapters"), _int32(rank, "rank"), _int32(n_in, "n_in"), _int32(n_out, "n_out"),
+                       y_type)
+
+
+def moe_adapters_workspace_bytes(desc, rows: int) -> int:
+    n = C.c_size_t()
+    _check(lib().moe_adapters_workspace_bytes(C.byref(desc), _int32(rows, "rows"), C.byref(n)))
+    return n.value
+
+
+def _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows):
+    """What both directions take alike: (device index, the arguments up to dst_rows but for the rows of y)."""
+    torch = _torch()
+    n, r, K, N = desc.n_adapters, desc.rank, desc.n_in, desc.n_out
+    dev, bf16, i32 = x.get_device(), torch.bfloat16, torch.int32
+    if desc.y_type not in (MOE_F32, MOE_BF16):
+        _bad(f"y_type must be MOE_F32 or MOE_BF16 (got {desc.y_type})")
+    if x.dim() != 2 or x.shape[1] != K:
+        _bad(f"x must be 2-D with {K} columns (got {tuple(x.shape)})")
+    rows, src_div, x_rows = _int32(rows, "rows"), _int32(src_div, "src_div"), _int32(x.shape[0], "the number of x's rows")
+    return dict(dev=dev, rows=rows, src_div=src_div, x_rows=x_rows, a=_arg(a, "a", bf16, n * r * K, dev, K),
+                b=_arg(b, "b", bf16, n * N * r, dev, r), x=_arg(x, "x", bf16, x_rows * K, dev, K),
+                scales=None if scales is None else _arg(scales, "scales", torch.float32, n, dev),
+                offsets=_arg(offsets, "offsets", i32, n + 1, dev),
+                src=None if src_rows is None else _arg(src_rows, "src_rows", i32, rows, dev),
+                dst=None if dst_rows is None else _arg(dst_rows, "dst_rows", i32, rows, dev))
+
+
+def _adapter_rows(desc, t, name, dev):
+    """(rows, address) of y or dy."""
+    if t.dim() != 2:
+        _bad(f"{name} must be 2-D (got {tuple(t.shape)})")
+    kind, p = _matrix(t, name, t.shape[0], desc.n_out, dev)
+    if kind != desc.y_type:
+        _bad(f"{name} must have the descriptor's y_type (got {t.dtype})")
+    return _int32(t.shape[0], f"the number of {name}'s rows"), p
+
+
+def moe_adapters_forward(desc, a, b, scales, x, offsets, rows, base, y, h=None, src_rows=None, src_div=1, dst_rows=None,
+                         stream=None):
+    """Position i of adapter e's range gives y[dst_rows[i]] = base (or zeros) + scales[e] * b[e] (a[e] x[src_rows[i] //
+    src_div]); a [n, rank, n_in], b [n, n_out, rank], x bfloat16, scales [n] float32 or None, h [rows, rank] float32 or
+    None: a[e] x by position, for the backward call."""
+    A = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows)
+    dev = A["dev"]
+    y_rows, yp = _adapter_rows(desc, y, "y", dev)
+    base_kind, bp = _matrix(base, "base", y_rows, desc.n_out, dev)
+    _same_type(base_kind, desc.y_type, "base and y")
+    hp = None if h is None else _arg(h, "h", _torch().float32, A["rows"] * desc.rank, dev, desc.rank)
+    _on_device(dev, stream, lib().moe_adapters_forward, C.byref(desc), A["a"], A["b"], A["scales"], A["x"], A["x_rows"],
+               A["offsets"], A["rows"], A["src"], A["src_div"], A["dst"], bp, yp, y_rows, hp)
+
+
+def moe_adapters_backward(desc, a, b, scales, x, h, dy, offsets, rows, base, dx, da, db, ws=None, src_rows=None, src_div=1,
+                          dst_rows=None, stream=None):
+    """The gradients for dy: dx [x's rows * src_div (without src_rows x's rows), n_in] bfloat16 = base (or zeros) + ..., da
+    [n, rank, n_in] and db [n, n_out, rank] float32; dx (with base) and da with db may be None."""
+    torch = _torch()
+    A = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows)
+    dev, n, r, K, N = A["dev"], desc.n_adapters, desc.rank, desc.n_in, desc.n_out
+    y_rows, dyp = _adapter_rows(desc, dy, "dy", dev)
+    dx_rows = A["x_rows"] * (A["src_div"] if src_rows is not None else 1)
+    bf16, f32 = torch.bfloat16, torch.float32
+    _on_device(dev, stream, lib().moe_adapters_backward, C.byref(desc), A["a"], A["b"], A["scales"], A["x"], A["x_rows"],
+               None if h is None else _arg(h, "h", f32, A["rows"] * r, dev, r), dyp, y_rows, A["offsets"], A["rows"],
+               A["src"], A["src_div"], A["dst"], None if base is None else _arg(base, "base", bf16, dx_rows * K, dev, K),
+               None if dx is None else _arg(dx, "dx", bf16, dx_rows * K, dev, K),
+               None if da is None else _arg(da, "da", f32, n * r * K, dev, K),
+               None if db is None else _arg(db, "db", f32, n * N * r, dev, r), *_bytes(ws, dev))
 
 
 def make_desc(hidden, n_experts, top_k, inter, shared_inter, gemv_max_rows=-1, max_chunk=2048,

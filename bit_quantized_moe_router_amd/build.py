@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["pack.hip", "route.hip", "gemm.hip", "gemv.hip", "probe.hip", "mx4.hip", "mx4_experts.hip", "balance.hip",
-           "api.cpp"]
+           "select.hip", "combine.hip", "adapters_forward.hip", "adapters_backward.hip", "api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

@@ -202,7 +202,7 @@ int max_long_tiles(const moe_layer_desc* d) {
 }
 
 // ---- kernel timing (measurement mode) ----------------------------------------
-constexpr int kNumKernels = 16;
+constexpr int kNumKernels = 23;
 struct Pending {
   int kid;
   hipEvent_t a, b;
@@ -838,13 +838,7 @@ moe_status moe_mx4_experts(const moe_mx4_desc* d, const uint8_t* w_codes, const 
   TRY(check_device());
   Mx4ExpertArgs A{w_codes,   w_scales, x,        x_scales,  expert_offsets, src_rows, dst_rows,
                   row_scale, y,        y_scales, d->n_experts, d->n,        d->k,     rows,
-                  x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1, 0,        0};
-  if (src_div > 1) {
-    int log2 = 1;
-    while ((1ll << log2) < src_div) log2++;
-    A.src_magic = (uint32_t)((1ull << (31 + log2)) / (uint32_t)src_div + 1);
-    A.src_shift = log2 - 1;
-  }
+                  x_rows,    y_rows,   src_div,  d->y_type, d->x_type == MOE_MX4, d->swiglu == 1, divisor(src_div)};
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
   const MxKernel m = mx4_experts_kernel(A, cus);
@@ -955,6 +949,337 @@ moe_status moe_balance_loss_backward(const void* logits, int32_t logits_type, in
   A.dlogits = dlogits;
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(15, s, "balance loss gradient", [&](const KTime& kt) { return launch_balance_backward(A, s, kt); });
+}
+
+static moe_status value_type(const void* p, int32_t type, const char* name) {
+  if (type != MOE_F32 && type != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s must be MOE_F32 or MOE_BF16 (got type %d)", name, type);
+  if (reinterpret_cast<uintptr_t>(p) & (type == MOE_F32 ? 3 : 1))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "%s is not aligned to its type", name);
+  return MOE_OK;
+}
+
+static moe_status select_shape(const moe_select_desc* d, int32_t T) {
+  if (!d) return fail(MOE_ERR_INVALID_ARGUMENT, "desc is null");
+  TRY(balance_shape(T, d->n_experts, d->top_k));
+  if (d->scores != MOE_SOFTMAX && d->scores != MOE_SIGMOID)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scores must be MOE_SOFTMAX or MOE_SIGMOID (got %d)", d->scores);
+  if (d->n_groups < 1 || d->n_groups > 64 || d->n_experts % d->n_groups)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_groups must be in 1..64 and divide n_experts (got %d of %d)", d->n_groups,
+                d->n_experts);
+  if (d->top_groups < 1 || d->top_groups > d->n_groups)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "top_groups must be in 1..n_groups (got %d of %d)", d->top_groups, d->n_groups);
+  if (d->group_best != 1 && d->group_best != 2)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "group_best must be 1 or 2 (got %d)", d->group_best);
+  if (d->top_k > d->top_groups * (d->n_experts / d->n_groups))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "top_k (%d) exceeds the %d experts of top_groups groups", d->top_k,
+                d->top_groups * (d->n_experts / d->n_groups));
+  if (d->renormalise != 0 && d->renormalise != 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "renormalise must be 0 or 1 (got %d)", d->renormalise);
+  if (!(d->scale - d->scale == 0.f) || d->scale == 0.f)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "scale must be finite and not zero");
+  return MOE_OK;
+}
+
+static SelectArgs select_args(const moe_select_desc* d, const void* logits, int32_t type, int32_t T) {
+  SelectArgs A{};
+  A.logits = logits;
+  A.T = T;
+  A.E = d->n_experts;
+  A.k = d->top_k;
+  // Groups that all stay, or that are single experts by their own score and index, leave every expert to choose from.
+  A.groups = d->top_groups == d->n_groups ? 1 : d->n_groups;
+  A.per = d->n_experts / A.groups;
+  A.top_groups = d->top_groups;
+  A.best = d->group_best;
+  A.f32 = type == MOE_F32;
+  A.softmax = d->scores == MOE_SOFTMAX;
+  A.renorm = d->renormalise == 1;
+  A.scale = d->scale;
+  return A;
+}
+
+static moe_status sort_ws(size_t need, void* ws, size_t ws_bytes) {
+  if (ws_bytes < need) return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes < required %zu", ws_bytes, need);
+  if (need && !ws) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(MOE_ERR_INVALID_ARGUMENT, "ws must be 16-byte aligned");
+  return MOE_OK;
+}
+
+static size_t sort_bytes(int parts, int32_t E) { return al((size_t)parts * E * 4); }
+
+moe_status moe_select_workspace_bytes(int32_t T, int32_t n_experts, int32_t top_k, size_t* bytes) {
+  TRY(balance_shape(T, n_experts, top_k));
+  if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+  *bytes = sort_bytes(select_parts(T), n_experts);
+  return MOE_OK;
+}
+
+moe_status moe_select_forward(const moe_select_desc* d, const void* logits, int32_t logits_type, int32_t T,
+                              const float* bias, const uint8_t* valid, int32_t* topk_ids, float* topk_weights,
+                              int32_t* expert_counts, int32_t* expert_offsets, int32_t* sorted_assign, void* ws,
+                              size_t ws_bytes, void* stream) {
+  TRY(select_shape(d, T));
+  TRY(value_type(logits, logits_type, "logits"));
+  const bool order = expert_counts || expert_offsets || sorted_assign;
+  if (T > 0 && (!logits || !topk_ids || !topk_weights)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (order && (!expert_counts || !expert_offsets || (T > 0 && !sorted_assign)))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "expert_counts, expert_offsets and sorted_assign go together");
+  if (order) TRY(sort_ws(sort_bytes(select_parts(T), d->n_experts), ws, ws_bytes));
+  if (T == 0 && !order) return MOE_OK;
+  TRY(check_device());
+  SelectArgs A = select_args(d, logits, logits_type, T);
+  A.bias = bias;
+  A.valid = valid;
+  A.ids = topk_ids;
+  A.weights = topk_weights;
+  SortArgs S{};
+  if (order) {
+    S.ids = topk_ids;
+    S.n = (int64_t)T * d->top_k;
+    S.E = d->n_experts;
+    S.counts = expert_counts;
+    S.offsets = expert_offsets;
+    S.sorted = sorted_assign;
+    S.part_count = static_cast<int32_t*>(ws);
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(16, s, "routing from scores", [&](const KTime& kt) { return launch_select_forward(A, S, order, s, kt); });
+}
+
+moe_status moe_select_backward(const moe_select_desc* d, const void* logits, int32_t logits_type, int32_t T,
+                               const int32_t* topk_ids, const float* topk_weights, const float* dweights,
+                               const void* base, void* dlogits, void* stream) {
+  TRY(select_shape(d, T));
+  TRY(value_type(logits, logits_type, "logits"));
+  TRY(value_type(base, logits_type, "base"));
+  TRY(value_type(dlogits, logits_type, "dlogits"));
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_weights || !dweights || !dlogits)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if (base == logits) return fail(MOE_ERR_INVALID_ARGUMENT, "base must not be the logits");
+  TRY(check_device());
+  SelectArgs A = select_args(d, logits, logits_type, T);
+  A.ids = const_cast<int32_t*>(topk_ids);
+  A.weights = const_cast<float*>(topk_weights);
+  A.dweights = dweights;
+  A.base = base;
+  A.dlogits = dlogits;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(17, s, "routing gradient", [&](const KTime& kt) { return launch_select_backward(A, s, kt); });
+}
+
+static moe_status sort_shape(int32_t n, int32_t E) {
+  if (n < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "n must be >= 0 (got %d)", n);
+  if (E < 1 || E > 512) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_experts must be in 1..512 (got %d)", E);
+  return MOE_OK;
+}
+
+moe_status moe_sort_workspace_bytes(int32_t n, int32_t n_experts, size_t* bytes) {
+  TRY(sort_shape(n, n_experts));
+  if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+  *bytes = sort_bytes(sort_parts(n), n_experts);
+  return MOE_OK;
+}
+
+moe_status moe_sort_assignments(const int32_t* ids, int32_t n, int32_t n_experts, int32_t* expert_counts,
+                                int32_t* expert_offsets, int32_t* sorted_assign, void* ws, size_t ws_bytes,
+                                void* stream) {
+  TRY(sort_shape(n, n_experts));
+  if (!expert_counts || !expert_offsets || (n > 0 && (!ids || !sorted_assign)))
+    return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  TRY(sort_ws(sort_bytes(sort_parts(n), n_experts), ws, ws_bytes));
+  TRY(check_device());
+  SortArgs S{};
+  S.ids = ids;
+  S.n = n;
+  S.E = n_experts;
+  S.counts = expert_counts;
+  S.offsets = expert_offsets;
+  S.sorted = sorted_assign;
+  S.part_count = static_cast<int32_t*>(ws);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(18, s, "order by expert", [&](const KTime& kt) { return launch_sort(S, s, kt); });
+}
+
+static moe_status combine_shape(int32_t T, int32_t k, int32_t width) {
+  if (T < 0) return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0 (got %d)", T);
+  if (k < 1 || k > 16) return fail(MOE_ERR_INVALID_ARGUMENT, "k must be in 1..16 (got %d)", k);
+  if (width < 1 || width > 1 << 24)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "width must be in 1..2^24 (got %d)", width);
+  if ((int64_t)T * k > 0x7FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "T * k must be below 2^31 (got %d * %d)", T, k);
+  return MOE_OK;
+}
+
+moe_status moe_combine_forward(const void* rows, int32_t rows_type, int32_t T, int32_t k, int32_t width,
+                               const int32_t* topk_ids, const float* weights, const void* base, void* y, int32_t y_type,
+                               void* stream) {
+  TRY(combine_shape(T, k, width));
+  TRY(value_type(rows, rows_type, "rows"));
+  TRY(value_type(base, y_type, "base"));
+  TRY(value_type(y, y_type, "y"));
+  if (T == 0) return MOE_OK;
+  if (!rows || !y) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  TRY(check_device());
+  CombineArgs A{};
+  A.rows = rows;
+  A.ids = topk_ids;
+  A.weights = weights;
+  A.base = base;
+  A.y = y;
+  A.T = T;
+  A.k = k;
+  A.H = width;
+  A.rows_f32 = rows_type == MOE_F32;
+  A.y_f32 = y_type == MOE_F32;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(19, s, "combine", [&](const KTime& kt) { return launch_combine_forward(A, s, kt); });
+}
+
+moe_status moe_combine_backward(const void* dy, int32_t y_type, const void* rows, int32_t rows_type, int32_t T, int32_t k,
+                                int32_t width, const int32_t* topk_ids, const float* weights, void* drows, float* dweights,
+                                void* stream) {
+  TRY(combine_shape(T, k, width));
+  TRY(value_type(dy, y_type, "dy"));
+  TRY(value_type(rows, rows_type, "rows"));
+  TRY(value_type(drows, rows_type, "drows"));
+  if (T == 0 || (!drows && !dweights)) return MOE_OK;
+  if (!dy || (dweights && !rows)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  TRY(check_device());
+  CombineArgs A{};
+  A.rows = rows;
+  A.ids = topk_ids;
+  A.weights = weights;
+  A.T = T;
+  A.k = k;
+  A.H = width;
+  A.rows_f32 = rows_type == MOE_F32;
+  A.y_f32 = y_type == MOE_F32;
+  A.dy = dy;
+  A.drows = drows;
+  A.dweights = dweights;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(20, s, "combine gradient", [&](const KTime& kt) { return launch_combine_backward(A, s, kt); });
+}
+
+static moe_status adapter_shape(const moe_adapter_desc* d, int32_t rows) {
+  if (!d) return fail(MOE_ERR_INVALID_ARGUMENT, "desc is null");
+  if (d->n_adapters < 1 || d->n_adapters > 512)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_adapters must be in 1..512 (got %d)", d->n_adapters);
+  if (d->rank < 1 || d->rank > 128) return fail(MOE_ERR_UNSUPPORTED_SHAPE, "rank must be in 1..128 (got %d)", d->rank);
+  if (d->n_in < 1 || d->n_in > 65536 || d->n_out < 1 || d->n_out > 65536)
+    return fail(MOE_ERR_UNSUPPORTED_SHAPE, "n_in and n_out must be in 1..65536 (got %d, %d)", d->n_in, d->n_out);
+  if (d->y_type != MOE_F32 && d->y_type != MOE_BF16)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "y_type must be MOE_F32 or MOE_BF16 (got %d)", d->y_type);
+  if (rows < 0 || rows > 1 << 24) return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be in 0..2^24 (got %d)", rows);
+  return MOE_OK;
+}
+
+// What both directions check of the positions and their rows (rows > 0).
+static moe_status adapter_args(const moe_adapter_desc* d, const uint16_t* a, const uint16_t* b, const float* scales,
+                               const uint16_t* x, int32_t x_rows, const int32_t* offsets, int32_t rows,
+                               const int32_t* src_rows, int32_t src_div, const int32_t* dst_rows, int32_t y_rows,
+                               AdapterArgs* A) {
+  if (x_rows < 1 || y_rows < 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "x_rows and y_rows must be positive (got %d, %d)", x_rows, y_rows);
+  if (src_div < 1) return fail(MOE_ERR_INVALID_ARGUMENT, "src_div must be positive (got %d)", src_div);
+  if (!a || !b || !x || !offsets) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  if ((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(x)) & 1)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "a, b and x must be aligned to their type");
+  if (!src_rows && rows > x_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "without src_rows x needs a row per position (%d < %d)", x_rows, rows);
+  if (!dst_rows && rows > y_rows)
+    return fail(MOE_ERR_INVALID_ARGUMENT, "without dst_rows y needs a row per position (%d < %d)", y_rows, rows);
+  A->a = a;
+  A->b = b;
+  A->scales = scales;
+  A->x = x;
+  A->offsets = offsets;
+  A->src_rows = src_rows;
+  A->dst_rows = dst_rows;
+  A->n = d->n_adapters;
+  A->r = d->rank;
+  A->K = d->n_in;
+  A->N = d->n_out;
+  A->P = rows;
+  A->x_rows = x_rows;
+  A->y_rows = y_rows;
+  A->src_div = src_rows ? src_div : 1;
+  A->src = divisor(src_div);
+  return MOE_OK;
+}
+
+moe_status moe_adapters_forward(const moe_adapter_desc* d, const uint16_t* a, const uint16_t* b, const float* scales,
+                                const uint16_t* x, int32_t x_rows, const int32_t* offsets, int32_t rows,
+                                const int32_t* src_rows, int32_t src_div, const int32_t* dst_rows, const void* base, void* y,
+                                int32_t y_rows, float* h, void* stream) {
+  TRY(adapter_shape(d, rows));
+  if (rows == 0) return MOE_OK;
+  AdapterArgs A{};
+  TRY(adapter_args(d, a, b, scales, x, x_rows, offsets, rows, src_rows, src_div, dst_rows, y_rows, &A));
+  TRY(value_type(y, d->y_type, "y"));
+  TRY(value_type(base, d->y_type, "base"));
+  if (!y) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+  TRY(check_device());
+  A.base = base;
+  A.y = y;
+  A.h_out = h;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int cus = device_cus();
+  return timed(21, s, "adapters", [&](const KTime& kt) {
+    return launch_adapters_forward(A, d->y_type == MOE_F32, cus, s, kt);
+  });
+}
+
+moe_status moe_adapters_workspace_bytes(const moe_adapter_desc* d, int32_t rows, size_t* bytes) {
+  TRY(adapter_shape(d, rows));
+  if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+  *bytes = al((size_t)rows * d->rank * 4);
+  return MOE_OK;
+}
+
+moe_status moe_adapters_backward(const moe_adapter_desc* d, const uint16_t* a, const uint16_t* b, const float* scales,
+                                 const uint16_t* x, int32_t x_rows, const float* h, const void* dy, int32_t y_rows,
+                                 const int32_t* offsets, int32_t rows, const int32_t* src_rows, int32_t src_div,
+                                 const int32_t* dst_rows, const void* base, void* dx, float* da, float* db, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  TRY(adapter_shape(d, rows));
+  if ((da == nullptr) != (db == nullptr)) return fail(MOE_ERR_INVALID_ARGUMENT, "da and db go together");
+  if (!dx && base) return fail(MOE_ERR_INVALID_ARGUMENT, "base goes with dx");
+  if (!dx && !da) return MOE_OK;
+  AdapterArgs A{};
+  if (rows > 0) {
+    TRY(adapter_args(d, a, b, scales, x, x_rows, offsets, rows, src_rows, src_div, dst_rows, y_rows, &A));
+    TRY(value_type(dy, d->y_type, "dy"));
+    TRY(value_type(base, MOE_BF16, "base"));
+    TRY(value_type(dx, MOE_BF16, "dx"));
+    if (!dy || (da && !h)) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+    size_t need = 0;
+    TRY(moe_adapters_workspace_bytes(d, rows, &need));
+    if (da) TRY(sort_ws(need, ws, ws_bytes));
+  } else {
+    if (!da) return MOE_OK;
+    if (!offsets) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");
+    A.offsets = offsets;
+    A.n = d->n_adapters;
+    A.r = d->rank;
+    A.K = d->n_in;
+    A.N = d->n_out;
+  }
+  TRY(check_device());
+  A.h = h;
+  A.dy = dy;
+  A.base = base;
+  A.dx = dx;
+  A.da = da;
+  A.db = db;
+  A.dh = A.h_out = da ? static_cast<float*>(ws) : nullptr;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int cus = device_cus();
+  return timed(22, s, "adapters gradient", [&](const KTime& kt) {
+    return launch_adapters_backward(A, d->y_type == MOE_F32, cus, s, kt);
+  });
 }
 
 const char* moe_status_str(moe_status s) {

@@ -1,0 +1,199 @@
+// The sum over each token's routed rows, and its gradients:
+//   y_t = base_t + sum_j w_tj r_tj,   dr_tj = w_tj dy_t,   dw_tj = <dy_t, r_tj>
+// over the j whose id is not negative.
+//
+// Bound by the bytes of the rows, in small calls by the way ids -> rows -> sum.
+// Forward: threads split the columns, each sums its columns over j in order,
+// with all of a token's rows in flight.  Backward: one pass over the rows
+// gives both gradients, a token a wave (or four, where there are few tokens),
+// whose lanes hold the k dot products until the end.
+#include <type_traits>
+
+#include "launch.h"
+#include "vec.h"
+
+namespace moe {
+
+constexpr int kCombThreads = 256, kCombBatch = 8;
+
+// The columns of a thread: 16 bytes of a row.
+template <bool RF32>
+constexpr int kCombCols = RF32 ? 4 : 8;
+
+// tpr threads a row (a power of two up to 256).  Whole: a wave has one row, so
+// that ids and weights are read by the scalar unit and a left-out row is
+// skipped by a branch of the whole wave.
+template <bool RF32, bool YF32, bool Whole>
+__global__ __launch_bounds__(kCombThreads) void k_combine_rows(CombineArgs A, int tpr_log2) {
+  constexpr int V = kCombCols<RF32>, kR = RF32 ? 4 : 2, kY = YF32 ? 4 : 2;
+  const int tpr = 1 << tpr_log2, per = kCombThreads >> tpr_log2;
+  const int part = threadIdx.x & (tpr - 1);
+  const int64_t step = (int64_t)gridDim.x * per;
+  const int64_t H = A.H;
+  for (int64_t t0 = (int64_t)blockIdx.x * per; t0 < A.T; t0 += step) {
+    int sub = threadIdx.x >> tpr_log2;
+    if constexpr (Whole) sub = __builtin_amdgcn_readfirstlane(sub);
+    const int64_t t = t0 + sub;
+    if (t >= A.T) break;
+    for (int64_t c = (int64_t)part * V; c < H; c += (int64_t)tpr * V) {
+      const int n = (int)min((int64_t)V, H - c);
+      float acc[V] = {};
+      if (A.base) {
+        RowPiece<YF32, V> b;
+        b.load(static_cast<const char*>(A.base) + (t * H + c) * kY, n);
+#pragma unroll
+        for (int i = 0; i < V; i++) acc[i] = b.get(i);
+      }
+      for (int j0 = 0; j0 < A.k; j0 += kCombBatch) {
+        RowPiece<RF32, V> r[kCombBatch];
+        float w[kCombBatch];
+        bool on[kCombBatch];
+#pragma unroll
+        for (int u = 0; u < kCombBatch; u++) {
+          const int64_t a = t * A.k + j0 + u;
+          on[u] = j0 + u < A.k && (!A.ids || A.ids[a] >= 0);
+          w[u] = on[u] && A.weights ? A.weights[a] : 1.f;
+        }
+#pragma unroll
+        for (int u = 0; u < kCombBatch; u++) {
+          r[u].clear();
+          if (on[u]) r[u].load(static_cast<const char*>(A.rows) + ((t * A.k + j0 + u) * H + c) * kR, n);
+        }
+#pragma unroll
+        for (int u = 0; u < kCombBatch; u++) {
+          if (!on[u]) continue;
+#pragma unroll
+          for (int i = 0; i < V; i++) acc[i] = fmaf(w[u], r[u].get(i), acc[i]);
+        }
+      }
+      RowPiece<YF32, V> y;
+      y.set(acc);
+      y.store(static_cast<char*>(A.y) + (t * H + c) * kY, n);
+    }
+  }
+}
+
+__device__ __forceinline__ float comb_wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// A token by `Waves` waves of a workgroup of four; KB: k rounded up.
+template <bool RF32, bool YF32, int KB, int Waves>
+__global__ __launch_bounds__(kCombThreads) void k_combine_grad(CombineArgs A) {
+  constexpr int V = kCombCols<RF32>, kR = RF32 ? 4 : 2, kY = YF32 ? 4 : 2;
+  constexpr int kTokens = 4 / Waves, kCols = Waves * 64 * V;
+  __shared__ float s_dot[Waves > 1 ? Waves : 1][KB];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int64_t H = A.H, step = (int64_t)gridDim.x * kTokens;
+  // With Waves = 4 the loop's condition is the workgroup's, so that all of it meets at the barriers.
+  for (int64_t t = (int64_t)blockIdx.x * kTokens + (Waves == 1 ? wave : 0); t < A.T; t += step) {
+    float w[KB], dot[KB] = {};
+    bool on[KB];
+#pragma unroll
+    for (int j = 0; j < KB; j++) {
+      const int64_t a = t * A.k + j;
+      on[j] = j < A.k && (!A.ids || A.ids[a] >= 0);
+      w[j] = !on[j] ? 0.f : A.weights ? A.weights[a] : 1.f;
+    }
+    for (int64_t c = ((Waves == 1 ? 0 : wave * 64) + lane) * V; c < H; c += kCols) {
+      const int n = (int)min((int64_t)V, H - c);
+      RowPiece<YF32, V> d;
+      d.load(static_cast<const char*>(A.dy) + (t * H + c) * kY, n);
+      RowPiece<RF32, V> r[KB];
+      if (A.dweights) {
+#pragma unroll
+        for (int j = 0; j < KB; j++) {
+          r[j].clear();
+          if (on[j]) r[j].load(static_cast<const char*>(A.rows) + ((t * A.k + j) * H + c) * kR, n);
+        }
+#pragma unroll
+        for (int j = 0; j < KB; j++) {
+          if (!on[j]) continue;
+#pragma unroll
+          for (int i = 0; i < V; i++) dot[j] = fmaf(d.get(i), r[j].get(i), dot[j]);
+        }
+      }
+      if (A.drows) {
+#pragma unroll
+        for (int j = 0; j < KB; j++) {
+          if (j >= A.k) continue;
+          float v[V];
+#pragma unroll
+          for (int i = 0; i < V; i++) v[i] = on[j] ? w[j] * d.get(i) : 0.f;
+          r[j].set(v);
+          r[j].store(static_cast<char*>(A.drows) + ((t * A.k + j) * H + c) * kR, n);
+        }
+      }
+    }
+    if (!A.dweights) continue;
+#pragma unroll
+    for (int j = 0; j < KB; j++) dot[j] = comb_wave_sum(dot[j]);
+    if constexpr (Waves == 1) {
+      float mine = 0.f;
+#pragma unroll
+      for (int j = 0; j < KB; j++) mine = lane == j ? dot[j] : mine;
+      if (lane < A.k) A.dweights[t * A.k + lane] = mine;
+    } else {
+      if (lane == 0) {
+#pragma unroll
+        for (int j = 0; j < KB; j++) s_dot[wave][j] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < A.k) {
+        float sum = 0.f;
+#pragma unroll
+        for (int v = 0; v < Waves; v++) sum += s_dot[v][threadIdx.x];
+        A.dweights[t * A.k + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// At most this many workgroups; each goes through several tokens beyond them.
+constexpr int64_t kCombGrid = 1 << 20;
+
+hipError_t launch_combine_forward(const CombineArgs& A, hipStream_t s, const KTime& kt) {
+  const int V = A.rows_f32 ? 4 : 8;
+  const int64_t pieces = (A.H + V - 1) / V;
+  int log2 = 0;
+  while (log2 < 8 && (1 << log2) < pieces) log2++;
+  const int64_t per = kCombThreads >> log2, groups = (A.T + per - 1) / per;
+  const dim3 grid((unsigned)(groups < kCombGrid ? groups : kCombGrid));
+  auto go = [&](auto rf, auto yf) {
+    constexpr bool RF = rf.value, YF = yf.value;
+    auto* f = log2 >= 6 ? k_combine_rows<RF, YF, true> : k_combine_rows<RF, YF, false>;
+    MOE_LAUNCH(f, grid, dim3(kCombThreads), 0, s, kt.start, kt.stop, A, log2);
+  };
+  using std::false_type;
+  using std::true_type;
+  if (A.rows_f32) A.y_f32 ? go(true_type{}, true_type{}) : go(true_type{}, false_type{});
+  else A.y_f32 ? go(false_type{}, true_type{}) : go(false_type{}, false_type{});
+  return hipGetLastError();
+}
+
+template <bool RF, bool YF>
+static void launch_grad(const CombineArgs& A, hipStream_t s, const KTime& kt) {
+  const bool four = A.T < 1024 && A.H > 64 * kCombCols<RF>;
+  const int64_t groups = four ? A.T : (A.T + 3) / 4;
+  const dim3 grid((unsigned)(groups < kCombGrid ? groups : kCombGrid));
+  auto go = [&](auto kb) {
+    constexpr int KB = kb.value;
+    auto* f = four ? k_combine_grad<RF, YF, KB, 4> : k_combine_grad<RF, YF, KB, 1>;
+    MOE_LAUNCH(f, grid, dim3(kCombThreads), 0, s, kt.start, kt.stop, A);
+  };
+  if (A.k <= 4) go(std::integral_constant<int, 4>{});
+  else if (A.k <= 8) go(std::integral_constant<int, 8>{});
+  else go(std::integral_constant<int, 16>{});
+}
+
+hipError_t launch_combine_backward(const CombineArgs& A, hipStream_t s, const KTime& kt) {
+  auto* f = A.rows_f32 ? (A.y_f32 ? launch_grad<true, true> : launch_grad<true, false>)
+                       : (A.y_f32 ? launch_grad<false, true> : launch_grad<false, false>);
+  f(A, s, kt);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -6,6 +6,7 @@
 #include <atomic>
 
 #include "common.h"
+#include "positions.h"
 
 namespace moe {
 
@@ -137,12 +138,7 @@ struct Mx4ExpertArgs {
   uint8_t* y_scales;         // [y_rows][n_out / 32] with y_type = kMxTypeMx4
   int E, n, k, P, x_rows, y_rows, src_div, y_type;
   bool x_mx4, swiglu;
-  // r / src_div = (r * src_magic >> 32) >> src_shift for 0 <= r < 2^31, src_div >= 2.  With L = ceil(log2 src_div),
-  // src_shift = L - 1 and src_magic = floor(2^(31 + L) / src_div) + 1, so src_magic * src_div = 2^(31 + L) + e with
-  // 0 < e <= src_div: the quotient is off by r e / (src_div 2^(31 + L)) < 2^-L <= 1 / src_div, too little to reach
-  // the next whole number.
-  uint32_t src_magic;
-  int src_shift;
+  Divisor src;  // by src_div
 };
 // The kernels of the product: few rows an expert (kFewSplit: the waves split K); tiles of 256 weight rows (k16Half:
 // 128) by 256, 128 or 32 positions for rows of 4 or 16 bits, Odd where the scales' rows are no whole 16-byte pieces.
@@ -180,6 +176,85 @@ struct BalanceArgs {
 int balance_parts(int T, int E);
 hipError_t launch_balance_forward(const BalanceArgs& A, hipStream_t s, const KTime& kt = KTime{});
 hipError_t launch_balance_backward(const BalanceArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
+// Routing from scores and the order of assignments by expert (select.hip).
+constexpr int kSortMaxParts = 256;  // parts of the assignments that are counted apart
+struct SelectArgs {
+  const void* logits;    // [T][E] fp32 or bf16
+  const float* bias;     // [E] or null
+  const uint8_t* valid;  // [T] or null
+  int32_t* ids;          // [T][k]
+  float* weights;        // [T][k]
+  int T, E, k, groups, per, top_groups, best;  // per: experts a group
+  bool f32, softmax, renorm;
+  float scale;
+  int64_t per_part;      // tokens a part
+  int32_t* part_count;   // [parts][E] or null
+  // Backward pass.
+  const float* dweights; // [T][k]
+  const void* base;      // [T][E] of the logits' type, or null
+  void* dlogits;
+};
+struct SortArgs {
+  const int32_t* ids;    // [n]
+  int64_t n;
+  int E;
+  int32_t* counts;       // [E]
+  int32_t* offsets;      // [E + 1]
+  int32_t* sorted;       // [n]
+  int32_t* part_count;   // [kSortMaxParts][E], then the parts' prefix sums
+  int parts;
+  int64_t per_part;      // assignments a part
+};
+// Parts of n assignments, and of T tokens whose experts are to be chosen (1: no partial counts).
+int sort_parts(int64_t n);
+int select_parts(int T);
+hipError_t launch_sort(SortArgs S, hipStream_t s, const KTime& kt = KTime{});
+// order: counts, offsets and the sorted assignments too.
+hipError_t launch_select_forward(SelectArgs A, SortArgs S, bool order, hipStream_t s, const KTime& kt = KTime{});
+hipError_t launch_select_backward(const SelectArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
+// The sum over each token's routed rows (combine.hip).
+struct CombineArgs {
+  const void* rows;      // [T * k][H] fp32 or bf16
+  const int32_t* ids;    // [T][k] or null
+  const float* weights;  // [T][k] or null
+  const void* base;      // [T][H] of y's type, or null
+  void* y;               // [T][H] fp32 or bf16
+  int T, k, H;
+  bool rows_f32, y_f32;
+  // Backward pass.
+  const void* dy;        // [T][H] of y's type
+  void* drows;           // [T * k][H] of rows' type, or null
+  float* dweights;       // [T][k] or null
+};
+hipError_t launch_combine_forward(const CombineArgs& A, hipStream_t s, const KTime& kt = KTime{});
+hipError_t launch_combine_backward(const CombineArgs& A, hipStream_t s, const KTime& kt = KTime{});
+
+// Low-rank adapters (adapters.h).
+struct AdapterArgs {
+  const uint16_t* a;        // [n][r][K] bf16
+  const uint16_t* b;        // [n][N][r] bf16
+  const float* scales;      // [n] or null
+  const uint16_t* x;        // [x_rows][K] bf16
+  const int32_t* offsets;   // [n + 1]
+  const int32_t* src_rows;  // [P] or null
+  const int32_t* dst_rows;  // [P] or null
+  const void* base;         // forward [y_rows][N] of y's type, backward [..][K] bf16; or null
+  void* y;                  // [y_rows][N] fp32 or bf16
+  float* h_out;             // [P][r]: h of the forward, dh of the backward pass, or null
+  int n, r, K, N, P, x_rows, y_rows, src_div;
+  Divisor src;              // by src_div
+  // Backward pass.
+  const float* h;           // [P][r]
+  const float* dh;          // [P][r]: h_out of its first kernel
+  const void* dy;           // [y_rows][N] of y's type
+  void* dx;                 // [x_rows * src_div][K] bf16 or null
+  float* da;                // [n][r][K] or null, with db
+  float* db;                // [n][N][r]
+};
+hipError_t launch_adapters_forward(const AdapterArgs& A, bool y_f32, int cus, hipStream_t s, const KTime& kt = KTime{});
+hipError_t launch_adapters_backward(const AdapterArgs& A, bool y_f32, int cus, hipStream_t s, const KTime& kt = KTime{});
 
 // Measurement probes (csrc/probe.hip): a 16-byte-per-lane streaming read of
 // `bytes` with at most max_wgs workgroups (sink: max_wgs words), and the

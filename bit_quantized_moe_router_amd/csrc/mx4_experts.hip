@@ -15,6 +15,7 @@
 
 #include "launch.h"
 #include "mx4.h"
+#include "positions.h"
 
 namespace moe {
 
@@ -22,65 +23,9 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 constexpr int kE2m1 = 4;  // operand type code of the scaled matrix instructions
 
-struct MxTile {
-  int e, row, rows;  // expert, first position, positions (at most BT)
-};
-
-// Tile number `tile` of the order (expert, BT positions at a time), found by
-// every wave from the offsets alone: lane l sums the tiles of E/64 consecutive
-// experts, a scan over the lanes gives each its first tile.  Offsets are held
-// inside [0, P] and made increasing, so that whatever they are no position
-// outside the arrays is reached.  The loads do not wait for each other: this
-// stands before everything else a small call does.
-template <int BT>
-__device__ __forceinline__ bool mx4_find_tile(const int32_t* __restrict__ offsets, int E, int P, int tile, MxTile* out) {
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) >> 6;  // at most 8
-  const int e0 = lane * per;
-  int off[9];
-#pragma unroll
-  for (int j = 0; j <= 8; j++)
-    if (j <= per) off[j] = offsets[min(e0 + j, E)];  // past the last expert: no tiles
-  int n[8], mine = 0;
-#pragma unroll
-  for (int j = 0; j < 8; j++) {
-    n[j] = 0;
-    if (j < per) {
-      const int lo = min(max(off[j], 0), P), hi = min(max(off[j + 1], lo), P);
-      n[j] = (hi - lo + BT - 1) / BT;
-    }
-    mine += n[j];
-  }
-  int end = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(end, d);
-    if (lane >= d) end += v;
-  }
-  const int first = end - mine;
-  const uint64_t hit = __ballot(tile >= first && tile < end);
-  if (hit == 0) return false;
-  const int owner = __builtin_ctzll(hit);
-  int e = 0, row = 0, rows = 0, t = tile - first;
-#pragma unroll
-  for (int j = 0; j < 8; j++) {
-    if (t >= 0 && t < n[j]) {
-      const int lo = min(max(off[j], 0), P), hi = min(max(off[j + 1], lo), P);
-      e = e0 + j;
-      row = lo + t * BT;
-      rows = min(hi - row, BT);
-    }
-    t -= n[j];
-  }
-  out->e = __builtin_amdgcn_readlane(e, owner);
-  out->row = __builtin_amdgcn_readlane(row, owner);
-  out->rows = __builtin_amdgcn_readlane(rows, owner);
-  return true;
-}
-
 // Row of x for what src_rows says (or the position, where there is none), or -1 for none.
 __device__ __forceinline__ int mx4_src_of(const Mx4ExpertArgs& A, int r) {
-  if (A.src_rows && r >= 0 && A.src_div > 1) r = (int)(__umulhi((uint32_t)r, A.src_magic) >> A.src_shift);
+  if (A.src_rows && r >= 0 && A.src_div > 1) r = div_by(r, A.src);
   return (unsigned)r < (unsigned)A.x_rows ? r : -1;
 }
 __device__ __forceinline__ int mx4_src(const Mx4ExpertArgs& A, int i) {
@@ -131,8 +76,8 @@ __global__ __launch_bounds__(256) void k_mx4_few(Mx4ExpertArgs A) {
   const int cols = (n_out + kCols - 1) / kCols;
   const int tile = blockIdx.x / cols, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int n0 = (blockIdx.x - tile * cols) * kCols + (Split ? 0 : wave * kFewCols);
-  MxTile t;
-  if (!mx4_find_tile<16>(A.offsets, A.E, A.P, tile, &t)) return;
+  RowTile t;
+  if (!find_row_tile<16>(A.offsets, A.E, A.P, tile, &t)) return;
   if (!Split && n0 >= n_out) return;
   const int r = lane & 15, q = lane >> 4;
   const int nb = A.k >> 5;  // blocks a row

@@ -431,6 +431,177 @@ moe_status moe_balance_loss_backward(const void *logits, int32_t logits_type, in
                                      float z_coef, const int32_t *counts, const int32_t *n_valid,
                                      const float *grad_loss, void *dlogits, void *stream);
 
+/*
+ * Routing from scores: the form of moe_route for routers whose logits are
+ * there already (a training program's, those that moe_balance_loss_forward
+ * takes), with softmax or sigmoid scores, a bias that takes part in the choice
+ * alone, and groups of experts.
+ */
+enum { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 };
+typedef struct {
+    int32_t n_experts;  /* E: 1..512 */
+    int32_t top_k;      /* k: 1..16, at most top_groups * E / n_groups */
+    int32_t scores;     /* MOE_SOFTMAX: s = softmax(logits) over all experts; MOE_SIGMOID: s_e = 1 / (1 + exp(-logit_e)) */
+    int32_t n_groups;   /* 1..64, divides E: expert e is in group e / (E / n_groups) */
+    int32_t top_groups; /* 1..n_groups: the groups a token may choose from; n_groups = no limit */
+    int32_t group_best; /* a group's rank is by the sum of its 1 or 2 largest choice scores */
+    int32_t renormalise;/* 1: weights are divided by their sum; 0: they are the scores */
+    float scale;        /* finite factor of the weights */
+} moe_select_desc;
+
+/*
+ * For each token: choice scores c_e = s_e + bias_e (bias NULL: the scores), the
+ * top_groups best groups, and in them the k largest c, ties of groups and of
+ * experts towards the lower index:
+ *   topk_ids      [T][k] int32, in order of decreasing c
+ *   topk_weights  [T][k] float: scale * s / (sum of the k chosen s), or scale * s
+ *   expert_counts, expert_offsets, sorted_assign  [E], [E+1], [T*k] int32, as
+ *                 moe_route writes them, for moe_mx4_experts; or all three NULL
+ * from
+ *   logits  [T][E] of logits_type (MOE_F32 or MOE_BF16), any alignment of it
+ *   bias    [E] float or NULL
+ *   valid   [T] uint8, 0 for a padding token, or NULL: all are valid
+ *   ws      moe_select_workspace_bytes(T, E, k) bytes, 16-byte aligned
+ * The choice is that of c in float64 (c, the groups' sums and the softmax's
+ * sum are float64 wherever float32 leaves it open); without a bias experts are
+ * compared by their logits.  Weights are float32.  An expert whose logit is
+ * -inf, or whose bias is -inf or NaN, is never chosen; a token with fewer than
+ * k others has id -1 and weight 0 in the remaining places, a padding token in
+ * all.  A NaN logit (with MOE_SOFTMAX a logit of +inf too) in a valid row
+ * leaves it without experts (ids -1) and makes its weights NaN.  An id of -1 is
+ * counted nowhere: expert_offsets[E] is then less than T * k and sorted_assign
+ * behind it stays as it was.  T * top_k < 2^31; T = 0 writes the counts and
+ * offsets alone.  Repeated calls give identical bits.  Two calls that overlap
+ * in time need two workspaces, also when replayed from graphs.
+ */
+moe_status moe_select_workspace_bytes(int32_t T, int32_t n_experts, int32_t top_k, size_t *bytes);
+moe_status moe_select_forward(const moe_select_desc *desc, const void *logits, int32_t logits_type, int32_t T,
+                              const float *bias, const uint8_t *valid, int32_t *topk_ids, float *topk_weights,
+                              int32_t *expert_counts, int32_t *expert_offsets, int32_t *sorted_assign,
+                              void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Gradient with respect to the logits for dweights [T][k] float, from what the
+ * forward call read and wrote (ids and the bias have none), with the dw of a
+ * place whose id is -1 left out:
+ *   dlogits = base + (d weights / d logits)^T dweights
+ *   base     [T][E] of logits_type or NULL (zeros): the gradient to add to, such
+ *            as moe_balance_loss_backward's
+ *   dlogits  [T][E] of logits_type; may be base, or logits where base is not
+ *            logits; overlaps them in no other way
+ * A padding token adds nothing; a row whose weights are NaN gets NaN.
+ */
+moe_status moe_select_backward(const moe_select_desc *desc, const void *logits, int32_t logits_type, int32_t T,
+                               const int32_t *topk_ids, const float *topk_weights, const float *dweights,
+                               const void *base, void *dlogits, void *stream);
+
+/*
+ * Counts, offsets and the stable order of ids that are there already (a
+ * router's, or the adapter of each token): n int32 ids, those outside
+ * 0..E-1 counted nowhere; outputs as moe_select_forward's, of [E], [E+1] and
+ * [n].  0 <= n < 2^31, 1 <= n_experts <= 512.  ws: moe_sort_workspace_bytes(n,
+ * E) bytes, 16-byte aligned, not shared by calls that overlap in time.
+ */
+moe_status moe_sort_workspace_bytes(int32_t n, int32_t n_experts, size_t *bytes);
+moe_status moe_sort_assignments(const int32_t *ids, int32_t n, int32_t n_experts, int32_t *expert_counts,
+                                int32_t *expert_offsets, int32_t *sorted_assign, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/*
+ * The sum over each token's routed rows, such as moe_mx4_experts leaves them
+ * with dst_rows = sorted_assign:
+ *   y[t] = base[t] + sum_j weights[t][j] * rows[t * k + j]
+ * over the j whose topk_ids[t][j] is not negative; a row with a negative id is
+ * left out whatever it holds.
+ *   rows     [T*k][width] of rows_type (MOE_F32 or MOE_BF16)
+ *   topk_ids [T][k] int32 or NULL: every row takes part
+ *   weights  [T][k] float or NULL: 1
+ *   base     [T][width] of y_type (MOE_F32 or MOE_BF16) or NULL: zeros
+ *   y        [T][width] of y_type; may be base
+ * 1 <= k <= 16, 1 <= width <= 2^24, T * k < 2^31, any alignment of the types;
+ * sums in float32 in the order base, j = 0, 1, ..., rounded once to y_type.
+ */
+moe_status moe_combine_forward(const void *rows, int32_t rows_type, int32_t T, int32_t k, int32_t width,
+                               const int32_t *topk_ids, const float *weights, const void *base, void *y,
+                               int32_t y_type, void *stream);
+
+/*
+ * Its gradients: drows[t * k + j] = weights[t][j] * dy[t] (of rows_type, may be
+ * rows) and dweights[t][j] = sum_c dy[t][c] rows[t * k + j][c] (float), zeros
+ * where the id is negative; either may be NULL, and rows where dweights is.
+ * base's gradient is dy.
+ */
+moe_status moe_combine_backward(const void *dy, int32_t y_type, const void *rows, int32_t rows_type, int32_t T,
+                                int32_t k, int32_t width, const int32_t *topk_ids, const float *weights,
+                                void *drows, float *dweights, void *stream);
+
+/*
+ * Low-rank adapters beside a projection: adapter a adds scale_a B_a A_a x to a
+ * row, with A_a [rank][n_in] and B_a [n_out][rank] in bf16.  Rows are given by
+ * positions as in moe_mx4_experts, so that adapters stand beside its product:
+ * one for each request (expert_offsets and both row arrays from
+ * moe_sort_assignments of every token's adapter, ids of tokens without one
+ * being -1), or one for each expert.
+ */
+typedef struct {
+    int32_t n_adapters; /* 1..512 */
+    int32_t rank;       /* 1..128; any larger rank of the store is padded by zeros of A and B */
+    int32_t n_in;       /* 1..65536 */
+    int32_t n_out;      /* 1..65536 */
+    int32_t y_type;     /* MOE_F32 or MOE_BF16: the type of y, base and dy */
+} moe_adapter_desc;
+
+/*
+ * y[dst(i)] = base[dst(i)] + scales[a] * B_a (A_a x[src(i)]) for the positions i
+ * in [offsets[a], offsets[a+1]).
+ *   a, b      [n_adapters][rank][n_in] and [n_adapters][n_out][rank] bf16
+ *   scales    [n_adapters] float or NULL: 1
+ *   x         [x_rows][n_in] bf16
+ *   offsets   [n_adapters+1] int32, as in moe_mx4_experts
+ *   rows      the positions' upper bound on the host, at most 2^24
+ *   src_rows, src_div, dst_rows  as in moe_mx4_experts
+ *   base      [y_rows][n_out] of y_type or NULL: zeros; may be y
+ *   y         [y_rows][n_out] of y_type; rows that no position maps to stay
+ *             as they were; dst_rows names each row at most once
+ *   h         [rows][rank] float or NULL: A_a x by position, for the backward call
+ * Any alignment of the types; n_in and n_out that are multiples of 8 with
+ * 16-byte aligned rows are faster.  A src(i) outside x counts as a row of
+ * zeros, a dst(i) outside y is not written.  y overlaps no input but base.
+ * Products are exact and their sums float32; A x enters the second product
+ * split into bf16 parts that hold 17 bits of it for a bf16 y and 24 for a
+ * float32 one; y is rounded once.  Repeated calls give identical bits.  No
+ * workspace.
+ */
+moe_status moe_adapters_forward(const moe_adapter_desc *desc, const uint16_t *a, const uint16_t *b, const float *scales,
+                                const uint16_t *x, int32_t x_rows, const int32_t *offsets, int32_t rows,
+                                const int32_t *src_rows, int32_t src_div, const int32_t *dst_rows, const void *base,
+                                void *y, int32_t y_rows, float *h, void *stream);
+
+/*
+ * The gradients for dy [y_rows][n_out] of y_type, with dh_i = scales[a] B_a^T
+ * dy[dst(i)]:
+ *   dx[r(i)] = base[r(i)] + A_a^T dh_i       bf16 [x_rows * src_div][n_in]
+ *   da_a = sum_i dh_i x[src(i)]^T            float [n_adapters][rank][n_in]
+ *   db_a = scales[a] sum_i dy[dst(i)] h_i^T  float [n_adapters][n_out][rank]
+ * r(i) = src_rows[i], before src_div divides it (i without src_rows): each of the
+ * src_div positions of a row of x has its own row of dx, which
+ * moe_combine_forward sums (ids and weights NULL).  Without src_rows, src_div is
+ * taken as 1.
+ *   h     as the forward call wrote it
+ *   base  of dx, bf16, or NULL: zeros; may be dx
+ *   dx    may be NULL, with base; rows of no position stay as they were
+ *   da, db  may be NULL both; written for every adapter, zeros for one without rows
+ *   ws    moe_adapters_workspace_bytes(desc, rows) bytes, 16-byte aligned, not
+ *         shared by calls that overlap in time
+ * dy and h with an index outside count as zeros.  Sums are float32.
+ */
+moe_status moe_adapters_workspace_bytes(const moe_adapter_desc *desc, int32_t rows, size_t *bytes);
+moe_status moe_adapters_backward(const moe_adapter_desc *desc, const uint16_t *a, const uint16_t *b, const float *scales,
+                                 const uint16_t *x, int32_t x_rows, const float *h, const void *dy, int32_t y_rows,
+                                 const int32_t *offsets, int32_t rows, const int32_t *src_rows, int32_t src_div,
+                                 const int32_t *dst_rows, const void *base, void *dx, float *da, float *db,
+                                 void *ws, size_t ws_bytes, void *stream);
+
 /* Default R* of the library with batch_invariant = 0 (host output); with
  * batch_invariant = 1 the default is 4. */
 int32_t moe_default_gemv_max_rows(void);
@@ -456,7 +627,10 @@ const char *moe_last_error(void);
  *   grouped-GEMM path, 8 = separate dequant pass (dequant_pass = 1), 9 and
  *   10 = the measurement probes, 11 = moe_mx4_quantize, 12 = moe_mx4_dequantize,
  *   13 = moe_mx4_experts, 14 = moe_balance_loss_forward,
- *   15 = moe_balance_loss_backward
+ *   15 = moe_balance_loss_backward, 16 = moe_select_forward,
+ *   17 = moe_select_backward, 18 = moe_sort_assignments,
+ *   19 = moe_combine_forward, 20 = moe_combine_backward,
+ *   21 = moe_adapters_forward, 22 = moe_adapters_backward
  */
 moe_status moe_profile_enable(int32_t mask);
 moe_status moe_profile_reset(void);
