@@ -188,6 +188,7 @@ struct SelectArgs {
   int T, E, k, groups, per, top_groups, best;  // per: experts a group
   bool f32, softmax, renorm;
   float scale;
+  int lanes, run;        // of 16 lanes a token: lanes a group, experts a lane
   int64_t per_part;      // tokens a part
   int32_t* part_count;   // [parts][E] or null
   // Backward pass.

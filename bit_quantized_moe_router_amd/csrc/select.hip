@@ -24,16 +24,10 @@ namespace moe {
 
 // ---- one token, exactly -------------------------------------------------------
 
-// What a wave needs in LDS for one token.
+// What a wave needs in LDS for one token: the choice scores.
 struct SelectLds {
   double c[kMaxE];
 };
-
-__device__ __forceinline__ double shfl_xor_f64(double v, int d) {
-  const uint64_t u = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = __shfl_xor((uint32_t)u, d), hi = __shfl_xor((uint32_t)(u >> 32), d);
-  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
 
 template <bool F32>
 __device__ __forceinline__ float logit_at(const void* logits, int64_t i) {
@@ -41,114 +35,129 @@ __device__ __forceinline__ float logit_at(const void* logits, int64_t i) {
   return bf16_bits_to_f32(static_cast<const uint16_t*>(logits)[i]);
 }
 
-// The groups that stay (bit g), from the choice scores in LDS: lane g sums its
-// group's group_best largest, then counts the groups before it.  -inf is an
-// expert that is not there; a group without one never stays.
+// LDS that this wave has written may be read by its other lanes.
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+__device__ __forceinline__ double lane_from_f64(double v, int from) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __shfl((uint32_t)u, from), hi = __shfl((uint32_t)(u >> 32), from);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// The groups that stay (bit g), from the choice scores in LDS: 64 / n_groups lanes a group find its group_best largest,
+// then every group counts those before it.  -inf is an expert that is not there; a group without one never stays.
 __device__ __forceinline__ uint64_t groups_kept(const SelectArgs& A, const double* c) {
-  const int lane = threadIdx.x & 63;
-  double sum = -INFINITY;
-  if (lane < A.groups) {
-    double first = -INFINITY, second = -INFINITY;
-    for (int i = 0; i < A.per; i++) {
-      const double v = c[lane * A.per + i];
+  const int lane = threadIdx.x & 63, per = 64 / A.groups;
+  const int group = lane / per, pos = lane - group * per;
+  double first = -INFINITY, second = -INFINITY;
+  if (group < A.groups)
+    for (int i = pos; i < A.per; i += per) {
+      const double v = c[group * A.per + i];
       second = fmax(second, fmin(first, v));
       first = fmax(first, v);
     }
-    sum = A.best == 2 && second > -INFINITY ? first + second : first;
+  double a = first, b = second;
+  for (int i = 1; i < per; i++) {
+    const int from = lane - pos + (pos + i < per ? pos + i : pos + i - per);
+    const double ga = lane_from_f64(first, from), gb = lane_from_f64(second, from);
+    b = fmax(fmax(b, gb), fmin(a, ga));
+    a = fmax(a, ga);
   }
+  const double sum = A.best == 2 && b > -INFINITY ? a + b : a;
   int before = 0;
   for (int g = 0; g < A.groups; g++) {
-    const double v = lane_value_f64(sum, g);
-    before += v > sum || (v == sum && g < lane) ? 1 : 0;
+    const double v = lane_value_f64(sum, g * per);
+    before += v > sum || (v == sum && g < group) ? 1 : 0;
   }
-  return __ballot(lane < A.groups && sum > -INFINITY && before < A.top_groups);
+  const uint64_t in = __ballot(pos == 0 && group < A.groups && sum > -INFINITY && before < A.top_groups);
+  uint64_t kept = 0;
+  for (uint64_t left = in; left; left &= left - 1) kept |= 1ull << (__builtin_ctzll(left) / per);
+  return kept;
 }
 
-// The choice for token t by one wave: lane j < k returns place j's expert (or -1) and its logit; *top and *total are
-// the row's largest logit and its sum of exp(l - top).  false: the row holds what no choice is made from (a NaN, with
-// softmax +inf).
+// The choice for token t by one wave, in float64: lane j < k returns place j's expert (or -1).  false: the row holds
+// what no choice is made from (a NaN, with softmax +inf).  Taken for rows whose choice float32 leaves open, about one
+// in a thousand of random ones.
 template <bool F32>
-__device__ __forceinline__ bool select_exact(const SelectArgs& A, int64_t t, SelectLds& lds, int* id, float* chosen,
-                                             float* top, float* total) {
+__device__ __forceinline__ bool select_exact(const SelectArgs& A, int64_t t, double* c, int* id) {
+  // The scores are kept in LDS and gone through by loops, so that this rare part asks for few registers.
   const int lane = threadIdx.x & 63;
-  float l[kMaxEPerLane];
-  double key[kMaxEPerLane];
-  bool bad = false;
   float mx = -INFINITY;
+  bool bad = false;
 #pragma unroll
   for (int j = 0; j < kMaxEPerLane; j++) {
     const int e = lane + 64 * j;
-    l[j] = e < A.E ? logit_at<F32>(A.logits, t * A.E + e) : -INFINITY;
-    bad = bad || l[j] != l[j] || (A.softmax && l[j] == INFINITY);
-    mx = fmaxf(mx, l[j]);
+    const float l = e < A.E ? logit_at<F32>(A.logits, t * A.E + e) : -INFINITY;
+    c[e] = (double)l;
+    bad = bad || l != l || (A.softmax && l == INFINITY);
+    mx = fmaxf(mx, l);
   }
   mx = wave_max_f32(mx);
-  *top = mx;
   *id = -1;
-  *chosen = -INFINITY;
   if (__ballot(bad)) return false;
-  const bool any = mx > -INFINITY;
+  if (!(mx > -INFINITY)) return true;
+  wave_lds();
   // Choice scores: l itself where that gives the same order.
   const bool scores = A.bias || (A.groups > 1 && A.best == 2);
-  double s[kMaxEPerLane], sum = 0.0;
-#pragma unroll
-  for (int j = 0; j < kMaxEPerLane; j++) {
-    s[j] = 0.0;
-    if (any && l[j] > -INFINITY) s[j] = A.softmax ? exp((double)l[j] - (double)mx) : scores ? 1.0 / (1.0 + exp(-(double)l[j])) : 0.0;
-    sum += s[j];
+  double sum = 0.0;
+  if (scores) {
+#pragma unroll 1
+    for (int e = lane; e < A.E; e += 64) {
+      const double l = c[e], v = exp(A.softmax ? l - (double)mx : -l);
+      const double s = l == -INFINITY ? 0.0 : A.softmax ? v : 1.0 / (1.0 + v);
+      sum += s;
+      c[e] = s;
+    }
+    if (A.softmax) sum = wave_sum_f64(sum);
+    wave_lds();
   }
-  sum = wave_sum_f64(sum);
-  *total = (float)sum;
-  bool out[kMaxEPerLane];
-#pragma unroll
-  for (int j = 0; j < kMaxEPerLane; j++) {
-    const int e = lane + 64 * j;
-    out[j] = !(l[j] > -INFINITY);
-    key[j] = scores ? (A.softmax ? s[j] / sum : s[j]) : (double)l[j];
-    if (A.bias && e < A.E) {
+  // With the bias; -inf for experts that are not there (a score of 0 may be one of them).
+#pragma unroll 1
+  for (int e = lane; e < A.E; e += 64) {
+    double v = c[e];
+    if (scores && A.softmax) v /= sum;
+    bool out = !(logit_at<F32>(A.logits, t * A.E + e) > -INFINITY);
+    if (A.bias) {
       const float b = A.bias[e];
-      out[j] = out[j] || !(b > -INFINITY);
-      key[j] += (double)b;
+      out = out || !(b > -INFINITY);
+      v += (double)b;
     }
-    if (out[j]) key[j] = -INFINITY;
+    c[e] = out ? -INFINITY : v;
   }
+  wave_lds();
   if (A.groups > 1) {
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int j = 0; j < kMaxEPerLane; j++)
-      if (lane + 64 * j < A.E) lds.c[lane + 64 * j] = key[j];
-    __threadfence_block();
-    __builtin_amdgcn_wave_barrier();
-    const uint64_t kept = groups_kept(A, lds.c);
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int j = 0; j < kMaxEPerLane; j++) {
-      const int e = lane + 64 * j;
-      out[j] = out[j] || e >= A.E || !((kept >> (min(e, A.E - 1) / A.per)) & 1);
+    const uint64_t kept = groups_kept(A, c);
+    wave_lds();
+#pragma unroll 1
+    for (int e = lane; e < A.E; e += 64) {
       // In the groups the order is that of l where there is no bias.
-      key[j] = out[j] ? -INFINITY : A.bias ? key[j] : (double)l[j];
+      if (!((kept >> (e / A.per)) & 1)) c[e] = -INFINITY;
+      else if (!A.bias && c[e] > -INFINITY) c[e] = (double)logit_at<F32>(A.logits, t * A.E + e);
     }
+    wave_lds();
   }
+#pragma unroll 1
   for (int i = 0; i < A.k; i++) {
     double best = -INFINITY;
-    int at = 0x7FFFFFFF;
+    int at = lane;
 #pragma unroll
-    for (int j = 0; j < kMaxEPerLane; j++)
-      if (!out[j] && (key[j] > best || at == 0x7FFFFFFF)) best = key[j], at = lane + 64 * j;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double v = shfl_xor_f64(best, d);
-      const int w = __shfl_xor(at, d);
-      // An absent candidate has the largest index and -inf.
-      if (v > best || (v == best && w < at)) best = v, at = w;
+    for (int j = 0; j < kMaxEPerLane; j++) {
+      const double v = c[lane + 64 * j];  // -inf behind the last expert
+      if (v > best) best = v, at = lane + 64 * j;
     }
-    if (at == 0x7FFFFFFF) break;
-    float mine = 0.f;
-#pragma unroll
-    for (int j = 0; j < kMaxEPerLane; j++)
-      if (lane + 64 * j == at) out[j] = true, mine = l[j];
-    mine = __shfl(mine, at & 63);
-    if (lane == i) *id = at, *chosen = mine;
+    const double top = wave_max_f64(best);
+    if (!(top > -INFINITY)) break;
+    // Of lanes with the same score the one with the lowest expert.
+    uint64_t who = __ballot(best == top);
+    int e = lane_value(at, __builtin_ctzll(who));
+    for (who &= who - 1; who; who &= who - 1) e = min(e, lane_value(at, __builtin_ctzll(who)));
+    if (lane == i) *id = e;
+    if (lane == (e & 63)) c[e] = -INFINITY;
+    wave_lds();
   }
   return true;
 }
@@ -180,17 +189,430 @@ __device__ __forceinline__ float select_weight(const SelectArgs& A, float l, flo
   return A.scale * (A.softmax ? u / total : u);
 }
 
+// ---- four tokens a wave ------------------------------------------------------------
+//
+// 16 lanes a token.  Each lane has a run of up to NB experts (of one group, where there are groups: 16 / n_groups
+// lanes each), turned into keys of 32 bits: 23 bits of a score, then 4 bits of the lane and 5 of the place in its run,
+// counted down.  One integer maximum then finds the best of the lanes and who it is, ties towards the lower index.  A
+// lane sorts its keys down to its eight largest; k times the largest head of the 16 lanes is taken and its lane moves
+// up.  Bound by the instructions: about 1400 for four tokens of 512 experts with k = 16, a third of them the scores (an
+// exponential and a reciprocal each, four times a plain instruction's time), a third the sort and the rounds.  65536
+// such tokens in 8 groups take 72 us (bf16, 67 MB read, 12 written); a wave a token, in float64, 1470.
+//
+// Logits that bf16 holds are compared by their 16 bits, exactly.  Other scores are in fixed point, from float32
+// functions: they order nearly every row as float64 would.  Neighbours among the chosen that are closer than the scores'
+// error are put in order by float64; a row goes to select_exact where that does not settle it, where the last chosen
+// and the next, or the last group that stays and the next, are that close, where a lane ran out of sorted keys, and
+// where a logit is NaN or +inf.
 constexpr int kSelThreads = 256, kSelWaves = kSelThreads / 64;
+constexpr int kSelPart = 16;  // tokens that a workgroup of kSelThreads takes at once
+constexpr int kSelRuns = 8;     // a lane's sorted keys
+constexpr int kSelMaxRun = 32;  // a lane's experts
 
+// What a score is: the logit itself (no bias, no sums), its softmax or its sigmoid.
+enum { kByLogit = 0, kBySoftmax = 1, kBySigmoid = 2, kByOne = 3 /* a wave a token */ };
+
+__device__ __forceinline__ uint32_t umax16(uint32_t v) {
+  v = max(v, (uint32_t)dpp_i32<0xB1>((int)v));
+  v = max(v, (uint32_t)dpp_i32<0x4E>((int)v));
+  v = max(v, (uint32_t)dpp_i32<0x141>((int)v));
+  return max(v, (uint32_t)dpp_i32<0x140>((int)v));
+}
+__device__ __forceinline__ float min16(float v) { return -max16(-v); }
+
+__device__ __forceinline__ void order2(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi, b = lo;
+}
+// Largest first (19 exchanges).
+__device__ __forceinline__ void sort8(uint32_t* v) {
+  order2(v[0], v[2]), order2(v[1], v[3]), order2(v[4], v[6]), order2(v[5], v[7]);
+  order2(v[0], v[4]), order2(v[1], v[5]), order2(v[2], v[6]), order2(v[3], v[7]);
+  order2(v[0], v[1]), order2(v[2], v[3]), order2(v[4], v[5]), order2(v[6], v[7]);
+  order2(v[2], v[4]), order2(v[3], v[5]);
+  order2(v[1], v[4]), order2(v[3], v[6]);
+  order2(v[1], v[2]), order2(v[3], v[4]), order2(v[5], v[6]);
+}
+// The eight largest of two sorted runs, sorted: one against the other reversed is a bitonic run of the larger halves.
+__device__ __forceinline__ void merge8(uint32_t* a, const uint32_t* b) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) a[i] = max(a[i], b[7 - i]);
+#pragma unroll
+  for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      if (!(i & d)) order2(a[i], a[i + d]);
+}
+// What the bias asks of all rows of a call.
+struct BiasRange {
+  bool any, exact;  // it is there and not the same for every expert; it holds +inf (every row by select_exact)
+  // Keys of the scores with it: score * scale + offset, off by `step` a unit of the scores' error and by `same` besides.
+  float scale, offset, far, step;
+};
+
+__device__ __forceinline__ BiasRange bias_range(const SelectArgs& A) {
+  BiasRange r{};
+  if (!A.bias) return r;
+  float low = INFINITY, high = -INFINITY;
+  bool odd = false, inf = false;
+  for (int e = threadIdx.x & 63; e < A.E; e += 64) {
+    const float b = A.bias[e];
+    if (b > -INFINITY && b < INFINITY) low = fminf(low, b), high = fmaxf(high, b);
+    else odd = true, inf = inf || b == INFINITY;
+  }
+  low = -wave_max_f32(-low);
+  high = wave_max_f32(high);
+  r.exact = __ballot(inf) != 0;
+  // The same finite bias everywhere changes no order.
+  r.any = __ballot(odd) != 0 || low != high;
+  if (!(low <= high)) low = high = 0.f;
+  // 512 at least and below 2^32.
+  r.scale = 4294000000.f / (1.f + (high - low));
+  r.offset = fmaf(-low, r.scale, 600.f);
+  r.far = fmaxf(fabsf(low), fabsf(high));
+  r.step = 2.f / 512 * r.scale;
+  return r;
+}
+
+// Lanes whose numbers are next to each other in the order of (v, larger first; id, smaller first) change places in
+// pairs (`odd`: lanes 1 and 2, 3 and 4, ...; else 0 and 1, ...), of the first k of 16.
+__device__ __forceinline__ void swap_pairs(double& v, int& id, int k, bool odd) {
+  const int g = threadIdx.x & 15;
+  const bool left = (g & 1) == (odd ? 1 : 0);
+  const int other = (threadIdx.x & 48) + ((left ? g + 1 : g - 1) & 15);
+  const double w = __shfl(v, other);
+  const int wid = __shfl(id, other);
+  const bool pair = left ? g + 1 < k : g >= 1 && g < k;
+  const bool before = v > w || (v == w && id < wid);  // this lane's comes first
+  if (pair && before != left) v = w, id = wid;
+}
+
+// A lane's part of a token.
+struct SelectLane {
+  int group, pos, lanes;  // its group, its place in it, lanes a group
+  int e0, n;              // its experts
+};
+
+__device__ __forceinline__ SelectLane select_lane(const SelectArgs& A) {
+  const int g = threadIdx.x & 15;
+  SelectLane L;
+  L.lanes = A.lanes;
+  L.group = g / A.lanes;
+  L.pos = g - L.group * A.lanes;
+  const int first = L.pos * A.run;
+  L.e0 = L.group * A.per + first;
+  L.n = L.group < A.groups ? max(0, min(A.run, A.per - first)) : 0;
+  return L;
+}
+
+// Eight of a lane's logits, from number p of its run; places past its run hold -inf, a row that is not there zeros.
 template <bool F32>
-__device__ __forceinline__ void select_token(const SelectArgs& A, int64_t t, SelectLds& lds, int* s_count) {
+__device__ __forceinline__ RowPiece<F32, 8> select_piece(const char* at, bool row, int n, int p) {
+  RowPiece<F32, 8> r;
+#pragma unroll
+  for (int i = 0; i < r.kWords; i++) r.w[i] = !row ? 0u : F32 ? 0xFF800000u : 0xFF80FF80u;
+  at += p * (F32 ? 4 : 2);
+  if (!row) return r;
+  if (n >= p + 8) {
+    r.load(at, 8);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      if (p + i >= n) continue;
+      if constexpr (F32) r.w[i] = reinterpret_cast<const uint32_t*>(at)[i];
+      else {
+        const uint32_t v = reinterpret_cast<const uint16_t*>(at)[i];
+        r.w[i / 2] = i & 1 ? (r.w[i / 2] & 0xFFFFu) | v << 16 : (r.w[i / 2] & 0xFFFF0000u) | v;
+      }
+    }
+  }
+  return r;
+}
+
+// v to an integer, cut off at 0 and 2^32; a NaN and -inf give 0.
+__device__ __forceinline__ uint32_t to_u32(float v) {
+  uint32_t u;
+  asm("v_cvt_u32_f32 %0, %1" : "=v"(u) : "v"(v));
+  return u;
+}
+
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+
+template <bool F32, int By, bool Biased>
+__device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0, int64_t t1, const SelectLane& L,
+                                                const BiasRange& B, const float4* s_bias, int* s_count) {
+  constexpr uint32_t kScore = 0xFFFFFE00u;  // a key's bits of the score
+  const int lane = threadIdx.x & 63, g = lane & 15;
+  const int64_t t = t0 + (lane >> 4);
+  const bool row = t < t1 && (!A.valid || A.valid[t]);
+  const char* at_row = static_cast<const char*>(A.logits) + (t * A.E + L.e0) * (F32 ? 4 : 2);
+  constexpr float kLog2 = 1.4426950408889634f;
+  // The lane's logits eight at a time, the next eight on their way.  A loop: unrolled, the code and its registers were
+  // several times as long and as many, and slower.
+  auto each = [&](auto f) {
+    RowPiece<F32, 8> cur = select_piece<F32>(at_row, row, L.n, 0);
+#pragma unroll 1
+    for (int p = 0; p < A.run; p += 8) {
+      RowPiece<F32, 8> next = cur;
+      if (p + 8 < A.run) next = select_piece<F32>(at_row, row, L.n, p + 8);
+      f(p, cur);
+      cur = next;
+    }
+  };
+  // What the row as a whole is asked for: its largest logit, the sum of exp(l - top), its smallest, whether bf16 holds
+  // all of its values, and whether one is +inf or a NaN.
+  float top = -INFINITY, low = INFINITY, total = 1.f;
+  uint32_t bits = 0;
+  bool bad = false;
+  const bool sums = By == kBySoftmax || (A.softmax && !A.renorm);
+  if (sums || (F32 && !Biased)) {
+    each([&](int, const RowPiece<F32, 8>& r) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        top = fmaxf(top, r.get(i));
+        if constexpr (F32 && !Biased) {
+          low = fminf(low, r.get(i) > -INFINITY ? r.get(i) : INFINITY);
+          bits |= __float_as_uint(r.get(i));
+        }
+      }
+    });
+    top = max16(top);
+  }
+  const float ref = top > -INFINITY ? top : 0.f;
+  if (sums) {
+    total = 0.f;
+    each([&](int, const RowPiece<F32, 8>& r) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) total += __builtin_amdgcn_exp2f((r.get(i) - ref) * kLog2);
+    });
+    total = sum16(total);
+  }
+  const float inv = By == kBySoftmax ? __builtin_amdgcn_rcpf(total) : 1.f;
+  // Errors of float32 scores, absolute.  Sigmoid: with t = l log2 e off by 2^-23.4 |t| and one step each of exp2, the sum and
+  // the reciprocal, s is off by s (1 - s) (|l| 2^-23.4 + 2^-23) + s 1.5 2^-23 < 2^-22.  Softmax: s (2 |l - top| +
+  // terms a lane + 24) 2^-24, of which the sum's terms, |l - top| < 7 on their average, have 18; s |l - top| < 0.4 / total
+  // and s <= 1 / total.  With a bias the sum's rounding.
+  float err = By == kBySigmoid ? 2.5e-7f : By == kBySoftmax ? (float)(A.run + 26) * 6e-8f / fmaxf(total, 1.f) : 0.f;
+  // Keys by the values' own bits (whole), or by v * scale + offset.
+  bool whole = !F32 && !Biased;
+  float offset = 0.f, scale = 0.f;
+  uint32_t gap = 0;
+  if constexpr (Biased) {
+    err += 6e-8f * (1.f + B.far);
+    scale = B.scale, offset = B.offset;
+    // Two keys in order may be out of order by this many steps of 512: each score's error, the roundings of offset (of
+    // |low| scale) and of the sum, and the cut.
+    gap = to_u32(fminf((err + 6e-8f * B.far) * B.step + 6.f, 8e6f));
+  } else if constexpr (F32) {
+    bits |= (uint32_t)dpp_i32<0xB1>((int)bits);
+    bits |= (uint32_t)dpp_i32<0x4E>((int)bits);
+    bits |= (uint32_t)dpp_i32<0x141>((int)bits);
+    bits |= (uint32_t)dpp_i32<0x140>((int)bits);
+    whole = __ballot((bits & 0xFFFFu) != 0) == 0;  // of all four rows
+    low = fmaxf(min16(low), ref - 64.f);
+    scale = 4294000000.f * __builtin_amdgcn_rcpf(fmaxf(ref - low, 1e-20f));
+    offset = 600.f;
+    gap = whole ? 0u : 8u;  // l - low, the product and the cut: two steps each, twice
+  }
+  // A key below this is no expert: -inf, or past the run.  (-inf's own bits are the first below the finite ones'.)
+  const uint32_t none = whole ? 0x00810000u : 512u;
+
+  // ---- keys, sorted; the largest two scores of the lane where groups are ranked ----
+  uint32_t key[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) key[i] = 0;
+  float a = -INFINITY, b = -INFINITY;
+  each([&](int p, const RowPiece<F32, 8>& r) {
+    // Rows without an infinity or a NaN need not look at each value.
+    bool odd;
+    if constexpr (F32) {
+      uint32_t far = 0;
+#pragma unroll
+      for (int i = 0; i < 8; i++) far = max(far, f32_abs_bits(r.get(i)));
+      bad = bad || far > 0x7F800000u;
+      odd = __ballot(far >= 0x7F800000u) != 0;
+    } else {
+      u16x2_t far = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 4; i++) far = __builtin_elementwise_max(far, __builtin_bit_cast(u16x2_t, r.w[i] & 0x7FFF7FFFu));
+      const uint32_t most = max(far.x, far.y);
+      bad = bad || most > 0x7F80u;
+      odd = __ballot(most >= 0x7F80u) != 0;
+    }
+    if (odd) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) bad = bad || r.get(i) == INFINITY;
+    }
+    float c[8];
+    if (By != kByLogit && (Biased || A.groups > 1)) {
+#pragma unroll
+      for (int i = 0; i < 8; i++)
+        c[i] = By == kBySoftmax ? __builtin_amdgcn_exp2f((r.get(i) - ref) * kLog2) * inv
+                                : __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(r.get(i) * -kLog2));
+      if constexpr (Biased) {
+        // -inf: excluded, or past the run.
+        const float4 b0 = s_bias[(p / 4) * 16 + g], b1 = s_bias[(p / 4 + 1) * 16 + g];
+        c[0] += b0.x, c[1] += b0.y, c[2] += b0.z, c[3] += b0.w;
+        c[4] += b1.x, c[5] += b1.y, c[6] += b1.z, c[7] += b1.w;
+      }
+      if (odd) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) c[i] = r.get(i) > -INFINITY ? c[i] : -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) c[i] = r.get(i);
+    }
+    if (A.groups > 1) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        b = __builtin_amdgcn_fmed3f(a, b, c[i]);
+        a = fmaxf(a, c[i]);
+      }
+    }
+    uint32_t k8[8];
+    if (!Biased && (!F32 || whole)) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        // Bits in the order of the values; + 0: no -0.
+        const uint32_t u = __float_as_uint(r.get(i) + 0.f);
+        k8[i] = ((u ^ ((uint32_t)((int)u >> 31) | 0x80000000u)) & 0xFFFF0000u) | (uint32_t)(31 - i);
+      }
+    } else if constexpr (Biased) {
+#pragma unroll
+      for (int i = 0; i < 8; i++) k8[i] = (to_u32(fmaf(c[i], scale, offset)) & kScore) | (uint32_t)(31 - i);
+    } else {
+      // Logits below `low` are held at it.
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float l = r.get(i);
+        k8[i] = ((l > -INFINITY ? to_u32(fmaf(fmaxf(l - low, 0.f), scale, offset)) : 0u) & kScore) | (uint32_t)(31 - i);
+      }
+    }
+    sort8(k8);
+    const uint32_t place = ((uint32_t)(15 - g) << 5) - (uint32_t)p;
+#pragma unroll
+    for (int i = 0; i < 8; i++) k8[i] += place;
+    merge8(key, k8);
+  });
+  bool open = bad || B.exact;  // left to select_exact
+  bool full = false, kept = true;
+  uint32_t mine = 0, last = 0;
+  // ---- groups ----
+  if (A.groups > 1) {
+    // The largest two of the group's lanes.
+    const int base = lane - L.pos;
+    float ta = a, tb = b;
+    for (int d = 1; d < L.lanes; d++) {
+      const int from = base + (L.pos + d < L.lanes ? L.pos + d : L.pos + d - L.lanes);
+      const float ga = __shfl(a, from), gb = __shfl(b, from);
+      tb = __builtin_amdgcn_fmed3f(ta, tb, ga);
+      ta = fmaxf(ta, ga);
+      tb = fmaxf(tb, gb);  // gb <= ga <= ta
+    }
+    const float score = L.group >= A.groups ? -INFINITY : By != kByLogit && A.best == 2 && tb > -INFINITY ? ta + tb : ta;
+    int before = 0;
+    for (int d = 1; d < A.groups; d++) {
+      const int other = L.group + d < A.groups ? L.group + d : L.group + d - A.groups;
+      const float v = __shfl(score, lane - g + other * L.lanes);
+      before += v > score || (v == score && other < L.group) ? 1 : 0;
+    }
+    kept = L.group < A.groups && score > -INFINITY && before < A.top_groups;
+    if constexpr (By != kByLogit) {
+      const float in = min16(kept ? score : INFINITY), out = max16(kept ? -INFINITY : score);
+      // Sums of two scores and their own rounding.
+      open = open || (out > -INFINITY && !(in - out > 4.f * err + 2.4e-7f * (fabsf(in) + 1.f)));
+    }
+  }
+  // ---- the k largest ----
+#pragma unroll
+  for (int j = 0; j < 8; j++) key[j] = kept && key[j] >= none ? key[j] : 0u;
+  full = A.run > kSelRuns && key[kSelRuns - 1] != 0;
+#pragma unroll 1
+  for (int i = 0; i < A.k; i++) {
+    last = umax16(key[0]);
+    const bool won = key[0] == last;
+#pragma unroll
+    for (int j = 0; j < kSelRuns - 1; j++) key[j] = won ? key[j + 1] : key[j];
+    key[kSelRuns - 1] = won ? 0u : key[kSelRuns - 1];
+    mine = g == i ? last : mine;
+  }
+  // A lane whose sorted keys are used up may have had another one before the last chosen.
+  open = open || (full && key[0] == 0);
+  const uint32_t next = umax16(key[0]);
+  const uint32_t after = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x101, 0xF, 0xF, true);  // lane g + 1's
+  const bool chosen = row && mine >= none;
+  const bool edge = row && last >= none && next >= none && (last >> 9) - (next >> 9) < gap;
+  const int from_e0 = __shfl(L.e0, (lane & 48) + 15 - (int)(mine >> 5 & 15u));
+  int id = chosen ? from_e0 + 31 - (int)(mine & 31u) : -1;
+  float lc = id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY;
+  const bool close = chosen && g + 1 < A.k && after >= none && (mine >> 9) - (after >> 9) < gap;
+  if (By == kBySoftmax && Biased) {
+    open = open || close || edge;  // the softmax's sum is float32
+  } else if (__ballot(close || edge)) {
+    // Those next to each other, and the last and the first that was not chosen, by what they are compared by.
+    const int next_e0 = __shfl(L.e0, (lane & 48) + 15 - (int)(next >> 5 & 15u));
+    int at = id >= 0 ? id : 0x7FFFFFFF, other = edge ? next_e0 + 31 - (int)(next & 31u) : -1;
+    double v = -INFINITY, w = -INFINITY;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; pass++) {
+      const int e = pass == 0 ? other : id;
+      w = v;
+      v = -INFINITY;
+      if (e >= 0) {
+        v = (double)logit_at<F32>(A.logits, t * A.E + e);
+        if (Biased) v = 1.0 / (1.0 + exp(-v)) + (double)A.bias[e];
+      }
+    }
+    // w: the other's.  One that is better takes the last one's place; what comes after it must not be near.
+    if (edge && g == A.k - 1 && (w > v || (w == v && other < at))) v = w, at = other;
+    const uint32_t head = key[0] == next ? key[1] : key[0], third = umax16(head);
+    open = open || (edge && ((third >= none && (last >> 9) - (third >> 9) < gap) || (full && head == 0)));
+    swap_pairs(v, at, A.k, false);
+    swap_pairs(v, at, A.k, true);
+    swap_pairs(v, at, A.k, false);
+    w = __shfl(v, (lane & 48) + ((g + 1) & 15));
+    const int wat = __shfl(at, (lane & 48) + ((g + 1) & 15));
+    open = open || (g + 1 < A.k && wat != 0x7FFFFFFF && !(v > w || (v == w && at < wat)));
+    const int now = at != 0x7FFFFFFF ? at : -1;
+    if (now != id) {
+      id = now;
+      lc = id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY;
+    }
+  }
+  // Bit 16 r + ..: row r is left open, and written by select_one.
+  const uint64_t todo = __ballot(row && open);
+  if (t < t1 && ((todo >> (lane & 48)) & 0xFFFFu) == 0) {
+    const float w = row ? select_weight(A, g < A.k ? lc : -INFINITY, top, total) : 0.f;
+    if (g < A.k) {
+      A.ids[t * A.k + g] = id;
+      A.weights[t * A.k + g] = w;
+      if (s_count && id >= 0) atomicAdd(&s_count[id], 1);
+    }
+  }
+  return todo;
+}
+
+// One token a wave: rows that the 16-lane form leaves open or has no lanes for (more than 16 groups, or groups too wide
+// for their lanes).
+template <bool F32>
+__device__ __forceinline__ void select_one(const SelectArgs& A, int64_t t, SelectLds& lds, int* s_count) {
   const int lane = threadIdx.x & 63;
   int id = -1;
   float w = 0.f;
   if (!A.valid || A.valid[t]) {
-    float l, top, total;
-    if (select_exact<F32>(A, t, lds, &id, &l, &top, &total)) w = select_weight(A, l, top, total);
-    else w = __builtin_nanf("");
+    float top = -INFINITY, total = 1.f;
+    const bool fine = select_exact<F32>(A, t, lds.c, &id);
+    if (A.softmax && !A.renorm) {
+      for (int e = lane; e < A.E; e += 64) top = fmaxf(top, logit_at<F32>(A.logits, t * A.E + e));
+      top = wave_max_f32(top);
+      total = 0.f;
+      if (top > -INFINITY)
+        for (int e = lane; e < A.E; e += 64) total += __expf(logit_at<F32>(A.logits, t * A.E + e) - top);
+      total = wave_sum_f32(total);
+    }
+    w = select_weight(A, id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY, top, total);
+    if (!fine) w = __builtin_nanf("");
   }
   if (lane < A.k) {
     A.ids[t * A.k + lane] = id;
@@ -199,24 +621,70 @@ __device__ __forceinline__ void select_token(const SelectArgs& A, int64_t t, Sel
   }
 }
 
-// Part b: tokens b * per_part .. ; its counts by expert go to the workspace.
-template <bool F32>
-__global__ __launch_bounds__(kSelThreads) void k_select(SelectArgs A) {
-  __shared__ SelectLds lds[kSelWaves];
-  __shared__ int s_count[kMaxE];
+// Tokens [t0, t1) by `waves` waves.
+template <bool F32, int By>
+__device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, int64_t t1, int waves, SelectLds* lds,
+                                             float* s_bias, int* s_count) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int e = threadIdx.x; e < A.E; e += kSelThreads) s_count[e] = 0;
+  if constexpr (By == kByOne) {
+    for (int64_t t = t0 + wave; t < t1; t += waves) select_one<F32>(A, t, lds[wave], s_count);
+  } else {
+    const BiasRange B = bias_range(A);
+    const SelectLane L = select_lane(A);
+    // The lanes' biases, four at a time: number j of lane g at (j / 4 * 16 + g) * 4 + j % 4.
+    if (By != kByLogit && B.any) {
+      for (int i = threadIdx.x; i < 16 * kSelMaxRun; i += 64 * waves) {
+        const int g = i / 4 % 16, j = i / 64 * 4 + i % 4;
+        const int group = g / A.lanes, at = (g - group * A.lanes) * A.run + j;
+        s_bias[i] = group < A.groups && j < A.run && at < A.per ? A.bias[group * A.per + at] : -INFINITY;
+      }
+    }
+    __syncthreads();
+    const float4* s_b = reinterpret_cast<const float4*>(s_bias);
+    auto go = [&](auto biased) {
+      // Rows that are left open wait for every 16th turn, so that their code's registers are not the loop's.
+      const int64_t step = 4 * waves;
+      int64_t t = t0 + 4 * wave;
+      while (t < t1) {
+        const int64_t from = t;
+        uint64_t open = 0;  // four bits a turn
+        for (int i = 0; i < 16 && t < t1; i++, t += step) {
+          const uint64_t todo = select_four<F32, By, biased.value>(A, t, t1, L, B, s_b, s_count);
+          if (todo) {
+#pragma unroll
+            for (int r = 0; r < 4; r++) open |= (uint64_t)(((todo >> (16 * r)) & 0xFFFFu) != 0) << (4 * i + r);
+          }
+        }
+        for (; open; open &= open - 1) {
+          const int b = __builtin_ctzll(open);
+          select_one<F32>(A, from + (b >> 2) * step + (b & 3), lds[wave], s_count);
+        }
+      }
+    };
+    if (By != kByLogit && B.any) go(std::integral_constant<bool, By != kByLogit>{});
+    else go(std::false_type{});
+  }
+}
+
+// Part b: tokens b * per_part .. ; its counts by expert go to the workspace.
+template <bool F32, int By, int NT>
+__global__ __launch_bounds__(NT) void k_select(SelectArgs A) {
+  __shared__ SelectLds lds[NT / 64];
+  __shared__ __attribute__((aligned(16))) float s_bias[kMaxE];
+  __shared__ int s_count[kMaxE];
+  for (int e = threadIdx.x; e < A.E; e += NT) s_count[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * A.per_part, t1 = min((int64_t)A.T, t0 + A.per_part);
-  for (int64_t t = t0 + wave; t < t1; t += kSelWaves) select_token<F32>(A, t, lds[wave], A.part_count ? s_count : nullptr);
+  select_range<F32, By>(A, t0, t1, NT / 64, lds, s_bias, A.part_count ? s_count : nullptr);
   if (!A.part_count) return;
   __syncthreads();
-  for (int e = threadIdx.x; e < A.E; e += kSelThreads) A.part_count[(int64_t)blockIdx.x * A.E + e] = s_count[e];
+  for (int e = threadIdx.x; e < A.E; e += NT) A.part_count[(int64_t)blockIdx.x * A.E + e] = s_count[e];
 }
 
 // ---- the order by expert ---------------------------------------------------------
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortThreads = 1024;
+constexpr int kSmallThreads = 512;  // where tokens are chosen for as well: two waves a SIMD, with the registers that takes
 
 // Exclusive prefix sum over the workgroup's first 512 threads (0 beyond E).
 __device__ __forceinline__ int sort_offsets(int v, int* s_wave) {
@@ -232,16 +700,16 @@ __device__ __forceinline__ int sort_offsets(int v, int* s_wave) {
 // Assignments [lo, hi) into the order, stably: a wave has a run of them, 64 at a
 // time; lanes with the same expert find each other by ballots.  first(e, n): the
 // place of the range's first assignment of expert e, of which it has n (called by
-// thread e < 512 of the whole workgroup, n = 0 for e >= E).
-template <class First>
+// thread e < 512 of the whole workgroup, n = 0 for e >= E).  NT threads.
+template <int NT, class First>
 __device__ __forceinline__ void sort_range(const int32_t* __restrict__ ids, int64_t lo, int64_t hi, int E,
                                            int32_t* __restrict__ sorted, int (*s_cnt)[kMaxE], First first) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int nbits = E > 1 ? 32 - __clz(E - 1) : 0;
   const uint64_t below = lane == 0 ? 0ull : ~0ull >> (64 - lane);
-  for (int i = tid; i < kSortWaves * kMaxE; i += kSortThreads) s_cnt[0][i] = 0;
+  for (int i = tid; i < (NT / 64) * kMaxE; i += NT) s_cnt[0][i] = 0;
   __syncthreads();
-  const int64_t run = ((hi - lo + kSortWaves - 1) / kSortWaves + 63) & ~(int64_t)63;
+  const int64_t run = ((hi - lo + (NT / 64) - 1) / (NT / 64) + 63) & ~(int64_t)63;
   const int64_t a0 = min(hi, lo + wave * run), a1 = min(hi, a0 + run);
   for (int64_t a = a0 + lane; a < a1; a += 64) {
     const int e = ids[a];
@@ -250,10 +718,10 @@ __device__ __forceinline__ void sort_range(const int32_t* __restrict__ ids, int6
   __syncthreads();
   int n = 0;
   if (tid < E)
-    for (int w = 0; w < kSortWaves; w++) n += s_cnt[w][tid];
+    for (int w = 0; w < (NT / 64); w++) n += s_cnt[w][tid];
   int at = first(tid, n);
   if (tid < E) {
-    for (int w = 0; w < kSortWaves; w++) {
+    for (int w = 0; w < (NT / 64); w++) {
       const int c = s_cnt[w][tid];
       s_cnt[w][tid] = at;
       at += c;
@@ -273,8 +741,9 @@ __device__ __forceinline__ void sort_range(const int32_t* __restrict__ ids, int6
   }
 }
 
+template <int NT>
 __device__ __forceinline__ void sort_all(const SortArgs& A, int (*s_cnt)[kMaxE], int* s_wave) {
-  sort_range(A.ids, 0, A.n, A.E, A.sorted, s_cnt, [&](int e, int n) {
+  sort_range<NT>(A.ids, 0, A.n, A.E, A.sorted, s_cnt, [&](int e, int n) {
     const int off = sort_offsets(n, s_wave);
     if (e < A.E) {
       A.counts[e] = n;
@@ -287,22 +756,22 @@ __device__ __forceinline__ void sort_all(const SortArgs& A, int (*s_cnt)[kMaxE],
 
 // Few assignments: one workgroup.
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs A) {
-  __shared__ int s_cnt[kSortWaves][kMaxE];
+  __shared__ int s_cnt[kSortThreads / 64][kMaxE];
   __shared__ int s_wave[kMaxE / 64];
-  sort_all(A, s_cnt, s_wave);
+  sort_all<kSortThreads>(A, s_cnt, s_wave);
 }
 
 // Few tokens: the choice and the order in one workgroup.
-template <bool F32>
-__global__ __launch_bounds__(kSortThreads) void k_select_small(SelectArgs A, SortArgs S) {
-  __shared__ SelectLds lds[kSortWaves];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  for (int64_t t = wave; t < A.T; t += kSortWaves) select_token<F32>(A, t, lds[wave], nullptr);
+template <bool F32, int By>
+__global__ __launch_bounds__(kSmallThreads) void k_select_small(SelectArgs A, SortArgs S) {
+  __shared__ SelectLds lds[kSmallThreads / 64];
+  __shared__ __attribute__((aligned(16))) float s_bias[kMaxE];
+  select_range<F32, By>(A, 0, A.T, kSmallThreads / 64, lds, s_bias, nullptr);
   __syncthreads();
   int(*s_cnt)[kMaxE] = reinterpret_cast<int(*)[kMaxE]>(lds);
-  static_assert(sizeof(lds) >= sizeof(int) * kSortWaves * kMaxE, "the counters take the scores' place");
+  static_assert(sizeof(lds) >= sizeof(int) * kSmallThreads / 64 * kMaxE, "the counters take the scores' place");
   __shared__ int s_wave[kMaxE / 64];
-  sort_all(S, s_cnt, s_wave);
+  sort_all<kSmallThreads>(S, s_cnt, s_wave);
 }
 
 // Counts of a part's assignments.
@@ -351,13 +820,13 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_scan(SortArgs A) {
 }
 
 __global__ __launch_bounds__(kSortThreads) void k_sort_place(SortArgs A) {
-  __shared__ int s_cnt[kSortWaves][kMaxE];
+  __shared__ int s_cnt[kSortThreads / 64][kMaxE];
   __shared__ int s_wave[kMaxE / 64];
   const int64_t lo = (int64_t)blockIdx.x * A.per_part, hi = min((int64_t)A.n, lo + A.per_part);
   const int e = threadIdx.x;
   const int total = e < A.E ? A.counts[e] : 0;
   const int before = e < A.E ? A.part_count[(int64_t)blockIdx.x * A.E + e] : 0;
-  sort_range(A.ids, lo, hi, A.E, A.sorted, s_cnt, [&](int, int) {
+  sort_range<kSortThreads>(A.ids, lo, hi, A.E, A.sorted, s_cnt, [&](int, int) {
     const int off = sort_offsets(total, s_wave);
     if (blockIdx.x == 0 && e < A.E) {
       A.offsets[e] = off;
@@ -475,7 +944,7 @@ int sort_parts(int64_t n) {
 
 int select_parts(int T) {
   if (T <= kSelectSmall) return 1;
-  const int parts = (T + 15) / 16;
+  const int parts = (T + kSelPart - 1) / kSelPart;
   return parts < kSortMaxParts ? parts : kSortMaxParts;
 }
 
@@ -496,18 +965,39 @@ hipError_t launch_sort(SortArgs S, hipStream_t s, const KTime& kt) {
   return launch_order(S, s, kt.stop);
 }
 
+// The kernel for these arguments.
+template <class F>
+static void by_select(const SelectArgs& A, F f) {
+  using std::integral_constant;
+  auto by = [&](auto f32) {
+    if (A.groups > 16 || A.run > kSelMaxRun) f(f32, integral_constant<int, kByOne>{});
+    else if (!A.bias && (A.groups == 1 || A.best == 1)) f(f32, integral_constant<int, kByLogit>{});
+    else if (A.softmax) f(f32, integral_constant<int, kBySoftmax>{});
+    else f(f32, integral_constant<int, kBySigmoid>{});
+  };
+  if (A.f32) by(std::true_type{});
+  else by(std::false_type{});
+}
+
 hipError_t launch_select_forward(SelectArgs A, SortArgs S, bool order, hipStream_t s, const KTime& kt) {
   const int parts = select_parts(A.T);
-  if (parts == 1 && order) {
-    auto* f = A.f32 ? k_select_small<true> : k_select_small<false>;
-    MOE_LAUNCH(f, dim3(1), dim3(kSortThreads), 0, s, kt.start, kt.stop, A, S);
-    return hipGetLastError();
-  }
+  A.lanes = A.groups > 16 ? 1 : 16 / A.groups;
+  A.run = (A.per + A.lanes - 1) / A.lanes;
   A.per_part = (A.T + (int64_t)parts - 1) / parts;
   A.part_count = order ? S.part_count : nullptr;
-  auto* f = A.f32 ? k_select<true> : k_select<false>;
-  MOE_LAUNCH(f, dim3(parts), dim3(kSelThreads), 0, s, kt.start, order ? nullptr : kt.stop, A);
-  if (!order) return hipGetLastError();
+  const bool small = parts == 1 && order;
+  by_select(A, [&](auto f32, auto by) {
+    constexpr bool F = f32.value;
+    constexpr int B = by.value;
+    if (small) {
+      MOE_LAUNCH((k_select_small<F, B>), dim3(1), dim3(kSmallThreads), 0, s, kt.start, kt.stop, A, S);
+    } else {
+      const bool wide = A.per_part > kSelPart;
+      auto* f = wide ? k_select<F, B, 1024> : k_select<F, B, kSelThreads>;
+      MOE_LAUNCH(f, dim3(parts), dim3(wide ? 1024 : kSelThreads), 0, s, kt.start, order ? nullptr : kt.stop, A);
+    }
+  });
+  if (small || !order) return hipGetLastError();
   S.parts = parts;
   S.per_part = A.per_part * A.k;
   return launch_order(S, s, kt.stop);
