@@ -75,7 +75,9 @@ __device__ __forceinline__ int adapter_dst(const AdapterArgs& A, int i) {
   return (unsigned)r < (unsigned)A.y_rows ? r : -1;
 }
 
-constexpr int kAdThreads = 256;
+// The weight gradients' thin operands, for 32 positions at a time (from a multiple of 32) and every rank (padded): three
+// parts of 32 numbers each, so that a lane reads the 8 positions of an operand at once.
+constexpr int kThinRank = 3 * 32;
 
 // Eight numbers of a row that has n of them left (Even: all or none), as the
 // parts that enter the matrix instructions.
@@ -93,23 +95,23 @@ __device__ __forceinline__ RowPiece<F32, 8> piece8(const void* row, int64_t at, 
 }
 
 // ---------------------------------------------------------------------------
-// RT x 16 positions of one adapter a workgroup; NR x 16 ranks (rank padded).
-// Shrink: the four waves split the summed columns, 32 at a time, and join
+// RT x 16 positions of one adapter a workgroup of W waves; NR x 16 ranks (rank padded).
+// Shrink: the waves split the summed columns, 32 at a time, and join
 // their sums in LDS in a fixed order; the result goes to LDS in bf16 parts.
 // Widen: the waves split the output columns, and so do `splits` workgroups of
 // the same positions, each of which shrinks for itself.
 // Even: n_in, n_out and rank are multiples of 8 (rank of NR in the backward
 // direction), so that a run of 8 is in its row or out of it.
 // ---------------------------------------------------------------------------
-template <bool Back, bool YF32, int RT, int NR, bool Even>
-__global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int splits) {
-  constexpr int BT = 16 * RT, R = 16 * NR;
+template <bool Back, bool YF32, int RT, int NR, int W, bool Even>
+__global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int splits) {
+  constexpr int BT = 16 * RT, R = 16 * NR, H = W / 2;
   constexpr int kParts = !Back && YF32 ? 3 : 2;         // of the numbers between, for the rows written
   constexpr bool kWideF32 = Back && YF32;               // the wide rows read are fp32
   constexpr int kInParts = kWideF32 ? 3 : 1;
   constexpr int kU = RT + NR <= 2 ? 8 : RT + NR <= 5 ? 4 : 2;  // steps of 32 columns in flight
   constexpr int kRow = R + 8;                           // numbers between two rows of a part in LDS
-  __shared__ float s_sum[4][BT][R + 1];
+  __shared__ float s_sum[H][BT][R + 1];
   __shared__ __attribute__((aligned(16))) uint16_t s_part[kParts][BT][kRow];
 
   RowTile t;
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
   f32x4_t acc[RT][NR] = {};
   const uint16_t* fa = A.a + (int64_t)t.e * r * K;
   const uint16_t* fb = A.b + (int64_t)t.e * N * r;
-  for (int k0 = wave * 32 * kU; k0 < wide; k0 += 4 * 32 * kU) {
+  for (int k0 = wave * 32 * kU; k0 < wide; k0 += W * 32 * kU) {
     RowPiece<kWideF32, 8> x[kU][RT];
     RowPiece<false, 8> w[kU][Back ? 1 : NR];
     uint32_t turn[kU][Back ? 8 : 1][(NR + 1) / 2];
@@ -209,28 +211,61 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
       }
     }
   }
-  // Result: position m, rank 16 f + 4 q + j (backward: NR (4 q + j) + f).
+  // Result: position m, rank 16 f + 4 q + j (backward: NR (4 q + j) + f).  The upper half of the waves hands its sums to
+  // the lower one, whose places are summed in order.
+  auto at = [&](int i, int f, int j) -> float& {
+    return s_sum[wave % H][i * 16 + m][Back ? NR * (4 * q + j) + f : 16 * f + 4 * q + j];
+  };
+  if (wave >= H) {
 #pragma unroll
-  for (int i = 0; i < RT; i++)
+    for (int i = 0; i < RT; i++)
 #pragma unroll
-    for (int f = 0; f < NR; f++)
+      for (int f = 0; f < NR; f++)
 #pragma unroll
-      for (int j = 0; j < 4; j++) s_sum[wave][i * 16 + m][Back ? NR * (4 * q + j) + f : 16 * f + 4 * q + j] = acc[i][f][j];
+        for (int j = 0; j < 4; j++) at(i, f, j) = acc[i][f][j];
+  }
+  __syncthreads();
+  if (wave < H) {
+#pragma unroll
+    for (int i = 0; i < RT; i++)
+#pragma unroll
+      for (int f = 0; f < NR; f++)
+#pragma unroll
+        for (int j = 0; j < 4; j++) at(i, f, j) += acc[i][f][j];
+  }
   __syncthreads();
   const float scale = A.scales ? A.scales[t.e] : 1.f;
-  for (int j = threadIdx.x; j < BT * R; j += kAdThreads) {
+  for (int j = threadIdx.x; j < BT * R; j += 64 * W) {
     const int p = j / R, c = j % R;
-    float v = (s_sum[0][p][c] + s_sum[1][p][c]) + (s_sum[2][p][c] + s_sum[3][p][c]);
+    float v = s_sum[0][p][c];
+#pragma unroll
+    for (int w = 1; w < H; w++) v += s_sum[w][p][c];
     if (c >= r) v = 0.f;
     const float sv = scale * v;
-    // h is kept without the scale, dh with it.
-    if (A.h_out && split == 0 && p < t.rows && c < r) A.h_out[(int64_t)(t.row + p) * r + c] = Back ? sv : v;
+    if (!Back && A.h_out && split == 0 && p < t.rows && c < r) A.h_out[(int64_t)(t.row + p) * r + c] = v;  // without the scale
     uint32_t part[kParts];
     split_parts<kParts>(sv, part);
 #pragma unroll
     for (int s = 0; s < kParts; s++) s_part[s][p][c] = (uint16_t)part[s];
+    if constexpr (Back) s_sum[0][p][c] = sv;
   }
   __syncthreads();
+  if (Back && A.thin && split == 0) {
+    // dh and h in the layout of k_adapters_sums' operands.
+    for (int j = threadIdx.x; j < BT * R; j += 64 * W) {
+      const int p = j % BT, c = j / BT;
+      if (p >= t.rows) continue;
+      const int64_t pos = t.row + p;
+      uint16_t* to = A.thin + ((pos >> 5) * R + c) * kThinRank + (pos & 31);
+      uint32_t part[3];
+      split_parts<3>(s_sum[0][p][c], part);
+#pragma unroll
+      for (int s = 0; s < 3; s++) to[32 * s] = (uint16_t)part[s];
+      split_parts<3>(c < r ? A.h[pos * r + c] : 0.f, part);
+#pragma unroll
+      for (int s = 0; s < 3; s++) to[A.thin_h + 32 * s] = (uint16_t)part[s];
+    }
+  }
 
   // ---- widen ----
   // The operands of the numbers between: with one chunk of 32 ranks or more, a part an instruction; with 16 ranks
@@ -243,11 +278,23 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
     return __builtin_bit_cast(bf16x8_t, v);
   };
   if constexpr (!Back) {
-    // Four fragments of 16 columns: row 4 a + b of fragment g is column 16 a + 4 g + b, so that a lane has 16
-    // columns in a row of its position.
+    // Four fragments of 16 columns: row 4 a + b of fragment f is column 32 (f / 2) + 8 a + 4 (f % 2) + b, so that a lane
+    // has runs of 8 columns of its position and four lanes 64 bytes.
     const int groups = (N + 63) >> 6;
-    for (int g = split * 4 + wave; g < groups; g += 4 * splits) {
+    for (int g = split * W + wave; g < groups; g += W * splits) {
       const int n0 = g * 64;
+      RowPiece<YF32, 8> base[RT][2];
+      if (A.base) {
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            const int c = n0 + 32 * u + 8 * q;
+            base[i][u].clear();
+            if (dst[i] >= 0 && c < N)
+              base[i][u].load(static_cast<const char*>(A.base) + ((int64_t)dst[i] * N + c) * (YF32 ? 4 : 2), Even ? 8 : N - c);
+          }
+      }
       f32x4_t o[RT][4] = {};
 #pragma unroll
       for (int ch = 0; ch < kChunks; ch++) {
@@ -255,7 +302,7 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
         bf16x8_t w[4];
 #pragma unroll
         for (int f = 0; f < 4; f++) {
-          const int n = min(n0 + 16 * (m >> 2) + 4 * f + (m & 3), N - 1);
+          const int n = min(n0 + 32 * (f >> 1) + 8 * (m >> 2) + 4 * (f & 1) + (m & 3), N - 1);
           const auto v = piece8<false, Even>(fb, (int64_t)n * r + c, r - c);
           w[f] = as_bf16x8(v.w[0], v.w[1], v.w[2], v.w[3]);
         }
@@ -273,18 +320,16 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
         if (dst[i] < 0) continue;
 #pragma unroll
         for (int u = 0; u < 2; u++) {
-          const int c = n0 + 16 * q + 8 * u, n = N - c;
+          const int c = n0 + 32 * u + 8 * q, n = N - c;
           if (n <= 0) continue;
           const int64_t at = ((int64_t)dst[i] * N + c) * (YF32 ? 4 : 2);
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) v[j] = o[i][2 * u + j / 4][j % 4];
-          RowPiece<YF32, 8> p;
-          if (A.base) {
-            p.load(static_cast<const char*>(A.base) + at, Even ? 8 : n);
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += p.get(j);
+          for (int j = 0; j < 8; j++) {
+            v[j] = o[i][2 * u + j / 4][j % 4];
+            if (A.base) v[j] += base[i][u].get(j);
           }
+          RowPiece<YF32, 8> p;
           p.set(v);
           p.store(static_cast<char*>(A.y) + at, Even ? 8 : n);
         }
@@ -292,11 +337,24 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
     }
   } else {
     if (!A.dx) return;
-    // Eight fragments from rows of 8 columns turned around: row a of fragment f is column 8 a + f, so that a lane has 32
-    // columns in a row.
+    // Eight fragments from rows of 8 columns turned around: row 4 a + b of fragment f is column 32 b + 8 a + f, so that a
+    // lane has runs of 8 columns of its position and four lanes 64 bytes.
+    const int run = 8 * (4 * (m & 3) + (m >> 2));
     const int groups = (K + 127) >> 7;
-    for (int g = split * 4 + wave; g < groups; g += 4 * splits) {
+    for (int g = split * W + wave; g < groups; g += W * splits) {
       const int n0 = g * 128;
+      RowPiece<false, 8> base[RT][4];
+      if (A.base) {
+#pragma unroll
+        for (int i = 0; i < RT; i++)
+#pragma unroll
+          for (int u = 0; u < 4; u++) {
+            const int c = n0 + 32 * u + 8 * q;
+            base[i][u].clear();
+            if (raw[i] >= 0 && c < K)
+              base[i][u].load(static_cast<const char*>(A.base) + ((int64_t)raw[i] * K + c) * 2, Even ? 8 : K - c);
+          }
+      }
       f32x4_t o[RT][8] = {};
 #pragma unroll
       for (int ch = 0; ch < kChunks; ch++) {
@@ -304,7 +362,7 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
 #pragma unroll
         for (int j = 0; j < 8; j++) {
           const int c = min((NR == 1 ? 8 * (q & 1) : 32 * ch + 8 * q) + j, r - 1);
-          const auto v = piece8<false, Even>(fa, (int64_t)c * K + n0 + 8 * m, K - n0 - 8 * m);
+          const auto v = piece8<false, Even>(fa, (int64_t)c * K + n0 + run, K - n0 - run);
 #pragma unroll
           for (int i = 0; i < 4; i++) rows[j][i] = v.w[i];
         }
@@ -327,18 +385,16 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
         if (raw[i] < 0) continue;
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-          const int c = n0 + 32 * q + 8 * u, n = K - c;
+          const int c = n0 + 32 * u + 8 * q, n = K - c;
           if (n <= 0) continue;
           const int64_t at = ((int64_t)raw[i] * K + c) * 2;
           float v[8];
 #pragma unroll
-          for (int j = 0; j < 8; j++) v[j] = o[i][j][u];
-          RowPiece<false, 8> p;
-          if (A.base) {
-            p.load(static_cast<const char*>(A.base) + at, Even ? 8 : n);
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] += p.get(j);
+          for (int j = 0; j < 8; j++) {
+            v[j] = o[i][j][u];
+            if (A.base) v[j] += base[i][u].get(j);
           }
+          RowPiece<false, 8> p;
           p.set(v);
           p.store(static_cast<char*>(A.dx) + at, Even ? 8 : n);
         }
@@ -350,16 +406,16 @@ __global__ __launch_bounds__(kAdThreads) void k_adapters_rows(AdapterArgs A, int
 // Sixteenths of the rank, rounded up to what the kernels are made for.
 inline int adapter_frags(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : 8; }
 
-template <bool Back, bool YF32, int RT, int NR, bool Even>
+template <bool Back, bool YF32, int RT, int NR, int W, bool Even>
 hipError_t adapters_rows(const AdapterArgs& A, int cus, hipStream_t s, hipEvent_t ev0, hipEvent_t ev1) {
   constexpr int BT = 16 * RT;
   const int64_t tiles = ((int64_t)A.P + BT - 1) / BT + (A.n < A.P ? A.n : A.P);
   const int groups = Back ? (A.dx ? (A.K + 127) / 128 : 1) : (A.N + 63) / 64;
-  int64_t splits = 2 * cus / tiles;
-  if (splits > (groups + 3) / 4) splits = (groups + 3) / 4;
+  int64_t splits = cus / tiles;
+  if (splits > (groups + W - 1) / W) splits = (groups + W - 1) / W;
   if (splits < 1) splits = 1;
-  MOE_LAUNCH((k_adapters_rows<Back, YF32, RT, NR, Even>), dim3((unsigned)(tiles * splits)), dim3(kAdThreads), 0, s, ev0,
-             ev1, A, (int)splits);
+  MOE_LAUNCH((k_adapters_rows<Back, YF32, RT, NR, W, Even>), dim3((unsigned)(tiles * splits)), dim3(64 * W), 0, s, ev0, ev1, A,
+             (int)splits);
   return hipGetLastError();
 }
 
@@ -367,19 +423,24 @@ template <bool Back, bool YF32>
 hipError_t adapters_rows_any(const AdapterArgs& A, int cus, hipStream_t s, hipEvent_t ev0, hipEvent_t ev1) {
   const int nr = adapter_frags(A.r);
   const bool even = A.K % 8 == 0 && A.N % 8 == 0 && A.r % 8 == 0;
-  const bool many = even && A.P >= 64 * cus;
-  auto* f = !even ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, false>
-                     : nr == 2 ? adapters_rows<Back, YF32, 1, 2, false>
-                     : nr == 4 ? adapters_rows<Back, YF32, 1, 4, false>
-                               : adapters_rows<Back, YF32, 1, 8, false>)
-            : many  ? (nr == 1   ? adapters_rows<Back, YF32, 4, 1, true>
-                       : nr == 2 ? adapters_rows<Back, YF32, 4, 2, true>
-                       : nr == 4 ? adapters_rows<Back, YF32, 2, 4, true>
-                                 : adapters_rows<Back, YF32, 1, 8, true>)
-                    : (nr == 1   ? adapters_rows<Back, YF32, 1, 1, true>
-                       : nr == 2 ? adapters_rows<Back, YF32, 1, 2, true>
-                       : nr == 4 ? adapters_rows<Back, YF32, 1, 4, true>
-                                 : adapters_rows<Back, YF32, 1, 8, true>);
+  const int64_t tiles = ((int64_t)A.P + 15) / 16;  // with the last ones of adapters, a few more
+  const bool some = 4 * tiles > 3 * cus, many = even && tiles >= 4 * cus;
+  auto* f = !even ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, false>
+                     : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 8, false>
+                     : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, false>
+                               : adapters_rows<Back, YF32, 1, 8, 8, false>)
+            : many  ? (nr == 1   ? adapters_rows<Back, YF32, 2, 1, 8, true>
+                       : nr == 2 ? adapters_rows<Back, YF32, 2, 2, 8, true>
+                       : nr == 4 ? adapters_rows<Back, YF32, 2, 4, 8, true>
+                                 : adapters_rows<Back, YF32, 1, 8, 8, true>)
+            : some  ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, true>
+                       : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 8, true>
+                       : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, true>
+                                 : adapters_rows<Back, YF32, 1, 8, 8, true>)
+                    : (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 16, true>
+                       : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 16, true>
+                       : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, true>
+                                 : adapters_rows<Back, YF32, 1, 8, 8, true>);
   return f(A, cus, s, ev0, ev1);
 }
 

@@ -1235,7 +1235,7 @@ moe_status moe_adapters_forward(const moe_adapter_desc* d, const uint16_t* a, co
 moe_status moe_adapters_workspace_bytes(const moe_adapter_desc* d, int32_t rows, size_t* bytes) {
   TRY(adapter_shape(d, rows));
   if (!bytes) return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
-  *bytes = al((size_t)rows * d->rank * 4);
+  *bytes = adapters_thin_bytes(d->rank, rows);
   return MOE_OK;
 }
 
@@ -1274,7 +1274,8 @@ moe_status moe_adapters_backward(const moe_adapter_desc* d, const uint16_t* a, c
   A.dx = dx;
   A.da = da;
   A.db = db;
-  A.dh = A.h_out = da ? static_cast<float*>(ws) : nullptr;
+  A.thin = da ? static_cast<uint16_t*>(ws) : nullptr;
+  A.thin_h = adapters_thin_bytes(d->rank, rows) / 4;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int cus = device_cus();
   return timed(22, s, "adapters gradient", [&](const KTime& kt) {

@@ -5,8 +5,8 @@
 // Bound by the bytes of the rows, in small calls by the way ids -> rows -> sum.
 // Forward: threads split the columns, each sums its columns over j in order,
 // with all of a token's rows in flight.  Backward: one pass over the rows
-// gives both gradients, a token a wave (or four, where there are few tokens),
-// whose lanes hold the k dot products until the end.
+// gives both gradients; the lanes of a token hold its k dot products until the
+// end.
 #include <type_traits>
 
 #include "launch.h"
@@ -22,8 +22,9 @@ constexpr int kCombCols = RF32 ? 4 : 8;
 
 // tpr threads a row (a power of two up to 256).  Whole: a wave has one row, so
 // that ids and weights are read by the scalar unit and a left-out row is
-// skipped by a branch of the whole wave.
-template <bool RF32, bool YF32, bool Whole>
+// skipped by a branch of the whole wave.  Even: the width is a multiple of a
+// thread's columns, and there is no shorter last piece.
+template <bool RF32, bool YF32, bool Whole, bool Even>
 __global__ __launch_bounds__(kCombThreads) void k_combine_rows(CombineArgs A, int tpr_log2) {
   constexpr int V = kCombCols<RF32>, kR = RF32 ? 4 : 2, kY = YF32 ? 4 : 2;
   const int tpr = 1 << tpr_log2, per = kCombThreads >> tpr_log2;
@@ -36,7 +37,7 @@ __global__ __launch_bounds__(kCombThreads) void k_combine_rows(CombineArgs A, in
     const int64_t t = t0 + sub;
     if (t >= A.T) break;
     for (int64_t c = (int64_t)part * V; c < H; c += (int64_t)tpr * V) {
-      const int n = (int)min((int64_t)V, H - c);
+      const int n = Even ? V : (int)min((int64_t)V, H - c);
       float acc[V] = {};
       if (A.base) {
         RowPiece<YF32, V> b;
@@ -79,16 +80,21 @@ __device__ __forceinline__ float comb_wave_sum(float v) {
   return v;
 }
 
-// A token by `Waves` waves of a workgroup of four; KB: k rounded up.
-template <bool RF32, bool YF32, int KB, int Waves>
-__global__ __launch_bounds__(kCombThreads) void k_combine_grad(CombineArgs A) {
+// A token by `Waves` waves of a workgroup of four, or, where a row has fewer
+// pieces than a wave has lanes, by 2^lanes_log2 lanes (Waves = 0); KB: k rounded up.
+template <bool RF32, bool YF32, int KB, int Waves, bool Even>
+__global__ __launch_bounds__(kCombThreads) void k_combine_grad(CombineArgs A, int lanes_log2) {
   constexpr int V = kCombCols<RF32>, kR = RF32 ? 4 : 2, kY = YF32 ? 4 : 2;
-  constexpr int kTokens = 4 / Waves, kCols = Waves * 64 * V;
   __shared__ float s_dot[Waves > 1 ? Waves : 1][KB];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int64_t H = A.H, step = (int64_t)gridDim.x * kTokens;
+  // Lanes a token within a wave, this one's number among all of the token's, and tokens a workgroup.
+  const int lanes = Waves == 0 ? 1 << lanes_log2 : 64, part = Waves == 0 ? lane & (lanes - 1) : Waves == 1 ? lane : threadIdx.x;
+  const int tokens = Waves == 0 ? kCombThreads >> lanes_log2 : 4 / Waves;
+  const int sub = Waves == 0 ? (int)(threadIdx.x >> lanes_log2) : Waves == 1 ? wave : 0;
+  const int64_t H = A.H, step = (int64_t)gridDim.x * tokens;
+  const int cols = (Waves > 1 ? kCombThreads : lanes) * V;
   // With Waves = 4 the loop's condition is the workgroup's, so that all of it meets at the barriers.
-  for (int64_t t = (int64_t)blockIdx.x * kTokens + (Waves == 1 ? wave : 0); t < A.T; t += step) {
+  for (int64_t t = (int64_t)blockIdx.x * tokens + sub; t < A.T; t += step) {
     float w[KB], dot[KB] = {};
     bool on[KB];
 #pragma unroll
@@ -97,8 +103,8 @@ __global__ __launch_bounds__(kCombThreads) void k_combine_grad(CombineArgs A) {
       on[j] = j < A.k && (!A.ids || A.ids[a] >= 0);
       w[j] = !on[j] ? 0.f : A.weights ? A.weights[a] : 1.f;
     }
-    for (int64_t c = ((Waves == 1 ? 0 : wave * 64) + lane) * V; c < H; c += kCols) {
-      const int n = (int)min((int64_t)V, H - c);
+    for (int64_t c = part * V; c < H; c += cols) {
+      const int n = Even ? V : (int)min((int64_t)V, H - c);
       RowPiece<YF32, V> d;
       d.load(static_cast<const char*>(A.dy) + (t * H + c) * kY, n);
       RowPiece<RF32, V> r[KB];
@@ -128,6 +134,16 @@ __global__ __launch_bounds__(kCombThreads) void k_combine_grad(CombineArgs A) {
       }
     }
     if (!A.dweights) continue;
+    if constexpr (Waves == 0) {
+      for (int d = 1; d < lanes; d <<= 1) {
+#pragma unroll
+        for (int j = 0; j < KB; j++) dot[j] += __shfl_xor(dot[j], d);
+      }
+#pragma unroll
+      for (int j = 0; j < KB; j++)
+        if (j < A.k && part == (j & (lanes - 1))) A.dweights[t * A.k + j] = dot[j];
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < KB; j++) dot[j] = comb_wave_sum(dot[j]);
     if constexpr (Waves == 1) {
@@ -164,7 +180,8 @@ hipError_t launch_combine_forward(const CombineArgs& A, hipStream_t s, const KTi
   const dim3 grid((unsigned)(groups < kCombGrid ? groups : kCombGrid));
   auto go = [&](auto rf, auto yf) {
     constexpr bool RF = rf.value, YF = yf.value;
-    auto* f = log2 >= 6 ? k_combine_rows<RF, YF, true> : k_combine_rows<RF, YF, false>;
+    auto* f = A.H % V ? (log2 >= 6 ? k_combine_rows<RF, YF, true, false> : k_combine_rows<RF, YF, false, false>)
+                      : (log2 >= 6 ? k_combine_rows<RF, YF, true, true> : k_combine_rows<RF, YF, false, true>);
     MOE_LAUNCH(f, grid, dim3(kCombThreads), 0, s, kt.start, kt.stop, A, log2);
   };
   using std::false_type;
@@ -176,13 +193,23 @@ hipError_t launch_combine_forward(const CombineArgs& A, hipStream_t s, const KTi
 
 template <bool RF, bool YF>
 static void launch_grad(const CombineArgs& A, hipStream_t s, const KTime& kt) {
-  const bool four = A.T < 1024 && A.H > 64 * kCombCols<RF>;
-  const int64_t groups = four ? A.T : (A.T + 3) / 4;
+  // Four waves a token where few tokens would leave the device idle (1 token of 10 rows of 4222 bf16 values: 20 us against
+  // 24); part of a wave where a row is narrow (15920 tokens of 6 rows of 61: 12 us against 43).
+  const int64_t pieces = (A.H + kCombCols<RF> - 1) / kCombCols<RF>;
+  int log2 = 0;
+  while (log2 < 6 && (1 << log2) < pieces) log2++;
+  const int waves = log2 < 6 ? 0 : A.T < 1024 && pieces > 64 ? 4 : 1;
+  const int64_t tokens = waves == 0 ? kCombThreads >> log2 : waves == 1 ? 4 : 1, groups = (A.T + tokens - 1) / tokens;
   const dim3 grid((unsigned)(groups < kCombGrid ? groups : kCombGrid));
   auto go = [&](auto kb) {
     constexpr int KB = kb.value;
-    auto* f = four ? k_combine_grad<RF, YF, KB, 4> : k_combine_grad<RF, YF, KB, 1>;
-    MOE_LAUNCH(f, grid, dim3(kCombThreads), 0, s, kt.start, kt.stop, A);
+    auto* f = A.H % kCombCols<RF> ? (waves == 0   ? k_combine_grad<RF, YF, KB, 0, false>
+                                     : waves == 1 ? k_combine_grad<RF, YF, KB, 1, false>
+                                                  : k_combine_grad<RF, YF, KB, 4, false>)
+                                  : (waves == 0   ? k_combine_grad<RF, YF, KB, 0, true>
+                                     : waves == 1 ? k_combine_grad<RF, YF, KB, 1, true>
+                                                  : k_combine_grad<RF, YF, KB, 4, true>);
+    MOE_LAUNCH(f, grid, dim3(kCombThreads), 0, s, kt.start, kt.stop, A, log2);
   };
   if (A.k <= 4) go(std::integral_constant<int, 4>{});
   else if (A.k <= 8) go(std::integral_constant<int, 8>{});

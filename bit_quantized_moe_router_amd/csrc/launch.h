@@ -243,18 +243,20 @@ struct AdapterArgs {
   const int32_t* dst_rows;  // [P] or null
   const void* base;         // forward [y_rows][N] of y's type, backward [..][K] bf16; or null
   void* y;                  // [y_rows][N] fp32 or bf16
-  float* h_out;             // [P][r]: h of the forward, dh of the backward pass, or null
+  float* h_out;             // [P][r]: h of the forward pass, or null
   int n, r, K, N, P, x_rows, y_rows, src_div;
   Divisor src;              // by src_div
   // Backward pass.
   const float* h;           // [P][r]
-  const float* dh;          // [P][r]: h_out of its first kernel
+  uint16_t* thin;           // dh and, thin_h numbers on, h as operands (adapters.h), or null
+  int64_t thin_h;
   const void* dy;           // [y_rows][N] of y's type
   void* dx;                 // [x_rows * src_div][K] bf16 or null
   float* da;                // [n][r][K] or null, with db
   float* db;                // [n][N][r]
 };
 hipError_t launch_adapters_forward(const AdapterArgs& A, bool y_f32, int cus, hipStream_t s, const KTime& kt = KTime{});
+size_t adapters_thin_bytes(int r, int64_t rows);
 hipError_t launch_adapters_backward(const AdapterArgs& A, bool y_f32, int cus, hipStream_t s, const KTime& kt = KTime{});
 
 // Measurement probes (csrc/probe.hip): a 16-byte-per-lane streaming read of

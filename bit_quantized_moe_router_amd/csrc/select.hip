@@ -938,8 +938,9 @@ constexpr int64_t kSortSmall = 4096;
 constexpr int kSelectSmall = 32;
 
 int sort_parts(int64_t n) {
-  const int64_t parts = (n + kSortSmall - 1) / kSortSmall;
-  return (int)(parts < 1 ? 1 : parts < kSortMaxParts ? parts : kSortMaxParts);
+  if (n <= kSortSmall) return 1;
+  const int64_t parts = (n + kSortThreads - 1) / kSortThreads;
+  return (int)(parts < kSortMaxParts ? parts : kSortMaxParts);
 }
 
 int select_parts(int T) {

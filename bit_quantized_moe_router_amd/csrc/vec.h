@@ -39,6 +39,9 @@ struct RowPiece {
           const uint4 v = load_any<uint4>(static_cast<const char*>(p) + 4 * i);
           w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
         }
+      } else if constexpr (kWords == 2) {
+        const uint2 v = load_any<uint2>(p);
+        w[0] = v.x, w[1] = v.y;
       } else {
 #pragma unroll
         for (int i = 0; i < kWords; i++) w[i] = load_any<uint32_t>(static_cast<const char*>(p) + 4 * i);
@@ -59,6 +62,8 @@ struct RowPiece {
 #pragma unroll
         for (int i = 0; i < kWords; i += 4)
           store_any(static_cast<char*>(p) + 4 * i, make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]));
+      } else if constexpr (kWords == 2) {
+        store_any(p, make_uint2(w[0], w[1]));
       } else {
 #pragma unroll
         for (int i = 0; i < kWords; i++) store_any(static_cast<char*>(p) + 4 * i, w[i]);
