@@ -423,22 +423,21 @@ template <bool Back, bool YF32>
 hipError_t adapters_rows_any(const AdapterArgs& A, int cus, hipStream_t s, hipEvent_t ev0, hipEvent_t ev1) {
   const int nr = adapter_frags(A.r);
   const bool even = A.K % 8 == 0 && A.N % 8 == 0 && A.r % 8 == 0;
-  const int64_t tiles = ((int64_t)A.P + 15) / 16;  // with the last ones of adapters, a few more
-  const bool some = 4 * tiles > 3 * cus, many = even && tiles >= 4 * cus;
+  // Tiles of 32 positions from a tile of 16 a compute unit on, and from rank 17 on (8 adapters, 2048 -> 2048 bf16, forward,
+  // us with 16 / 32 positions: rank 64, 2048 rows 27 / 26, 4096 rows 42 / 31, 32768 rows 212 / 163; rank 32, 2048 rows
+  // 19 / 21, 4096 rows 27 / 23, 32768 rows 134 / 121; rank 16, 8192 rows 28 / 33, 32768 rows 106 / 106).  16 waves instead
+  // of 8 were no faster (rank 16, 16 rows 8.8 against 7.2, 4096 rows 23.1 against 20.3).
+  const bool many = even && (int64_t)A.P >= 16 * cus;
   auto* f = !even ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, false>
                      : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 8, false>
                      : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, false>
                                : adapters_rows<Back, YF32, 1, 8, 8, false>)
-            : many  ? (nr == 1   ? adapters_rows<Back, YF32, 2, 1, 8, true>
+            : many  ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, true>
                        : nr == 2 ? adapters_rows<Back, YF32, 2, 2, 8, true>
                        : nr == 4 ? adapters_rows<Back, YF32, 2, 4, 8, true>
                                  : adapters_rows<Back, YF32, 1, 8, 8, true>)
-            : some  ? (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, true>
+                    : (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 8, true>
                        : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 8, true>
-                       : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, true>
-                                 : adapters_rows<Back, YF32, 1, 8, 8, true>)
-                    : (nr == 1   ? adapters_rows<Back, YF32, 1, 1, 16, true>
-                       : nr == 2 ? adapters_rows<Back, YF32, 1, 2, 16, true>
                        : nr == 4 ? adapters_rows<Back, YF32, 1, 4, 8, true>
                                  : adapters_rows<Back, YF32, 1, 8, 8, true>);
   return f(A, cus, s, ev0, ev1);

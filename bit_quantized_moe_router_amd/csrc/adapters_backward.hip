@@ -5,8 +5,6 @@
 
 namespace moe {
 
-constexpr int kAdWaves = 4;
-
 // ---------------------------------------------------------------------------
 // A workgroup takes 16 F columns of x (for dA) or of dy (for dB) and up to 64 ranks
 // of one adapter, and its rows 32 at a time.  Lane (m, q) reads columns F m ..
@@ -14,21 +12,21 @@ constexpr int kAdWaves = 4;
 // fragments (row m of fragment f: column F m + f), and the same rows of rank m
 // of dh or h from where k_adapters_rows has left them in three parts.  Even: the
 // widths are multiples of 8, the rank of 4.
-// The four waves of a workgroup take the rows in turn and join their sums
-// through LDS in a fixed order.
+// The W waves of a workgroup take the rows in turn and join their sums through
+// LDS in a fixed order.
 // ---------------------------------------------------------------------------
-template <bool WideF32, int NB, int F, bool Even>
+template <bool WideF32, int NB, int F, int W, bool Even>
 __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, int e, int block, int rank0, int rpad,
                                             float (*s_sum)[16 * F + 4]) {
   constexpr int kIn = WideF32 ? 3 : 1;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int m = lane & 15, q = lane >> 4;
-  const int r = A.r, W = for_a ? A.K : A.N;
+  const int r = A.r, wide_n = for_a ? A.K : A.N;
   const int lo = min(max(A.offsets[e], 0), A.P), hi = min(max(A.offsets[e + 1], lo), A.P);
   const char* wide = static_cast<const char*>(for_a ? (const void*)A.x : A.dy);
   const uint16_t* thin = A.thin + (for_a ? 0 : A.thin_h);
   const int32_t* names = for_a ? A.src_rows : A.dst_rows;
-  const int c0 = block * 16 * F + F * m, left = W - c0;
+  const int c0 = block * 16 * F + F * m, left = wide_n - c0;
   f32x4_t acc[F][NB] = {};
   const int last = hi > lo ? (hi + 31) >> 5 : 0;
   // The eight rows' names, a step ahead of the rows.
@@ -48,9 +46,9 @@ __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, in
   int c = (lo >> 5) + wave;
   int row[8];
   if (c < last) name(c, row);
-  for (; c < last; c += kAdWaves) {
+  for (; c < last; c += W) {
     int ahead[8];
-    if (c + kAdWaves < last) name(c + kAdWaves, ahead);
+    if (c + W < last) name(c + W, ahead);
     uint4 t[NB][3];
 #pragma unroll
     for (int b = 0; b < NB; b++)
@@ -66,7 +64,7 @@ __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, in
       if (for_a && A.src_div > 1 && at >= 0) at = div_by(at, A.src);
       in[j] = p >= lo && p < hi && (unsigned)at < (unsigned)(for_a ? A.x_rows : A.y_rows);
       x[j].clear();
-      if (in[j] && left > 0) x[j].load(wide + ((int64_t)at * W + c0) * (WideF32 ? 4 : 2), Even ? F : left);
+      if (in[j] && left > 0) x[j].load(wide + ((int64_t)at * wide_n + c0) * (WideF32 ? 4 : 2), Even ? F : left);
     }
     // Rows of other adapters, and rows outside x or dy, count as zeros whatever dh or h hold for them.
     uint32_t mask[4];
@@ -119,8 +117,8 @@ __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, in
 #pragma unroll
     for (int j = 0; j < 8; j++) row[j] = ahead[j];
   }
-  // Waves 3, 2, 1, 0, each adding to what those before it left.  Ranks 4 q + i of column F m + f.
-  const int waves = max(1, min(kAdWaves, last - (lo >> 5)));
+  // The last wave to the first, each adding to what those before it left.  Ranks 4 q + i of column F m + f.
+  const int waves = max(1, min(W, last - (lo >> 5)));
   for (int w = waves - 1; w > 0; w--) {
     if (wave == w) {
 #pragma unroll
@@ -153,7 +151,7 @@ __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, in
         if (cr + i >= r) continue;
         RowPiece<true, F> o;
         o.set(v[i]);
-        o.store(A.da + ((int64_t)e * r + cr + i) * W + c0, Even ? F : left);
+        o.store(A.da + ((int64_t)e * r + cr + i) * wide_n + c0, Even ? F : left);
       }
     } else {
 #pragma unroll
@@ -162,45 +160,46 @@ __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, in
         const float u[4] = {v[0][f], v[1][f], v[2][f], v[3][f]};
         RowPiece<true, 4> o;
         o.set(u);
-        o.store(A.db + ((int64_t)e * W + c0 + f) * r + cr, Even ? 4 : r - cr);
+        o.store(A.db + ((int64_t)e * wide_n + c0 + f) * r + cr, Even ? 4 : r - cr);
       }
     }
   }
 }
 
-template <bool YF32, int NB, int F, bool Even>
-__global__ __launch_bounds__(64 * kAdWaves) void k_adapters_sums(AdapterArgs A, int blocks_a, int blocks_b, int rank_blocks) {
+template <bool YF32, int NB, int F, int W, bool Even>
+__global__ __launch_bounds__(64 * W) void k_adapters_sums(AdapterArgs A, int blocks_a, int blocks_b, int rank_blocks) {
   __shared__ float s_sum[16 * NB][16 * F + 4];
   const int per = (blocks_a + blocks_b) * rank_blocks;
   const int e = blockIdx.x / per;
   int u = blockIdx.x - e * per;
   const int rank0 = u % rank_blocks * 16 * NB, rpad = 16 * NB * rank_blocks;
   u /= rank_blocks;
-  if (u < blocks_a) adapter_sum<false, NB, F, Even>(A, true, e, u, rank0, rpad, s_sum);
-  else adapter_sum<YF32, NB, F, Even>(A, false, e, u - blocks_a, rank0, rpad, s_sum);
+  if (u < blocks_a) adapter_sum<false, NB, F, W, Even>(A, true, e, u, rank0, rpad, s_sum);
+  else adapter_sum<YF32, NB, F, W, Even>(A, false, e, u - blocks_a, rank0, rpad, s_sum);
 }
 
-template <bool YF32, int NB, int F, bool Even>
+template <bool YF32, int NB, int F, int W, bool Even>
 static void launch_sums(const AdapterArgs& A, hipStream_t s, const KTime& kt, hipEvent_t ev0) {
   constexpr int kCols = 16 * F;
   const int ba = (A.K + kCols - 1) / kCols, bb = (A.N + kCols - 1) / kCols, rb = (A.r + 16 * NB - 1) / (16 * NB);
-  MOE_LAUNCH((k_adapters_sums<YF32, NB, F, Even>), dim3((unsigned)(A.n * (ba + bb) * rb)), dim3(64 * kAdWaves), 0, s, ev0,
+  MOE_LAUNCH((k_adapters_sums<YF32, NB, F, W, Even>), dim3((unsigned)(A.n * (ba + bb) * rb)), dim3(64 * W), 0, s, ev0,
              kt.stop, A, ba, bb, rb);
 }
 
 template <bool YF32, int NB>
 static void sums(const AdapterArgs& A, int cus, hipStream_t s, const KTime& kt, hipEvent_t ev0) {
-  // Fewer columns a workgroup where 128 leave compute units without one (3 adapters of rank 64, 2048 + 1000 columns, 2085
-  // rows: 28 us with 32 columns).  Waves with columns of their own and all of an adapter's rows were slower where
-  // adapters have unlike numbers of rows (256 adapters of 128 rows on average: 118 us against 57).
-  const int64_t blocks = (int64_t)A.n * ((A.K + 127) / 128 + (A.N + 127) / 128) * ((A.r + 16 * NB - 1) / (16 * NB));
+  // 64 columns by 4 waves where those are workgroups enough, by 8 where the rows' turns would take longer than the rest, and
+  // 32 columns by more waves still where many compute units would have none.  Both kernels of the backward pass, 4096 rows,
+  // us with 32 by 16 (8 for rank 64) / 64 by 8 / 64 by 4 / 128 by 4:
+  //   rank 16:  1 adapter of 512 -> 512  29 / 38 / 52 / 55     3 of 2048 -> 2048  37 / 36 / 45 / 48
+  //             8 of 2048 -> 2048  39 / 34 / 40 / 42           64 of 2048 -> 2048  63 / 39 / 34 / 33
+  //   rank 64:  1 of 512 -> 512  53 / 58 / 76 / 99             8 of 4096 -> 4096  87 / 84 / 80 / 111
+  const int64_t blocks = (int64_t)A.n * ((A.K + 63) / 64 + (A.N + 63) / 64) * ((A.r + 16 * NB - 1) / (16 * NB));
   const bool even = A.K % 8 == 0 && A.N % 8 == 0 && A.r % 4 == 0;
-  auto* f = even ? (blocks >= cus       ? launch_sums<YF32, NB, 8, true>
-                    : blocks >= cus / 2 ? launch_sums<YF32, NB, 4, true>
-                                        : launch_sums<YF32, NB, 2, true>)
-                 : (blocks >= cus       ? launch_sums<YF32, NB, 8, false>
-                    : blocks >= cus / 2 ? launch_sums<YF32, NB, 4, false>
-                                        : launch_sums<YF32, NB, 2, false>);
+  constexpr int kMost = NB == 4 ? 8 : 16;
+  auto* f = blocks >= 8 * cus ? (even ? launch_sums<YF32, NB, 4, 4, true> : launch_sums<YF32, NB, 4, 4, false>)
+            : blocks >= cus   ? (even ? launch_sums<YF32, NB, 4, 8, true> : launch_sums<YF32, NB, 4, 8, false>)
+                              : (even ? launch_sums<YF32, NB, 2, kMost, true> : launch_sums<YF32, NB, 2, kMost, false>);
   f(A, s, kt, ev0);
 }
 

@@ -193,12 +193,13 @@ hipError_t launch_combine_forward(const CombineArgs& A, hipStream_t s, const KTi
 
 template <bool RF, bool YF>
 static void launch_grad(const CombineArgs& A, hipStream_t s, const KTime& kt) {
-  // Four waves a token where few tokens would leave the device idle (1 token of 10 rows of 4222 bf16 values: 20 us against
-  // 24); part of a wave where a row is narrow (15920 tokens of 6 rows of 61: 12 us against 43).
+  // Four waves a token where a row has pieces for more than one (8 bf16 rows of 2048, a wave or four a token: 1 token 15.6,
+  // 7.2 us; 512 tokens 20.5, 11.3; 2048 tokens 30.3, 28.0); part of a wave where it has few (15920 tokens of 6 rows of 61,
+  // a wave a token or 8 lanes: 42.7, 14.3).
   const int64_t pieces = (A.H + kCombCols<RF> - 1) / kCombCols<RF>;
   int log2 = 0;
   while (log2 < 6 && (1 << log2) < pieces) log2++;
-  const int waves = log2 < 6 ? 0 : A.T < 1024 && pieces > 64 ? 4 : 1;
+  const int waves = log2 < 6 ? 0 : pieces > 64 ? 4 : 1;
   const int64_t tokens = waves == 0 ? kCombThreads >> log2 : waves == 1 ? 4 : 1, groups = (A.T + tokens - 1) / tokens;
   const dim3 grid((unsigned)(groups < kCombGrid ? groups : kCombGrid));
   auto go = [&](auto kb) {
