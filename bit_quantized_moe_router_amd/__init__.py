@@ -371,8 +371,9 @@ def _same_type(kind, of, names):
 
 def make_select_desc(n_experts, top_k, scores=MOE_SOFTMAX, n_groups=1, top_groups=1, group_best=1, renormalise=1,
                      scale=1.0) -> SelectDesc:
-    return SelectDesc(_int32(n_experts, "n_experts"), _int32(top_k, "top_k"), scores, _int32(n_groups, "n_groups"),
-                      _int32(top_groups, "top_groups"), group_best, renormalise, scale)
+    sizes = dict(n_experts=n_experts, top_k=top_k, scores=scores, n_groups=n_groups, top_groups=top_groups,
+                 group_best=group_best, renormalise=renormalise)
+    return SelectDesc(*(_int32(v, name) for name, v in sizes.items()), scale)
 
 
 def moe_select_workspace_bytes(T: int, n_experts: int, top_k: int) -> int:
@@ -446,7 +447,10 @@ def _combine_shape(rows, y, name, *by_place):
     if rows.dim() != 2 or y.dim() != 2 or (rows.shape[0] % y.shape[0] if y.shape[0] else rows.shape[0]):
         _bad(f"rows must be [T * k, width] and {name} [T, width] (got {tuple(rows.shape)}, {tuple(y.shape)})")
     T = y.shape[0]
-    k = rows.shape[0] // T if T else next((t.shape[-1] for t in by_place if t is not None and t.dim() > 1), 1)
+    if T:
+        k = rows.shape[0] // T
+    else:
+        k = next((t.shape[-1] for t in by_place if t is not None and t.dim() > 1), 1)
     return _int32(T, "T"), _int32(k, "k"), _int32(y.shape[1], "width"), y.get_device()
 
 

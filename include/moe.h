@@ -482,8 +482,8 @@ moe_status moe_select_forward(const moe_select_desc *desc, const void *logits, i
 
 /*
  * Gradient with respect to the logits for dweights [T][k] float, from what the
- * forward call read and wrote (ids and the bias have none), with the dw of a
- * place whose id is -1 left out:
+ * forward call read and wrote (ids and the bias have none; the ids of a row
+ * differ), with the dw of a place whose id is -1 left out:
  *   dlogits = base + (d weights / d logits)^T dweights
  *   base     [T][E] of logits_type or NULL (zeros): the gradient to add to, such
  *            as moe_balance_loss_backward's
@@ -517,7 +517,7 @@ moe_status moe_sort_assignments(const int32_t *ids, int32_t n, int32_t n_experts
  *   topk_ids [T][k] int32 or NULL: every row takes part
  *   weights  [T][k] float or NULL: 1
  *   base     [T][width] of y_type (MOE_F32 or MOE_BF16) or NULL: zeros
- *   y        [T][width] of y_type; may be base
+ *   y        [T][width] of y_type; may be base, overlaps nothing else
  * 1 <= k <= 16, 1 <= width <= 2^24, T * k < 2^31, any alignment of the types;
  * sums in float32 in the order base, j = 0, 1, ..., rounded once to y_type.
  */
@@ -526,8 +526,8 @@ moe_status moe_combine_forward(const void *rows, int32_t rows_type, int32_t T, i
                                int32_t y_type, void *stream);
 
 /*
- * Its gradients: drows[t * k + j] = weights[t][j] * dy[t] (of rows_type, may be
- * rows) and dweights[t][j] = sum_c dy[t][c] rows[t * k + j][c] (float), zeros
+ * Its gradients: drows[t * k + j] = weights[t][j] * dy[t] (of rows_type; may be
+ * rows, overlaps nothing else) and dweights[t][j] = sum_c dy[t][c] rows[t * k + j][c] (float), zeros
  * where the id is negative; either may be NULL, and rows where dweights is.
  * base's gradient is dy.
  */
@@ -554,9 +554,10 @@ typedef struct {
 /*
  * y[dst(i)] = base[dst(i)] + scales[a] * B_a (A_a x[src(i)]) for the positions i
  * in [offsets[a], offsets[a+1]).
- *   a, b      [n_adapters][rank][n_in] and [n_adapters][n_out][rank] bf16
+ *   a, b      [n_adapters][rank][n_in] and [n_adapters][n_out][rank] bf16, finite
  *   scales    [n_adapters] float or NULL: 1
- *   x         [x_rows][n_in] bf16
+ *   x         [x_rows][n_in] bf16; a NaN or an infinity makes its row of y NaN
+ *             (or an infinity) and reaches no other
  *   offsets   [n_adapters+1] int32, as in moe_mx4_experts
  *   rows      the positions' upper bound on the host, at most 2^24
  *   src_rows, src_div, dst_rows  as in moe_mx4_experts
@@ -589,7 +590,8 @@ moe_status moe_adapters_forward(const moe_adapter_desc *desc, const uint16_t *a,
  * taken as 1.
  *   h     as the forward call wrote it
  *   base  of dx, bf16, or NULL: zeros; may be dx
- *   dx    may be NULL, with base; rows of no position stay as they were
+ *   dx    may be NULL, with base; rows of no position stay as they were; src_rows
+ *         then names each row at most once
  *   da, db  may be NULL both; written for every adapter, zeros for one without rows
  *   ws    moe_adapters_workspace_bytes(desc, rows) bytes, 16-byte aligned, not
  *         shared by calls that overlap in time

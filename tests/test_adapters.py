@@ -232,6 +232,18 @@ def test_many_rows(gpu, r, out):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("out", [f32, bf16])
+@pytest.mark.parametrize("n,r,K,N", [(40, 16, 520, 264), (40, 40, 523, 257), (48, 64, 512, 136), (20, 100, 648, 272),
+                                     (190, 16, 512, 256), (190, 30, 516, 250), (140, 64, 640, 384), (90, 128, 704, 520)])
+def test_many_adapters(gpu, n, r, K, N, out):
+    """Columns enough for each of the weight gradients' workgroups, adapters with no row, with few and with many."""
+    rng = np.random.default_rng(n + r)
+    lens = rng.integers(0, 6, n)
+    lens[[1, n // 2, n - 1]] = 0, 300, 70
+    Adapters(gpu, lens.tolist(), r, K, N, out, n, extra=3).check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K,N", [(24, 16), (25, 17)])
 def test_rows_outside(gpu, K, N):
     """Source rows outside x count as zeros; destinations outside y are not written; bad offsets reach nothing."""

@@ -286,6 +286,39 @@ def test_close_scores(gpu, softmax, E):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T", [9, 150])
+def test_all_chosen_side_by_side(gpu, T, dtype):
+    """More of the chosen next to each other than a group of lanes keeps sorted for its share."""
+    logits, bias, _ = make(gpu, T, 512, dtype, 11)
+    rows = torch.arange(T, device=gpu)
+    for i in range(14):
+        logits[rows, (32 * (rows % 16) + 2 * i) % 512] += 12
+    for kw in (dict(), dict(bias=bias), dict(bias=bias, groups=4, top_groups=2, best=2)):
+        Select(logits, 16, True, **kw).check()
+        Select(logits, 16, False, **kw).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(5000, 256, 8), (8200, 60, 6), (300001, 16, 4)])
+def test_many_tokens(gpu, T, E, k):
+    """Workgroups that go through their tokens in several turns; the choice against a sort, the order against the ids."""
+    logits, _, valid = make(gpu, T, E, torch.float32, T)
+    x = Select(logits, k, valid=valid)
+    x.forward()
+    best, at = torch.sort(logits, dim=1, descending=True, stable=True)
+    ids = torch.where(valid[:, None], at[:, :k].to(i32), -1)
+    assert torch.equal(x.ids, ids)
+    w = torch.softmax(best[:, :k].double(), 1) * valid[:, None]
+    # The difference of two logits is rounded once, its exponential and the quotient add a few steps.
+    assert ((x.w - w).abs() <= (24 + 4 * 12) * ref.U * w).all()
+    counts, offsets, order = ref.order(ids.cpu().numpy(), E)
+    assert np.array_equal(x.counts.cpu().numpy(), counts) and np.array_equal(x.offsets.cpu().numpy(), offsets)
+    places = x.order.cpu().numpy()
+    assert np.array_equal(places[:len(order)], order) and (places[len(order):] == -7).all()
+
+
+@pytest.mark.gpu
 def test_close_groups_without_a_bias(gpu):
     """Groups whose sums of two agree to a few steps of float32."""
     g = torch.Generator().manual_seed(5)
