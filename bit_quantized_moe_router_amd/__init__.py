@@ -358,7 +358,7 @@ def _matrix(t, name, rows, cols, dev=None):
     if t is None:
         return None, None
     kind = _value_type(t, name)
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or not t.is_contiguous() or t.get_device() != dev:
+    if t.shape != (rows, cols) or not t.is_contiguous() or t.get_device() != dev:
         _bad(f"{name} must be a contiguous [{rows}, {cols}] tensor on the call's device (got {tuple(t.shape)}, strides "
              f"{t.stride()}, {t.device})")
     return kind, t.data_ptr()
@@ -444,14 +444,16 @@ def moe_sort_assignments(ids, n_experts, expert_counts, expert_offsets, sorted_a
 def _combine_shape(rows, y, name, *by_place):
     """(T, k, width, device index) from rows [T * k, width] and y or dy [T, width]; without tokens k is that of the first
     [T, k] tensor."""
-    if rows.dim() != 2 or y.dim() != 2 or (rows.shape[0] % y.shape[0] if y.shape[0] else rows.shape[0]):
-        _bad(f"rows must be [T * k, width] and {name} [T, width] (got {tuple(rows.shape)}, {tuple(y.shape)})")
-    T = y.shape[0]
+    if rows.dim() != 2 or y.dim() != 2:
+        _bad(f"rows and {name} must be 2-D (got {tuple(rows.shape)}, {tuple(y.shape)})")
+    n, (T, width) = rows.shape[0], y.shape
     if T:
-        k = rows.shape[0] // T
+        k = n // T
     else:
         k = next((t.shape[-1] for t in by_place if t is not None and t.dim() > 1), 1)
-    return _int32(T, "T"), _int32(k, "k"), _int32(y.shape[1], "width"), y.get_device()
+    if n != T * k:
+        _bad(f"rows must be [T * k, width] and {name} [T, width] (got {tuple(rows.shape)}, {tuple(y.shape)})")
+    return _int32(T, "T"), _int32(k, "k"), _int32(width, "width"), y.get_device()
 
 
 def moe_combine_forward(rows, topk_ids, weights, base, y, stream=None):
@@ -500,7 +502,8 @@ def moe_adapters_workspace_bytes(desc, rows: int) -> int:
 
 
 def _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows):
-    """What both directions take alike: (device index, the arguments up to dst_rows but for the rows of y)."""
+    """What both directions take alike: (device index, rows, src_div, x's rows), (a, b, scales, x), (offsets, src_rows,
+    dst_rows)."""
     torch = _torch()
     n, r, K, N = desc.n_adapters, desc.rank, desc.n_in, desc.n_out
     dev, bf16, i32 = x.get_device(), torch.bfloat16, torch.int32
@@ -509,12 +512,11 @@ def _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_r
     if x.dim() != 2 or x.shape[1] != K:
         _bad(f"x must be 2-D with {K} columns (got {tuple(x.shape)})")
     rows, src_div, x_rows = _int32(rows, "rows"), _int32(src_div, "src_div"), _int32(x.shape[0], "the number of x's rows")
-    return dict(dev=dev, rows=rows, src_div=src_div, x_rows=x_rows, a=_arg(a, "a", bf16, n * r * K, dev, K),
-                b=_arg(b, "b", bf16, n * N * r, dev, r), x=_arg(x, "x", bf16, x_rows * K, dev, K),
-                scales=None if scales is None else _arg(scales, "scales", torch.float32, n, dev),
-                offsets=_arg(offsets, "offsets", i32, n + 1, dev),
-                src=None if src_rows is None else _arg(src_rows, "src_rows", i32, rows, dev),
-                dst=None if dst_rows is None else _arg(dst_rows, "dst_rows", i32, rows, dev))
+    return ((dev, rows, src_div, x_rows),
+            (_arg(a, "a", bf16, n * r * K, dev, K), _arg(b, "b", bf16, n * N * r, dev, r),
+             None if scales is None else _arg(scales, "scales", torch.float32, n, dev), _arg(x, "x", bf16, x_rows * K, dev)),
+            (_arg(offsets, "offsets", i32, n + 1, dev), None if src_rows is None else _arg(src_rows, "src_rows", i32, rows, dev),
+             None if dst_rows is None else _arg(dst_rows, "dst_rows", i32, rows, dev)))
 
 
 def _adapter_rows(desc, t, name, dev):
@@ -532,14 +534,14 @@ def moe_adapters_forward(desc, a, b, scales, x, offsets, rows, base, y, h=None, 
     """Position i of adapter e's range gives y[dst_rows[i]] = base (or zeros) + scales[e] * b[e] (a[e] x[src_rows[i] //
     src_div]); a [n, rank, n_in], b [n, n_out, rank], x bfloat16, scales [n] float32 or None, h [rows, rank] float32 or
     None: a[e] x by position, for the backward call."""
-    A = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows)
-    dev = A["dev"]
+    (dev, rows, src_div, x_rows), factors, (off, src, dst) = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows,
+                                                                           src_div, dst_rows)
     y_rows, yp = _adapter_rows(desc, y, "y", dev)
     base_kind, bp = _matrix(base, "base", y_rows, desc.n_out, dev)
     _same_type(base_kind, desc.y_type, "base and y")
-    hp = None if h is None else _arg(h, "h", _torch().float32, A["rows"] * desc.rank, dev, desc.rank)
-    _on_device(dev, stream, lib().moe_adapters_forward, C.byref(desc), A["a"], A["b"], A["scales"], A["x"], A["x_rows"],
-               A["offsets"], A["rows"], A["src"], A["src_div"], A["dst"], bp, yp, y_rows, hp)
+    hp = None if h is None else _arg(h, "h", _torch().float32, rows * desc.rank, dev, desc.rank)
+    _on_device(dev, stream, lib().moe_adapters_forward, C.byref(desc), *factors, x_rows, off, rows, src, src_div, dst, bp, yp,
+               y_rows, hp)
 
 
 def moe_adapters_backward(desc, a, b, scales, x, h, dy, offsets, rows, base, dx, da, db, ws=None, src_rows=None, src_div=1,
@@ -547,14 +549,15 @@ def moe_adapters_backward(desc, a, b, scales, x, h, dy, offsets, rows, base, dx,
     """The gradients for dy: dx [x's rows * src_div (without src_rows x's rows), n_in] bfloat16 = base (or zeros) + ..., da
     [n, rank, n_in] and db [n, n_out, rank] float32; dx (with base) and da with db may be None."""
     torch = _torch()
-    A = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows, src_div, dst_rows)
-    dev, n, r, K, N = A["dev"], desc.n_adapters, desc.rank, desc.n_in, desc.n_out
+    (dev, rows, src_div, x_rows), factors, (off, src, dst) = _adapter_args(desc, a, b, scales, x, offsets, rows, src_rows,
+                                                                           src_div, dst_rows)
+    n, r, K, N = desc.n_adapters, desc.rank, desc.n_in, desc.n_out
     y_rows, dyp = _adapter_rows(desc, dy, "dy", dev)
-    dx_rows = A["x_rows"] * (A["src_div"] if src_rows is not None else 1)
+    dx_rows = x_rows * (src_div if src_rows is not None else 1)
     bf16, f32 = torch.bfloat16, torch.float32
-    _on_device(dev, stream, lib().moe_adapters_backward, C.byref(desc), A["a"], A["b"], A["scales"], A["x"], A["x_rows"],
-               None if h is None else _arg(h, "h", f32, A["rows"] * r, dev, r), dyp, y_rows, A["offsets"], A["rows"],
-               A["src"], A["src_div"], A["dst"], None if base is None else _arg(base, "base", bf16, dx_rows * K, dev, K),
+    _on_device(dev, stream, lib().moe_adapters_backward, C.byref(desc), *factors, x_rows,
+               None if h is None else _arg(h, "h", f32, rows * r, dev, r), dyp, y_rows, off, rows, src, src_div, dst,
+               None if base is None else _arg(base, "base", bf16, dx_rows * K, dev, K),
                None if dx is None else _arg(dx, "dx", bf16, dx_rows * K, dev, K),
                None if da is None else _arg(da, "da", f32, n * r * K, dev, K),
                None if db is None else _arg(db, "db", f32, n * N * r, dev, r), *_bytes(ws, dev))

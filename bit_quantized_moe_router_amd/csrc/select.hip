@@ -340,7 +340,7 @@ typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 
 template <bool F32, int By, bool Biased>
 __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0, int64_t t1, const SelectLane& L,
-                                                const BiasRange& B, const float4* s_bias, int* s_count) {
+                                                const BiasRange& B, const float4* s_bias, int* s_count, int* s_ids) {
   constexpr uint32_t kScore = 0xFFFFFE00u;  // a key's bits of the score
   const int lane = threadIdx.x & 63, g = lane & 15;
   const int64_t t = t0 + (lane >> 4);
@@ -588,6 +588,7 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
       A.ids[t * A.k + g] = id;
       A.weights[t * A.k + g] = w;
       if (s_count && id >= 0) atomicAdd(&s_count[id], 1);
+      if (s_ids) s_ids[t * A.k + g] = id;
     }
   }
   return todo;
@@ -596,7 +597,7 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
 // One token a wave: rows that the 16-lane form leaves open or has no lanes for (more than 16 groups, or groups too wide
 // for their lanes).
 template <bool F32>
-__device__ __forceinline__ void select_one(const SelectArgs& A, int64_t t, SelectLds& lds, int* s_count) {
+__device__ __forceinline__ void select_one(const SelectArgs& A, int64_t t, SelectLds& lds, int* s_count, int* s_ids) {
   const int lane = threadIdx.x & 63;
   int id = -1;
   float w = 0.f;
@@ -618,16 +619,17 @@ __device__ __forceinline__ void select_one(const SelectArgs& A, int64_t t, Selec
     A.ids[t * A.k + lane] = id;
     A.weights[t * A.k + lane] = w;
     if (s_count && id >= 0) atomicAdd(&s_count[id], 1);
+    if (s_ids) s_ids[t * A.k + lane] = id;
   }
 }
 
-// Tokens [t0, t1) by `waves` waves.
+// Tokens [t0, t1) by `waves` waves; s_ids: a copy of the ids in LDS, or null.
 template <bool F32, int By>
 __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, int64_t t1, int waves, SelectLds* lds,
-                                             float* s_bias, int* s_count) {
+                                             float* s_bias, int* s_count, int* s_ids) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if constexpr (By == kByOne) {
-    for (int64_t t = t0 + wave; t < t1; t += waves) select_one<F32>(A, t, lds[wave], s_count);
+    for (int64_t t = t0 + wave; t < t1; t += waves) select_one<F32>(A, t, lds[wave], s_count, s_ids);
   } else {
     const BiasRange B = bias_range(A);
     const SelectLane L = select_lane(A);
@@ -649,7 +651,7 @@ __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, in
         const int64_t from = t;
         uint64_t open = 0;  // four bits a turn
         for (int i = 0; i < 16 && t < t1; i++, t += step) {
-          const uint64_t todo = select_four<F32, By, biased.value>(A, t, t1, L, B, s_b, s_count);
+          const uint64_t todo = select_four<F32, By, biased.value>(A, t, t1, L, B, s_b, s_count, s_ids);
           if (todo) {
 #pragma unroll
             for (int r = 0; r < 4; r++) open |= (uint64_t)(((todo >> (16 * r)) & 0xFFFFu) != 0) << (4 * i + r);
@@ -657,7 +659,7 @@ __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, in
         }
         for (; open; open &= open - 1) {
           const int b = __builtin_ctzll(open);
-          select_one<F32>(A, from + (b >> 2) * step + (b & 3), lds[wave], s_count);
+          select_one<F32>(A, from + (b >> 2) * step + (b & 3), lds[wave], s_count, s_ids);
         }
       }
     };
@@ -675,7 +677,7 @@ __global__ __launch_bounds__(NT) void k_select(SelectArgs A) {
   for (int e = threadIdx.x; e < A.E; e += NT) s_count[e] = 0;
   __syncthreads();
   const int64_t t0 = (int64_t)blockIdx.x * A.per_part, t1 = min((int64_t)A.T, t0 + A.per_part);
-  select_range<F32, By>(A, t0, t1, NT / 64, lds, s_bias, A.part_count ? s_count : nullptr);
+  select_range<F32, By>(A, t0, t1, NT / 64, lds, s_bias, A.part_count ? s_count : nullptr, nullptr);
   if (!A.part_count) return;
   __syncthreads();
   for (int e = threadIdx.x; e < A.E; e += NT) A.part_count[(int64_t)blockIdx.x * A.E + e] = s_count[e];
@@ -754,10 +756,47 @@ __device__ __forceinline__ void sort_all(const SortArgs& A, int (*s_cnt)[kMaxE],
   });
 }
 
+// A handful of assignments, their ids in LDS: thread e counts those of expert e and of lower ones, thread a those that
+// come before its own.  No sums over lanes or waves, one way through LDS, but every id is looked at by every thread: of 256
+// experts 8 ids take 1.91 us against 2.72, 16 ids 2.24 against 2.72, 24 ids 2.76 against 2.73, 64 ids 4.81 against 2.74.
+constexpr int kSortTiny = 16;
+
+__device__ __forceinline__ void sort_tiny(const SortArgs& A, const int* s_ids) {
+  const int tid = threadIdx.x, n = (int)A.n;
+  if ((tid & ~63) >= max(n, A.E)) return;  // a wave with neither
+  const int mine = tid < n ? s_ids[tid] : -1;
+  const int4* four = reinterpret_cast<const int4*>(s_ids);
+  int lower = 0, same = 0, before = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; i += 4) {
+    const int4 v = four[i >> 2];
+    const int e4[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int e = i + j < n && (unsigned)e4[j] < (unsigned)A.E ? e4[j] : kMaxE;  // the last: counted nowhere
+      lower += e < tid ? 1 : 0;
+      same += e == tid ? 1 : 0;
+      before += e < mine || (e == mine && i + j < tid) ? 1 : 0;
+    }
+  }
+  if (tid < A.E) {
+    A.counts[tid] = same;
+    A.offsets[tid] = lower;
+    if (tid == A.E - 1) A.offsets[A.E] = lower + same;
+  }
+  if ((unsigned)mine < (unsigned)A.E) A.sorted[before] = tid;
+}
+
 // Few assignments: one workgroup.
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(SortArgs A) {
-  __shared__ int s_cnt[kSortThreads / 64][kMaxE];
+  __shared__ __attribute__((aligned(16))) int s_cnt[kSortThreads / 64][kMaxE];
   __shared__ int s_wave[kMaxE / 64];
+  if (A.n <= kSortTiny) {
+    if (threadIdx.x < A.n) s_cnt[0][threadIdx.x] = A.ids[threadIdx.x];
+    __syncthreads();
+    sort_tiny(A, s_cnt[0]);
+    return;
+  }
   sort_all<kSortThreads>(A, s_cnt, s_wave);
 }
 
@@ -766,8 +805,14 @@ template <bool F32, int By>
 __global__ __launch_bounds__(kSmallThreads) void k_select_small(SelectArgs A, SortArgs S) {
   __shared__ SelectLds lds[kSmallThreads / 64];
   __shared__ __attribute__((aligned(16))) float s_bias[kMaxE];
-  select_range<F32, By>(A, 0, A.T, kSmallThreads / 64, lds, s_bias, nullptr);
+  __shared__ __attribute__((aligned(16))) int s_ids[kSortTiny];
+  const bool tiny = S.n <= kSortTiny;
+  select_range<F32, By>(A, 0, A.T, kSmallThreads / 64, lds, s_bias, nullptr, tiny ? s_ids : nullptr);
   __syncthreads();
+  if (tiny) {
+    sort_tiny(S, s_ids);
+    return;
+  }
   int(*s_cnt)[kMaxE] = reinterpret_cast<int(*)[kMaxE]>(lds);
   static_assert(sizeof(lds) >= sizeof(int) * kSmallThreads / 64 * kMaxE, "the counters take the scores' place");
   __shared__ int s_wave[kMaxE / 64];

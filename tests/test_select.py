@@ -461,6 +461,40 @@ def test_sort(gpu, n, E):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 2, 8, 15, 16, 17, 63, 129])
+@pytest.mark.parametrize("E", [1, 16, 65, 512])
+def test_sort_few(gpu, n, E):
+    """Few assignments, those of no expert and equal ones among them; nothing behind what is asked for is written."""
+    g = torch.Generator().manual_seed(n * 1000 + E)
+    for ids in (torch.randint(-1, E + 1, (n,), generator=g, dtype=i32), torch.full((n,), E - 1, dtype=i32),
+                torch.full((n,), 2 ** 31 - 1, dtype=i32)):
+        full = lambda m: torch.full((m + 4,), -9, dtype=i32, device=gpu)  # noqa: E731
+        counts, offsets, order = full(E), full(E + 1), full(n)
+        ws = torch.empty(moe.moe_sort_workspace_bytes(n, E), dtype=torch.uint8, device=gpu)
+        moe.moe_sort_assignments(ids.to(gpu), E, counts[:E], offsets[:E + 1], order[:n], ws)
+        want = ref.order(ids.numpy(), E)
+        for got, exact in zip((counts, offsets, order), want):
+            got = got.cpu().numpy()
+            assert np.array_equal(got[:len(exact)], exact) and (got[len(exact):] == -9).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 8), (1, 16), (2, 8), (3, 6), (5, 3), (16, 1), (17, 1)])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_order_of_few(gpu, T, k, groups):
+    """The order that comes with a choice for few tokens is that of its ids, rows without an expert among them."""
+    logits, bias, _ = make(gpu, T, 64, torch.float32, 31 * T + k)
+    x = Select(logits, k, True, groups, 1 if groups == 1 else 2, 1, bias=bias)
+    x.forward()
+    for _ in range(2):
+        want = ref.order(x.ids.cpu().numpy().reshape(-1), 64)
+        for got, exact in zip((x.counts, x.offsets, x.order), want):
+            assert np.array_equal(got.cpu().numpy()[:len(exact)], exact)
+        x.logits[T // 2] = -float("inf")
+        x.forward()
+
+
+@pytest.mark.gpu
 def test_sort_nothing(gpu):
     counts, offsets = torch.full((6,), 3, dtype=i32, device=gpu), torch.full((7,), 3, dtype=i32, device=gpu)
     empty = torch.empty(0, dtype=i32, device=gpu)
