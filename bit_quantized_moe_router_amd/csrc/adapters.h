@@ -102,6 +102,14 @@ __device__ __forceinline__ RowPiece<F32, 8> piece8(const void* row, int64_t at, 
 // the same positions, each of which shrinks for itself.
 // Even: n_in, n_out and rank are multiples of 8 (rank of NR in the backward
 // direction), so that a run of 8 is in its row or out of it.
+//
+// Bound in small calls by the chain offsets -> source rows -> x and A -> sum of the
+// waves -> B (one row of rank 16, 2048 -> 2048, 7.5 us); in large ones by the bytes,
+// but a workgroup first only reads, then mostly writes, and a compute unit holds too
+// few of them to overlap the two throughout: 4096 rows of rank 16, 4096 -> 4096,
+// 36 us, 3.2 TB/s; 32768 rows of 256 adapters of rank 16, 2048 -> 1024, 79 us forward
+// (5.0 TB/s of what it moves, 325 MB read) and 74 backward (4.6 TB/s).  Consecutive
+// tiles on one XCD, so that an adapter's factors reach fewer caches, won 1 to 2 %.
 // ---------------------------------------------------------------------------
 template <bool Back, bool YF32, int RT, int NR, int W, bool Even>
 __global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int splits) {

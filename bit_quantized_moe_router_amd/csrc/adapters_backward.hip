@@ -14,6 +14,12 @@ namespace moe {
 // widths are multiples of 8, the rank of 4.
 // The W waves of a workgroup take the rows in turn and join their sums through
 // LDS in a fixed order.
+//
+// Bound by the chain offsets -> rows' names -> rows of each wave's few turns and the
+// join: 256 adapters of rank 16 over 32768 rows, 2048 -> 1024 in bf16, 62 us at 3.6 TB/s;
+// 3 of rank 64 over 2085 rows, 2048 -> 1000 in fp32, 19.9 us.  A wave with columns of its
+// own that no other wave shares needs no join, but an adapter with many rows then takes
+// as long as they do (skewed routing 118 us against 57).
 // ---------------------------------------------------------------------------
 template <bool WideF32, int NB, int F, int W, bool Even>
 __device__ __forceinline__ void adapter_sum(const AdapterArgs& A, bool for_a, int e, int block, int rank0, int rpad,

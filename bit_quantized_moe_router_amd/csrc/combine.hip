@@ -6,7 +6,12 @@
 // Forward: threads split the columns, each sums its columns over j in order,
 // with all of a token's rows in flight.  Backward: one pass over the rows
 // gives both gradients; the lanes of a token hold its k dot products until the
-// end.
+// end.  Sums are fp32, each result is rounded once, and there are no atomics.
+//
+// Measured: 1 token of 8 rows of 2048 columns fp32 4.2 us; 4096 tokens of 8 rows
+// of 2048 bf16 26.5 us, 6.4 TB/s with the last-level cache's share; 2085 tokens of
+// 6 rows of 1999 columns bf16, 15 % of them left out, 16.9 us forward and 31.2
+// backward (3.6 TB/s both), the rows' odd width leaving 7 of 8 unaligned.
 #include <type_traits>
 
 #include "launch.h"

@@ -545,7 +545,7 @@ moe_status moe_combine_backward(const void *dy, int32_t y_type, const void *rows
  */
 typedef struct {
     int32_t n_adapters; /* 1..512 */
-    int32_t rank;       /* 1..128; any larger rank of the store is padded by zeros of A and B */
+    int32_t rank;       /* 1..128; those of smaller rank beside others are padded by zeros of A and B */
     int32_t n_in;       /* 1..65536 */
     int32_t n_out;      /* 1..65536 */
     int32_t y_type;     /* MOE_F32 or MOE_BF16: the type of y, base and dy */
