@@ -987,7 +987,7 @@ static SelectArgs select_args(const moe_select_desc* d, const void* logits, int3
   A.T = T;
   A.E = d->n_experts;
   A.k = d->top_k;
-  // Groups that all stay, or that are single experts by their own score and index, leave every expert to choose from.
+  // Groups that all stay leave every expert to choose from.
   A.groups = d->top_groups == d->n_groups ? 1 : d->n_groups;
   A.per = d->n_experts / A.groups;
   A.top_groups = d->top_groups;

@@ -495,6 +495,25 @@ def test_order_of_few(gpu, T, k, groups):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [17, 64, 100, 2085, 4096, 4097, 70001])
+@pytest.mark.parametrize("runs", [1, 2, 3, 8])
+def test_sort_runs(gpu, n, runs):
+    """Long runs of one id, some of them no expert's, whose ends lie anywhere in a wave's 64."""
+    g = torch.Generator().manual_seed(n + runs)
+    cuts = torch.sort(torch.randint(0, n + 1, (runs - 1,), generator=g)).values.tolist()
+    values = torch.randint(-1, 9, (runs,), generator=g).tolist()
+    ids = torch.cat([torch.full((hi - lo,), v, dtype=i32) for lo, hi, v in zip([0] + cuts, cuts + [n], values)])
+    full = lambda m: torch.full((m,), -9, dtype=i32, device=gpu)  # noqa: E731
+    counts, offsets, order = full(8), full(9), full(n)
+    ws = torch.empty(moe.moe_sort_workspace_bytes(n, 8), dtype=torch.uint8, device=gpu)
+    moe.moe_sort_assignments(ids.to(gpu), 8, counts, offsets, order, ws)
+    want = ref.order(ids.numpy(), 8)
+    assert np.array_equal(counts.cpu().numpy(), want[0]) and np.array_equal(offsets.cpu().numpy(), want[1])
+    got = order.cpu().numpy()
+    assert np.array_equal(got[:len(want[2])], want[2]) and (got[len(want[2]):] == -9).all()
+
+
+@pytest.mark.gpu
 def test_sort_nothing(gpu):
     counts, offsets = torch.full((6,), 3, dtype=i32, device=gpu), torch.full((7,), 3, dtype=i32, device=gpu)
     empty = torch.empty(0, dtype=i32, device=gpu)
