@@ -201,9 +201,9 @@ __device__ __forceinline__ float select_weight(const SelectArgs& A, float l, flo
 //
 // Logits that bf16 holds are compared by their 16 bits, exactly.  Other scores are in fixed point, from float32
 // functions: they order nearly every row as float64 would.  Neighbours among the chosen that are closer than the scores'
-// error are put in order by float64; a row goes to select_exact where that does not settle it, where the last chosen
-// and the next, or the last group that stays and the next, are that close, where a lane ran out of sorted keys, and
-// where a logit is NaN or +inf.
+// error are put in order by float64, and so are the last chosen and the first left out; a row goes to select_exact where
+// that does not settle it, where a third one is that close to these two (on either side), where the last group that
+// stays and the next are that close, where a lane ran out of sorted keys, and where a logit is NaN or +inf.
 constexpr int kSelThreads = 256, kSelWaves = kSelThreads / 64;
 constexpr int kSelPart = 16;  // tokens that a workgroup of kSelThreads takes at once
 constexpr int kSelRuns = 8;     // a lane's sorted keys
@@ -567,7 +567,9 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
     // w: the other's.  One that is better takes the last one's place; what comes after it must not be near.
     if (edge && g == A.k - 1 && (w > v || (w == v && other < at))) v = w, at = other;
     const uint32_t head = key[0] == next ? key[1] : key[0], third = umax16(head);
-    open = open || (edge && ((third >= none && (last >> 9) - (third >> 9) < gap) || (full && head == 0)));
+    // Nor may another of the chosen be as near to it: which of the three goes is for float64 to say.
+    const bool another = g + 1 < A.k && (mine >> 9) - (next >> 9) < gap;
+    open = open || (edge && (another || (third >= none && (last >> 9) - (third >> 9) < gap) || (full && head == 0)));
     swap_pairs(v, at, A.k, false);
     swap_pairs(v, at, A.k, true);
     swap_pairs(v, at, A.k, false);

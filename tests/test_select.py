@@ -605,3 +605,36 @@ def test_same_choice_as_the_layers_router(gpu):
     assert torch.equal(s.ids, r["topk_ids"]) and torch.equal(s.counts, r["expert_counts"])
     assert torch.equal(s.offsets, r["expert_offsets"]) and torch.equal(s.order, r["sorted_assign"])
     assert (s.w - r["topk_weights"]).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("among", [1, 2])
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 8, 16])
+def test_three_close_around_the_last_place(gpu, k, among):
+    """Three experts a step of float32 apart, of which `among` are to be chosen, in any order, with all others far off."""
+    g = torch.Generator().manual_seed(100 * k + among)
+    T, E, above = 400, 64, max(0, k - among)
+    close = torch.tensor([1.0, 1.0 + 2.0 ** -23, 1.0 + 2.0 ** -22])
+    rows = torch.empty(T, E)
+    for t in range(T):
+        places = torch.randperm(E, generator=g)
+        rows[t, places[:above]] = 2 + torch.rand(above, generator=g)
+        rows[t, places[above:above + 3]] = close[torch.randperm(3, generator=g)]
+        rows[t, places[above + 3:]] = -torch.rand(E - above - 3, generator=g)
+    rows = rows.to(gpu)
+    for softmax in (True, False):
+        Select(rows, k, softmax).check()
+        Select(rows[:7].contiguous(), k, softmax).check()
+        # Of all groups but one, the same within them.
+        Select(rows, k, softmax, 4, 3, 1).check()
+    # Scores of a sigmoid that differ in their last bits, with a bias that is the same for the three.
+    near = rows.clone()
+    for v, l in zip(close.tolist(), (16.0, 16.125, 16.25)):
+        near[rows == v] = l
+    for dtype in (torch.float32, torch.bfloat16):
+        # The bias lifts the experts above the three by one.
+        l = near.to(dtype)
+        for t in range(0, 40):
+            bias = 0.25 + (rows[t] >= 2).float()
+            Select(l[t:t + 1].contiguous(), k, False, bias=bias).check()
+            Select(l[t:t + 1].contiguous(), k, True, bias=bias).check()
