@@ -414,8 +414,9 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
     offset = 600.f;
     gap = whole ? 0u : 8u;  // l - low, the product and the cut: two steps each, twice
   }
-  // A key below this is no expert: -inf, or past the run.  (-inf's own bits are the first below the finite ones'.)
-  const uint32_t none = whole ? 0x00810000u : 512u;
+  // A key below this is no expert: -inf, or past the run.  (By the values' own bits: the key of bf16's lowest value, which
+  // is an expert like any other; -inf's is the next below, 0x007F0000.)
+  const uint32_t none = whole ? 0x00800000u : 512u;
 
   // ---- keys, sorted; the largest two scores of the lane where groups are ranked ----
   uint32_t key[8];

@@ -638,3 +638,32 @@ def test_three_close_around_the_last_place(gpu, k, among):
             bias = 0.25 + (rows[t] >= 2).float()
             Select(l[t:t + 1].contiguous(), k, False, bias=bias).check()
             Select(l[t:t + 1].contiguous(), k, True, bias=bias).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("dtype,lowest", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.bfloat16),
+                                          (torch.float32, torch.float32)])
+@pytest.mark.parametrize("T", [6, 130])
+def test_masks_of_the_lowest_value(gpu, T, dtype, lowest, softmax):
+    """A logit of the type's lowest value is an expert like any other: chosen where there are no k better ones."""
+    logits, bias, _ = make(gpu, T, 48, torch.bfloat16, 12)
+    logits = logits.to(dtype)
+    low, inf = torch.finfo(lowest).min, float("inf")
+    logits[0] = low
+    logits[1::2, 4:] = low
+    logits[2::4, :46] = low
+    logits[3::4, 2] = -inf
+    logits[3::4, 20:] = -inf
+    some = (logits.float() > low).sum(1, keepdim=True)
+    for kw in (dict(), dict(renorm=False), dict(bias=bias), dict(groups=6, top_groups=3), dict(groups=6, top_groups=3, best=2),
+               dict(groups=6, top_groups=3, best=2, bias=bias)):
+        x = Select(logits, 8, softmax, **kw).check()
+        assert (x.ids >= 0).all()
+        if "bias" in kw or "groups" in kw:
+            continue
+        # Their scores are zeros, but where there are no others: those are the same for all.
+        place = torch.arange(8, device=gpu)
+        assert not x.w[(place >= some) & (some > 0)].any()
+        if not kw:
+            assert ((x.w[0] - 1 / 8).abs() <= 2.0 ** -24).all()
