@@ -245,8 +245,8 @@ __device__ __forceinline__ void merge8(uint32_t* a, const uint32_t* b) {
 }
 // What the bias asks of all rows of a call.
 struct BiasRange {
-  bool any, exact;  // it is there and not the same for every expert; it holds +inf (every row by select_exact)
-  // Keys of the scores with it: score * scale + offset, off by `step` a unit of the scores' error and by `same` besides.
+  bool any, exact;  // it is there and not the same for every expert; every row by select_exact
+  // Keys of the scores with it: score * scale + offset, off by `step` a unit of the scores' error.
   float scale, offset, far, step;
 };
 
@@ -262,14 +262,16 @@ __device__ __forceinline__ BiasRange bias_range(const SelectArgs& A) {
   }
   low = -wave_max_f32(-low);
   high = wave_max_f32(high);
-  r.exact = __ballot(inf) != 0;
   // The same finite bias everywhere changes no order.
   r.any = __ballot(odd) != 0 || low != high;
   if (!(low <= high)) low = high = 0.f;
-  // 512 at least and below 2^32.
-  r.scale = 4294000000.f / (1.f + (high - low));
-  r.offset = fmaf(-low, r.scale, 600.f);
   r.far = fmaxf(fabsf(low), fabsf(high));
+  // +inf, and biases so far from zero next to their range that float32 sums do not tell scores apart.
+  r.exact = __ballot(inf) != 0 || !(r.far < 1048576.f * (1.f + (high - low)));
+  // 512 at least: the offset is off by half a step of low * scale or of what is added to it, and a sum in float32 is never
+  // below its bias.  Keys beyond 2^32 are cut off there, which brings none nearer to another than `gap` unless they are.
+  r.scale = 4294000000.f / (1.f + (high - low));
+  r.offset = fmaf(-low, r.scale, fmaf(1.2e-7f * r.far, r.scale, 600.f));
   r.step = 2.f / 512 * r.scale;
   return r;
 }

@@ -667,3 +667,23 @@ def test_masks_of_the_lowest_value(gpu, T, dtype, lowest, softmax):
         assert not x.w[(place >= some) & (some > 0)].any()
         if not kw:
             assert ((x.w[0] - 1 / 8).abs() <= 2.0 ** -24).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("lo,hi", [(-3.0, -2.9), (-5.0, -4.8), (-100.0, -99.0), (2.9, 3.1), (1.0, 1.2), (0.5, 0.51), (99.0, 100.0),
+                                   (1000.0, 1001.0), (-1e6, 1 - 1e6), (1e9, 1.1e9), (-3e38, 3e38), (1e-30, 2e-30)])
+def test_biases_far_from_zero(gpu, lo, hi, softmax):
+    """Scores too small to change their sum with the bias, where every expert is to be chosen, or some of them."""
+    g = torch.Generator().manual_seed(3)
+    for T in (5, 150):
+        for E, k in ((16, 16), (64, 16), (16, 5)):
+            logits = -17 - 8 * torch.rand(T, E, generator=g)
+            logits[torch.arange(T), torch.randint(0, E, (T,), generator=g)] = 1.0
+            bias = (torch.rand(E, generator=g).double() * (hi - lo) + lo).float()
+            bias[E // 2] = lo
+            bias, logits = bias.to(gpu), logits.to(gpu)
+            for kw in (dict(), dict(groups=4, top_groups=4)) + ((dict(groups=4, top_groups=2, best=2),) if k != 16 or E == 64 else ()):
+                for dtype in (torch.float32, torch.bfloat16):
+                    x = Select(logits.to(dtype), k, softmax, bias=bias, **kw).check()
+                    assert (x.ids >= 0).all()
