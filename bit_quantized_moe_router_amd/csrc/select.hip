@@ -245,7 +245,7 @@ __device__ __forceinline__ void merge8(uint32_t* a, const uint32_t* b) {
 }
 // What the bias asks of all rows of a call.
 struct BiasRange {
-  bool any, exact;  // it is there and not the same for every expert; every row by select_exact
+  bool exact;  // every row by select_exact
   // Keys of the scores with it: score * scale + offset, off by `step` a unit of the scores' error.
   float scale, offset, far, step;
 };
@@ -254,16 +254,14 @@ __device__ __forceinline__ BiasRange bias_range(const SelectArgs& A) {
   BiasRange r{};
   if (!A.bias) return r;
   float low = INFINITY, high = -INFINITY;
-  bool odd = false, inf = false;
+  bool inf = false;
   for (int e = threadIdx.x & 63; e < A.E; e += 64) {
     const float b = A.bias[e];
     if (b > -INFINITY && b < INFINITY) low = fminf(low, b), high = fmaxf(high, b);
-    else odd = true, inf = inf || b == INFINITY;
+    else inf = inf || b == INFINITY;
   }
   low = -wave_max_f32(-low);
   high = wave_max_f32(high);
-  // The same finite bias everywhere changes no order.
-  r.any = __ballot(odd) != 0 || low != high;
   if (!(low <= high)) low = high = 0.f;
   r.far = fmaxf(fabsf(low), fabsf(high));
   // +inf, and biases so far from zero next to their range that float32 sums do not tell scores apart.
@@ -639,7 +637,7 @@ __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, in
     const BiasRange B = bias_range(A);
     const SelectLane L = select_lane(A);
     // The lanes' biases, four at a time: number j of lane g at (j / 4 * 16 + g) * 4 + j % 4.
-    if (By != kByLogit && B.any) {
+    if (By != kByLogit && A.bias) {
       for (int i = threadIdx.x; i < 16 * kSelMaxRun; i += 64 * waves) {
         const int g = i / 4 % 16, j = i / 64 * 4 + i % 4;
         const int group = g / A.lanes, at = (g - group * A.lanes) * A.run + j;
@@ -668,7 +666,8 @@ __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, in
         }
       }
     };
-    if (By != kByLogit && B.any) go(std::integral_constant<bool, By != kByLogit>{});
+    // One bias for all decides as well: of sums that are equal in float64, and of groups that have one expert left.
+    if (By != kByLogit && A.bias) go(std::integral_constant<bool, By != kByLogit>{});
     else go(std::false_type{});
   }
 }

@@ -687,3 +687,26 @@ def test_biases_far_from_zero(gpu, lo, hi, softmax):
                 for dtype in (torch.float32, torch.bfloat16):
                     x = Select(logits.to(dtype), k, softmax, bias=bias, **kw).check()
                     assert (x.ids >= 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("value", [0.0, 0.5, -3.0, 1.0, 1e10])
+def test_one_bias_for_all(gpu, value, softmax):
+    """The choice is that of the float64 sums: scores that do not differ in them are equal, whatever their logits."""
+    logits, _, _ = make(gpu, 60, 20, torch.float32, 6)
+    logits[::3] -= 300
+    logits[1::3] += 60
+    logits[2::3, 4] += 80
+    for T in (60, 3):
+        for dtype in (torch.float32, torch.bfloat16):
+            l = logits[:T].to(dtype)
+            bias = torch.full((20,), value, device=gpu)
+            Select(l, 4, softmax, bias=bias).check()
+            Select(l, 4, softmax, 5, 2, 2, bias=bias).check()
+    # Groups that have one expert left: their sum has the bias once.
+    few = torch.randn(60, 8, generator=torch.Generator().manual_seed(1)).to(gpu)
+    few[:, 1] = -float("inf")
+    few[::2, 4] = -float("inf")
+    for T in (60, 3):
+        Select(few[:T].contiguous(), 2, softmax, 4, 2, 2, bias=torch.full((8,), value, device=gpu)).check()
