@@ -910,7 +910,6 @@ __global__ __launch_bounds__(kSelThreads) void k_select_grad(SelectArgs A) {
   float* row = s_row[wave];
   for (int i = lane; i < kMaxE; i += 64) row[i] = 0.f;
   const bool dense = A.softmax && !A.renorm, in_place = A.base && A.base == A.dlogits;
-  const float inv_scale = 1.f / A.scale;
   for (int64_t t = (int64_t)blockIdx.x * kSelWaves + wave; t < A.T; t += (int64_t)gridDim.x * kSelWaves) {
     int id = -1;
     float w = 0.f, dw = 0.f;
@@ -945,7 +944,7 @@ __global__ __launch_bounds__(kSelThreads) void k_select_grad(SelectArgs A) {
     const float D = sum16(id >= 0 ? dw * w : 0.f);
     float d = 0.f;
     if (id >= 0) {
-      d = w * (A.renorm ? dw - D * inv_scale : dw);
+      d = w * (A.renorm ? dw - D / A.scale : dw);  // a scale's reciprocal may be beyond float32
       if (!A.softmax) {
         const float v = logit_at<F32>(A.logits, t * A.E + id);  // 1 - s = 1 / (1 + e^l)
         d *= v >= 0.f ? expf(-v) / (1.f + expf(-v)) : 1.f / (1.f + expf(v));

@@ -710,3 +710,20 @@ def test_one_bias_for_all(gpu, value, softmax):
     few[::2, 4] = -float("inf")
     for T in (60, 3):
         Select(few[:T].contiguous(), 2, softmax, 4, 2, 2, bias=torch.full((8,), value, device=gpu)).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("scale", [1e-39, -3e-40, 1e30])
+def test_gradient_of_extreme_scales(gpu, scale, softmax):
+    """A scale whose reciprocal float32 does not hold."""
+    logits, _, _ = make(gpu, 100, 24, torch.float32, 15)
+    x = Select(logits, 5, softmax, scale=scale)
+    x.forward()
+    x.dw /= abs(x.desc.scale) * 64  # gradients near 1
+    x.backward()
+    n = lambda t: t.double().cpu().numpy()  # noqa: E731
+    # For the weights as they were written: subnormal ones hold few bits.
+    want, size = ref.select_gradient(n(logits), x.ids.cpu().numpy(), n(x.w), n(x.dw), softmax, True, x.desc.scale)
+    # Five products and their sum, a quotient, a difference and a product; 1 - s by an exponential of an argument below 8.
+    assert (np.abs(n(x.d) - want) <= 64 * ref.U * size + 1e-37).all()
