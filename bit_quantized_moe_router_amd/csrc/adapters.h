@@ -17,8 +17,8 @@
 // dimension lies in memory, and where it is the strided one a lane reads a run
 // of each of its 8 rows and turns the 8 x 8 numbers around in registers.
 //
-// fp32 numbers enter the bf16 instructions as two or three parts of 8 bits
-// each, whose products are exact and summed in fp32: three hold all 24 bits.
+// fp32 numbers enter the bf16 instructions as three parts of 8 bits each, which
+// hold all 24; their products are exact and summed in fp32.
 #pragma once
 
 #include "launch.h"
@@ -26,17 +26,15 @@
 
 namespace moe {
 
-// Part of an fp32 number: the leading 8 bits of its significand, cut off, so
-// that what is left is exact and no part overflows; the last of two parts is
-// rounded instead (the pair then holds 16 to 17 bits).  An infinity or NaN is all in
-// its first part.
-template <int Parts>
-__device__ __forceinline__ void split_parts(float v, uint32_t part[Parts]) {
+// The parts of an fp32 number: each the leading 8 bits of the significand of
+// what is left, cut off, so that the next rest is exact and no part overflows.
+// An infinity or NaN is all in its first part.
+constexpr int kParts = 3;
+__device__ __forceinline__ void split_parts(float v, uint32_t part[kParts]) {
   const bool finite = f32_abs_bits(v) < 0x7F800000u;
 #pragma unroll
-  for (int p = 0; p < Parts; p++) {
-    const bool last = p == Parts - 1 && Parts == 2;
-    part[p] = last ? f32_to_bf16_bits(v) : __float_as_uint(v) >> 16;
+  for (int p = 0; p < kParts; p++) {
+    part[p] = __float_as_uint(v) >> 16;
     v = finite ? v - __uint_as_float(part[p] << 16) : 0.f;
   }
 }
@@ -77,7 +75,7 @@ __device__ __forceinline__ int adapter_dst(const AdapterArgs& A, int i) {
 
 // The weight gradients' thin operands, for 32 positions at a time (from a multiple of 32) and every rank (padded): three
 // parts of 32 numbers each, so that a lane reads the 8 positions of an operand at once.
-constexpr int kThinRank = 3 * 32;
+constexpr int kThinRank = kParts * 32;
 
 // Eight numbers of a row that has n of them left (Even: all or none), as the
 // parts that enter the matrix instructions.
@@ -114,9 +112,7 @@ __device__ __forceinline__ RowPiece<F32, 8> piece8(const void* row, int64_t at, 
 template <bool Back, bool YF32, int RT, int NR, int W, bool Even>
 __global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int splits) {
   constexpr int BT = 16 * RT, R = 16 * NR, H = W / 2;
-  constexpr int kParts = !Back && YF32 ? 3 : 2;         // of the numbers between, for the rows written
   constexpr bool kWideF32 = Back && YF32;               // the wide rows read are fp32
-  constexpr int kInParts = kWideF32 ? 3 : 1;
   constexpr int kU = RT + NR <= 2 ? 8 : RT + NR <= 5 ? 4 : 2;  // steps of 32 columns in flight
   constexpr int kRow = R + 8;                           // numbers between two rows of a part in LDS
   __shared__ float s_sum[H][BT][R + 1];
@@ -202,17 +198,17 @@ __global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int spl
             const auto& p = x[u][i].w;
             acc[i][f] = mfma_bf16(wv, as_bf16x8(p[0], p[1], p[2], p[3]), acc[i][f]);
           } else {
-            uint32_t d[kInParts][4];
+            uint32_t d[kParts][4];
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-              uint32_t part[kInParts];
-              split_parts<kInParts>(x[u][i].get(j), part);
+              uint32_t part[kParts];
+              split_parts(x[u][i].get(j), part);
 #pragma unroll
-              for (int p = 0; p < kInParts; p++) d[p][j / 2] = j & 1 ? d[p][j / 2] | part[p] << 16 : part[p];
+              for (int p = 0; p < kParts; p++) d[p][j / 2] = j & 1 ? d[p][j / 2] | part[p] << 16 : part[p];
             }
             // Small parts first.
 #pragma unroll
-            for (int p = kInParts - 1; p >= 0; p--)
+            for (int p = kParts - 1; p >= 0; p--)
               acc[i][f] = mfma_bf16(wv, as_bf16x8(d[p][0], d[p][1], d[p][2], d[p][3]), acc[i][f]);
           }
         }
@@ -252,7 +248,7 @@ __global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int spl
     const float sv = scale * v;
     if (!Back && A.h_out && split == 0 && p < t.rows && c < r) A.h_out[(int64_t)(t.row + p) * r + c] = v;  // without the scale
     uint32_t part[kParts];
-    split_parts<kParts>(sv, part);
+    split_parts(sv, part);
 #pragma unroll
     for (int s = 0; s < kParts; s++) s_part[s][p][c] = (uint16_t)part[s];
     if constexpr (Back) s_sum[0][p][c] = sv;
@@ -265,13 +261,13 @@ __global__ __launch_bounds__(64 * W) void k_adapters_rows(AdapterArgs A, int spl
       if (p >= t.rows) continue;
       const int64_t pos = t.row + p;
       uint16_t* to = A.thin + ((pos >> 5) * R + c) * kThinRank + (pos & 31);
-      uint32_t part[3];
-      split_parts<3>(s_sum[0][p][c], part);
+      uint32_t part[kParts];
+      split_parts(s_sum[0][p][c], part);
 #pragma unroll
-      for (int s = 0; s < 3; s++) to[32 * s] = (uint16_t)part[s];
-      split_parts<3>(c < r ? A.h[pos * r + c] : 0.f, part);
+      for (int s = 0; s < kParts; s++) to[32 * s] = (uint16_t)part[s];
+      split_parts(c < r ? A.h[pos * r + c] : 0.f, part);
 #pragma unroll
-      for (int s = 0; s < 3; s++) to[A.thin_h + 32 * s] = (uint16_t)part[s];
+      for (int s = 0; s < kParts; s++) to[A.thin_h + 32 * s] = (uint16_t)part[s];
     }
   }
 

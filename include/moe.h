@@ -568,10 +568,9 @@ typedef struct {
  * Any alignment of the types; n_in and n_out that are multiples of 8 with
  * 16-byte aligned rows are faster.  A src(i) outside x counts as a row of
  * zeros, a dst(i) outside y is not written.  y overlaps no input but base.
- * Products are exact and their sums float32; A x enters the second product
- * split into bf16 parts that hold 17 bits of it for a bf16 y and 24 for a
- * float32 one; y is rounded once.  Repeated calls give identical bits.  No
- * workspace.
+ * Products are exact and their sums float32; scales[a] A x is rounded to
+ * float32 before it enters the second product; y is rounded once.  Repeated
+ * calls give identical bits.  No workspace.
  */
 moe_status moe_adapters_forward(const moe_adapter_desc *desc, const uint16_t *a, const uint16_t *b, const float *scales,
                                 const uint16_t *x, int32_t x_rows, const int32_t *offsets, int32_t rows,
@@ -595,7 +594,9 @@ moe_status moe_adapters_forward(const moe_adapter_desc *desc, const uint16_t *a,
  *   da, db  may be NULL both; written for every adapter, zeros for one without rows
  *   ws    moe_adapters_workspace_bytes(desc, rows) bytes, 16-byte aligned, not
  *         shared by calls that overlap in time
- * dy and h with an index outside count as zeros.  Sums are float32.
+ * dy and h with an index outside count as zeros.  Products are exact and their
+ * sums float32 (da and db without products below 2^-24 of the leading one of
+ * two float32 numbers); dh is rounded to float32, dx once.
  */
 moe_status moe_adapters_workspace_bytes(const moe_adapter_desc *desc, int32_t rows, size_t *bytes);
 moe_status moe_adapters_backward(const moe_adapter_desc *desc, const uint16_t *a, const uint16_t *b, const float *scales,

@@ -498,3 +498,45 @@ def test_operators_together(gpu):
                            (db.double().cpu(), B.grad, 2.0 ** -16), (dxt.double().cpu(), X.grad, 2.0 ** -7),
                            (dlogits.double().cpu(), L.grad, 2.0 ** -7)):
         assert (got - grad).norm() <= tol * grad.norm(), (tol, (got - grad).norm() / grad.norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("out", [f32, bf16])
+@pytest.mark.parametrize("r,K,N", [(2, 3, 5), (16, 64, 64), (16, 33, 20), (24, 40, 72), (32, 64, 128), (50, 77, 131), (64, 72, 40),
+                                   (128, 64, 200)])
+def test_numbers_between_hold_24_bits(gpu, r, K, N, out):
+    """Whole numbers of 21 bits between the products, in pairs whose differences are the results: exact in every sum."""
+    x = Adapters(gpu, [20, 0, 30], r, K, N, out, 13, base=False, scales=False)
+    g = torch.Generator().manual_seed(r)
+
+    def wide(rows, cols):
+        m = torch.zeros(rows, cols)
+        m[:, :3] = torch.randint(0, 128, (rows, 3), generator=g) * torch.tensor([2.0 ** 14, 2.0 ** 7, 1.0])
+        return m, m[:, 2:3].double()
+
+    def pairs(cols):  # column c takes one pair's difference
+        m = torch.zeros(cols, r)
+        pair = 2 * (torch.arange(cols) % (r // 2))
+        sign = (torch.randint(0, 2, (cols,), generator=g) * 2 - 1).float()
+        m[torch.arange(cols), pair], m[torch.arange(cols), pair + 1] = sign, -sign
+        return m, sign.double()
+
+    takes = torch.zeros(r, 3)  # of the even ranks all three numbers, of the odd ones the first two
+    takes[:, :2] = 1
+    takes[0:r // 2 * 2:2, 2] = 1
+    xs, last = wide(len(x.x), K)
+    back, sign = pairs(N)
+    x.x.copy_(xs)
+    x.a.zero_()
+    x.a[:, :, :3] = takes.to(bf16).to(gpu)
+    x.b.copy_(back.to(bf16).to(gpu).expand_as(x.b))
+    x.forward()
+    assert torch.equal(x.y.double().cpu(), last * sign)
+    dys, last = wide(len(x.dy), N)
+    fore, sign = pairs(K)
+    x.dy.copy_(dys)
+    x.b.zero_()
+    x.b[:, :3] = takes.t().to(bf16).to(gpu)
+    x.a.copy_(fore.t().to(bf16).to(gpu).expand_as(x.a))
+    x.backward()
+    assert torch.equal(x.dx.double().cpu(), last * sign)
