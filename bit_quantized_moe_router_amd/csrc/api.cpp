@@ -1239,6 +1239,11 @@ moe_status moe_adapters_workspace_bytes(const moe_adapter_desc* d, int32_t rows,
   return MOE_OK;
 }
 
+static bool overlap(const void* p, int64_t p_bytes, const void* q, int64_t q_bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + (uint64_t)q_bytes && b < a + (uint64_t)p_bytes;
+}
+
 moe_status moe_adapters_backward(const moe_adapter_desc* d, const uint16_t* a, const uint16_t* b, const float* scales,
                                  const uint16_t* x, int32_t x_rows, const float* h, const void* dy, int32_t y_rows,
                                  const int32_t* offsets, int32_t rows, const int32_t* src_rows, int32_t src_div,
@@ -1258,6 +1263,16 @@ moe_status moe_adapters_backward(const moe_adapter_desc* d, const uint16_t* a, c
     size_t need = 0;
     TRY(moe_adapters_workspace_bytes(d, rows, &need));
     if (da) TRY(sort_ws(need, ws, ws_bytes));
+    // dx is written while other workgroups still read dy, and before the factors' gradients read x and dy.
+    const int64_t row = (int64_t)d->n_in * 2;
+    if (dx) {
+      const int64_t dx_rows = (int64_t)x_rows * A.src_div, y_size = d->y_type == MOE_F32 ? 4 : 2;
+      const int64_t dx_bytes = (dx_rows < 0x7FFFFFFF ? dx_rows : 0x7FFFFFFF) * row;  // rows that an int32 names
+      if (overlap(dx, dx_bytes, dy, (int64_t)y_rows * d->n_out * y_size))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dx must not overlap dy");
+      if (da && overlap(dx, dx_bytes, x, x_rows * row))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dx must not overlap x where da and db are asked for");
+    }
   } else {
     if (!da) return MOE_OK;
     if (!offsets) return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer argument");

@@ -590,7 +590,8 @@ moe_status moe_adapters_forward(const moe_adapter_desc *desc, const uint16_t *a,
  *   h     as the forward call wrote it
  *   base  of dx, bf16, or NULL: zeros; may be dx
  *   dx    may be NULL, with base; rows of no position stay as they were; src_rows
- *         then names each row at most once
+ *         then names each row at most once.  Overlaps no input but base, and x
+ *         where da and db are NULL; over dy, or over x with da and db, it is refused
  *   da, db  may be NULL both; written for every adapter, zeros for one without rows
  *   ws    moe_adapters_workspace_bytes(desc, rows) bytes, 16-byte aligned, not
  *         shared by calls that overlap in time

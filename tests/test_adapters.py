@@ -540,3 +540,28 @@ def test_numbers_between_hold_24_bits(gpu, r, K, N, out):
     x.a.copy_(fore.t().to(bf16).to(gpu).expand_as(x.a))
     x.backward()
     assert torch.equal(x.dx.double().cpu(), last * sign)
+
+
+@pytest.mark.parametrize("where", ["dy", "x", "dy_end", "x_end", "both"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_overlapping_gradient_is_refused(where, gather):
+    """dx over dy, and over x where the factors' gradients read it later; by its last or its first bytes alone too."""
+    L, K, N, rows, div = moe.lib(), 24, 40, 16, 2 if gather else 1
+    d = moe.make_adapter_desc(4, 8, K, N, moe.MOE_F32)
+    x, dy, dx = 1 << 20, 2 << 20, 3 << 20
+    x_bytes, dy_bytes, dx_bytes = rows * K * 2, rows * N * 4, rows * div * K * 2
+    at = {"dy": dy, "x": x, "dy_end": dy + dy_bytes - 2, "x_end": x - dx_bytes + 2, "both": dy + dy_bytes // 2}[where]
+
+    def call(dx, da):
+        return L.moe_adapters_backward(d, P, P, None, x, rows, P, dy, rows, P, rows, P if gather else None, div, None, None, dx,
+                                       P if da else None, P if da else None, P, 1 << 20, None)
+
+    assert call(at, True) == 1 and b"overlap" in L.moe_last_error()
+    if where not in ("x", "x_end"):
+        assert call(at, False) == 1 and b"overlap" in L.moe_last_error()
+    if torch.cuda.is_available():
+        return  # what is not refused would run
+    # Next to them, and over x alone where nothing reads it later: refused for want of a device only.
+    for at in (dx, dy + dy_bytes, dy - dx_bytes, x + x_bytes, x - dx_bytes):
+        assert call(at, True) != 1
+    assert call(x, False) != 1
