@@ -727,3 +727,15 @@ def test_gradient_of_extreme_scales(gpu, scale, softmax):
     want, size = ref.select_gradient(n(logits), x.ids.cpu().numpy(), n(x.w), n(x.dw), softmax, True, x.desc.scale)
     # Five products and their sum, a quotient, a difference and a product; 1 - s by an exponential of an argument below 8.
     assert (np.abs(n(x.d) - want) <= 64 * ref.U * size + 1e-37).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,n,top,k", GROUPS)
+def test_groups_of_sigmoid_sums(gpu, T, E, n, top, k, dtype):
+    """Ranked by sums of two sigmoid scores without a bias; logits of one sign, as sums for x and -x are all 1."""
+    logits, _, valid = make(gpu, T, E, torch.float32, T + E)
+    for sign in (1, -1):
+        l = (sign * logits.abs()).to(dtype)
+        Select(l, k, False, n, top, 2, valid=valid).check()
+        Select(l, k, False, n, top, 2, renorm=False, scale=2.5).check()
