@@ -387,7 +387,8 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
     });
     total = sum16(total);
   }
-  const float inv = By == kBySoftmax ? __builtin_amdgcn_rcpf(total) : 1.f;
+  // One lane's for the whole row: the lanes' sums differ in their order, and equal logits are to have equal scores.
+  const float inv = By == kBySoftmax ? __shfl(__builtin_amdgcn_rcpf(total), lane & 48) : 1.f;
   // Errors of float32 scores, absolute.  Sigmoid: with t = l log2 e off by 2^-23.4 |t| and one step each of exp2, the sum and
   // the reciprocal, s is off by s (1 - s) (|l| 2^-23.4 + 2^-23) + s 1.5 2^-23 < 2^-22.  Softmax: s (2 |l - top| +
   // terms a lane + 24) 2^-24, of which the sum's terms, |l - top| < 7 on their average, have 18; s |l - top| < 0.4 / total
@@ -543,44 +544,63 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
   const uint32_t next = umax16(key[0]);
   const uint32_t after = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0x101, 0xF, 0xF, true);  // lane g + 1's
   const bool chosen = row && mine >= none;
-  const bool edge = row && last >= none && next >= none && (last >> 9) - (next >> 9) < gap;
+  bool edge = row && last >= none && next >= none && (last >> 9) - (next >> 9) < gap;
   const int from_e0 = __shfl(L.e0, (lane & 48) + 15 - (int)(mine >> 5 & 15u));
   int id = chosen ? from_e0 + 31 - (int)(mine & 31u) : -1;
   float lc = id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY;
-  const bool close = chosen && g + 1 < A.k && after >= none && (mine >> 9) - (after >> 9) < gap;
-  if (By == kBySoftmax && Biased) {
-    open = open || close || edge;  // the softmax's sum is float32
-  } else if (__ballot(close || edge)) {
-    // Those next to each other, and the last and the first that was not chosen, by what they are compared by.
+  bool close = chosen && g + 1 < A.k && after >= none && (mine >> 9) - (after >> 9) < gap;
+  if (__ballot(close || edge)) {
     const int next_e0 = __shfl(L.e0, (lane & 48) + 15 - (int)(next >> 5 & 15u));
-    int at = id >= 0 ? id : 0x7FFFFFFF, other = edge ? next_e0 + 31 - (int)(next & 31u) : -1;
-    double v = -INFINITY, w = -INFINITY;
-#pragma unroll 1
-    for (int pass = 0; pass < 2; pass++) {
-      const int e = pass == 0 ? other : id;
-      w = v;
-      v = -INFINITY;
-      if (e >= 0) {
-        v = (double)logit_at<F32>(A.logits, t * A.E + e);
-        if (Biased) v = 1.0 / (1.0 + exp(-v)) + (double)A.bias[e];
-      }
-    }
-    // w: the other's.  One that is better takes the last one's place; what comes after it must not be near.
-    if (edge && g == A.k - 1 && (w > v || (w == v && other < at))) v = w, at = other;
+    const int next_id = edge ? next_e0 + 31 - (int)(next & 31u) : -1;
+    // The largest of what is left after the first one left out.
     const uint32_t head = key[0] == next ? key[1] : key[0], third = umax16(head);
-    // Nor may another of the chosen be as near to it: which of the three goes is for float64 to say.
-    const bool another = g + 1 < A.k && (mine >> 9) - (next >> 9) < gap;
-    open = open || (edge && (another || (third >= none && (last >> 9) - (third >> 9) < gap) || (full && head == 0)));
-    swap_pairs(v, at, A.k, false);
-    swap_pairs(v, at, A.k, true);
-    swap_pairs(v, at, A.k, false);
-    w = __shfl(v, (lane & 48) + ((g + 1) & 15));
-    const int wat = __shfl(at, (lane & 48) + ((g + 1) & 15));
-    open = open || (g + 1 < A.k && wat != 0x7FFFFFFF && !(v > w || (v == w && at < wat)));
-    const int now = at != 0x7FFFFFFF ? at : -1;
-    if (now != id) {
-      id = now;
-      lc = id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY;
+    const bool third_near = edge && ((third >= none && (last >> 9) - (third >> 9) < gap) || (full && head == 0));
+    // A chosen one that is near to the first left out.
+    const bool near = edge && chosen && (mine >> 9) - (next >> 9) < gap;
+    if constexpr (Biased) {
+      // Equal logits with equal biases are the same sum and have the same key: the lower index comes first already.  In
+      // bf16 beside a bias that is the same for many they are common (65536 tokens of 256 experts, bias 0, by float64 and
+      // by this: softmax 119, 45 us, sigmoid 47, 43; 512 in 8 groups, sigmoid 101, 86).
+      const float bc = id >= 0 ? A.bias[id] : 0.f;
+      const float l1 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(lc), 0x101, 0xF, 0xF, true));
+      const float b1 = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(bc), 0x101, 0xF, 0xF, true));
+      close = close && !(lc == l1 && bc == b1);
+      // The last place is settled if all that are near to it are one such sum.
+      const float ln = edge ? logit_at<F32>(A.logits, t * A.E + next_id) : 0.f, bn = edge ? A.bias[next_id] : 0.f;
+      const uint64_t unlike = __ballot(third_near || (near && !(lc == ln && bc == bn)));
+      edge = edge && ((unlike >> (lane & 48)) & 0xFFFFu) != 0;
+    }
+    if (By == kBySoftmax && Biased) {
+      open = open || close || edge;  // the softmax's sum is float32
+    } else if (__ballot(close || edge)) {
+      // Those next to each other, and the last and the first that was not chosen, by what they are compared by.
+      int at = id >= 0 ? id : 0x7FFFFFFF, other = edge ? next_id : -1;
+      double v = -INFINITY, w = -INFINITY;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; pass++) {
+        const int e = pass == 0 ? other : id;
+        w = v;
+        v = -INFINITY;
+        if (e >= 0) {
+          v = (double)logit_at<F32>(A.logits, t * A.E + e);
+          if (Biased) v = 1.0 / (1.0 + exp(-v)) + (double)A.bias[e];
+        }
+      }
+      // w: the other's.  One that is better takes the last one's place.  What comes after it must not be near, nor a second
+      // one of the chosen: which of the three goes is for float64 to say.
+      if (edge && g == A.k - 1 && (w > v || (w == v && other < at))) v = w, at = other;
+      open = open || (edge && (third_near || (near && g + 1 < A.k)));
+      swap_pairs(v, at, A.k, false);
+      swap_pairs(v, at, A.k, true);
+      swap_pairs(v, at, A.k, false);
+      w = __shfl(v, (lane & 48) + ((g + 1) & 15));
+      const int wat = __shfl(at, (lane & 48) + ((g + 1) & 15));
+      open = open || (g + 1 < A.k && wat != 0x7FFFFFFF && !(v > w || (v == w && at < wat)));
+      const int now = at != 0x7FFFFFFF ? at : -1;
+      if (now != id) {
+        id = now;
+        lc = id >= 0 ? logit_at<F32>(A.logits, t * A.E + id) : -INFINITY;
+      }
     }
   }
   // Bit 16 r + ..: row r is left open, and written by select_one.

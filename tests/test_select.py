@@ -739,3 +739,20 @@ def test_groups_of_sigmoid_sums(gpu, T, E, n, top, k, dtype):
         l = (sign * logits.abs()).to(dtype)
         Select(l, k, False, n, top, 2, valid=valid).check()
         Select(l, k, False, n, top, 2, renorm=False, scale=2.5).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("T", [40, 700])
+def test_equal_sums_beside_close_ones(gpu, T, softmax):
+    """Equal logits with equal biases, two of them or many around the last place, among others as close as float32 tells."""
+    g = torch.Generator().manual_seed(T)
+    for dtype in (torch.float32, torch.bfloat16):
+        for E, k in ((32, 6), (96, 16), (256, 8)):
+            few = torch.randint(0, 24, (T, E), generator=g).float() * 0.25
+            few[T // 2:] += 13  # a sigmoid's last bits
+            few[::3] += (torch.rand(len(few[::3]), E, generator=g) < 0.1) * 2.0 ** -20
+            for bias in (torch.zeros(E), torch.full((E,), 0.5), 0.25 * torch.randint(0, 2, (E,), generator=g).float()):
+                l, b = few.to(dtype).to(gpu), bias.to(gpu)
+                Select(l, k, softmax, bias=b).check()
+                Select(l, k, softmax, 4, 2, 1, bias=b).check()
