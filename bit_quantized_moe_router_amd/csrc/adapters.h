@@ -105,8 +105,9 @@ __device__ __forceinline__ RowPiece<F32, 8> piece8(const void* row, int64_t at, 
 // waves -> B (one row of rank 16, 2048 -> 2048, 7.5 us); in large ones by the bytes,
 // but a workgroup first only reads, then mostly writes, and a compute unit holds too
 // few of them to overlap the two throughout: 4096 rows of rank 16, 4096 -> 4096,
-// 36 us, 3.2 TB/s; 32768 rows of 256 adapters of rank 16, 2048 -> 1024, 79 us forward
-// (5.0 TB/s of what it moves, 325 MB read) and 74 backward (4.6 TB/s).  Consecutive
+// 37 us, 3.2 TB/s; 32768 rows of 256 adapters of rank 16, 2048 -> 1024, 80 us forward
+// (4.9 TB/s of what it moves, 325 MB read) and 74 backward (4.6 TB/s).  The third part of
+// the numbers between costs 0.3 to 0.6 us of these.  Consecutive
 // tiles on one XCD, so that an adapter's factors reach fewer caches, won 1 to 2 %.
 // ---------------------------------------------------------------------------
 template <bool Back, bool YF32, int RT, int NR, int W, bool Even>

@@ -197,7 +197,7 @@ __device__ __forceinline__ float select_weight(const SelectArgs& A, float l, flo
 // lane sorts its keys down to its eight largest; k times the largest head of the 16 lanes is taken and its lane moves
 // up.  Bound by the instructions: about 1400 for four tokens of 512 experts with k = 16, a third of them the scores (an
 // exponential and a reciprocal each, four times a plain instruction's time), a third the sort and the rounds.  65536
-// such tokens in 8 groups take 72 us (bf16, 67 MB read, 12 written); a wave a token, in float64, 1470.
+// such tokens in 8 groups take 68 to 71 us (bf16, 67 MB read, 12 written).
 //
 // Logits that bf16 holds are compared by their 16 bits, exactly.  Other scores are in fixed point, from float32
 // functions: they order nearly every row as float64 would.  Neighbours among the chosen that are closer than the scores'
@@ -617,8 +617,8 @@ __device__ __forceinline__ uint64_t select_four(const SelectArgs& A, int64_t t0,
   return todo;
 }
 
-// One token a wave: rows that the 16-lane form leaves open or has no lanes for (more than 16 groups, or groups too wide
-// for their lanes).
+// One token a wave: rows that the 16-lane form leaves open or has no lanes for (more than 16 groups, or more than 32 experts a
+// lane: 486 experts in 3 groups 370 us for 65536 tokens, 480 in 3 groups 73).
 template <bool F32>
 __device__ __forceinline__ void select_one(const SelectArgs& A, int64_t t, SelectLds& lds, int* s_count, int* s_ids) {
   const int lane = threadIdx.x & 63;
@@ -693,9 +693,11 @@ __device__ __forceinline__ void select_range(const SelectArgs& A, int64_t t0, in
 }
 
 // Part b: tokens b * per_part .. ; its counts by expert go to the workspace.
-// Bound by the instructions of select_four, some 1400 for 4 tokens of 512 experts in 8 groups, with few waves a SIMD as the
-// registers of select_one's rare turns count for all: 65536 such tokens (bf16, 16 places) 68 to 71 us, 1.1 TB/s; 4096 tokens of
-// 256 experts fp32 7.2 us.  One token in float64 for all of them, the first form, took 1400 us for the former.
+// Bound by the instructions of select_four, some 1400 for 4 tokens of 512 experts in 8 groups, with few waves a SIMD: there are
+// no more parts than compute units, and the registers of select_one's rare turns count for all (the 1024-thread forms with
+// scores are held to 128 and spill 28 to 40 bytes a lane).  65536 such tokens (bf16, 16 places) 68 to 71 us, 1.1 TB/s; 4096
+// tokens of 256 experts fp32 7.3 us.  A wave a token in float64 (kByOne: 32 groups) takes 386 us for the former, rows that are
+// all left open 414.
 template <bool F32, int By, int NT>
 __global__ __launch_bounds__(NT) void k_select(SelectArgs A) {
   __shared__ SelectLds lds[NT / 64];

@@ -463,12 +463,13 @@ typedef struct {
  *   valid   [T] uint8, 0 for a padding token, or NULL: all are valid
  *   ws      moe_select_workspace_bytes(T, E, k) bytes, 16-byte aligned
  * The choice is that of c in float64 (c, the groups' sums and the softmax's
- * sum are float64 wherever float32 leaves it open); without a bias experts are
- * compared by their logits.  Weights are float32.  An expert whose logit is
+ * sum are float64 wherever float32 leaves it open); without a bias (NULL)
+ * experts are compared by their logits.  Weights are float32.  An expert whose logit is
  * -inf, or whose bias is -inf or NaN, is never chosen; a token with fewer than
  * k others has id -1 and weight 0 in the remaining places, a padding token in
  * all.  A NaN logit (with MOE_SOFTMAX a logit of +inf too) in a valid row
- * leaves it without experts (ids -1) and makes its weights NaN.  An id of -1 is
+ * leaves it without experts (ids -1) and makes its weights NaN.  The type's
+ * lowest finite value is a logit like any other.  An id of -1 is
  * counted nowhere: expert_offsets[E] is then less than T * k and sorted_assign
  * behind it stays as it was.  T * top_k < 2^31; T = 0 writes the counts and
  * offsets alone.  Repeated calls give identical bits.  Two calls that overlap
